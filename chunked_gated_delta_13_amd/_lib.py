@@ -28,6 +28,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 # name -> (restype, argtypes); mirrors include/kda.h
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 _sz = ctypes.c_size_t
 SIGNATURES = {
     "kda_abi_version": (_i, []),
@@ -52,6 +53,9 @@ SIGNATURES = {
                              _i, _i, _i, _i, _i, _i, _vp]),
     "kda_spec_commit": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp,
                              _i, _i, _i, _i, _i, _i, _vp]),
+    "kda_conv_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _i, _i, _i, _i, _ll, _i, _i, _vp]),
+    "kda_conv_step": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _ll, _i, _i, _vp]),
 }
 
 _lib = None

@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/kda.h"
+#include "kda_host.h"
 #include "kda_internal.h"
 
 namespace kda {
@@ -25,6 +26,11 @@ hipError_t launch_prefill_bf16_gate(int dk, int dvw, int nw, int chunk, bool dua
 namespace {
 
 using kda::PrefillArgs;
+using kda::Range;
+using kda::aligned;
+using kda::mul_ok;
+using kda::overlap;
+using kda::range_of;
 
 // Shortest segment worth a split at T tokens.  Over n segments the two passes take about
 // 2.3 T / n chunk-times (5.3 us per 64-token chunk) and the scan n steps of about 13 us, least
@@ -36,24 +42,6 @@ long long min_segment(long long T) {
 }
 constexpr int kSliceWaves = 8;        // waves per workgroup for 128-column bf16 slices
 constexpr int kPipeChunkWaves = 8;    // chunk waves of the two-role prefill kernel
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void* p, size_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, lo + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-bool mul_ok(long long a, long long b, long long* out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > (1LL << 62) / a) return false;
-    *out = a * b;
-    return true;
-}
 
 // A second stream per device for work that overlaps the caller's stream (created once, default
 // priority, never destroyed), with the two events that fork it from and join it back to the

@@ -298,6 +298,53 @@ kda_status_t kda_chunk_prefill_noalloc(const void *q, const void *k, const void 
                                        int B, int T, int H, int dk, int dv, int chunk,
                                        kda_dtype_t dtype, int seg_len, int n_vs, void *stream);
 
+/*
+ * ---- Token mixers beside KDA: each keeps a state of fixed size per sequence ----
+ *
+ * The conventions above hold for them too, with these additions.  Inputs that a model cuts out of
+ * one projection's rows are taken where they lie: `*_stride` is the distance between the rows of
+ * consecutive tokens in elements (at least a row's width; sequence b's first row is row b * T), and
+ * the elements of one row are contiguous.  Outputs and states are contiguous.  No output may overlap
+ * the bytes spanned by an input, except where a state is said to be updated in place.  `lens`
+ * (DEVICE int32 [B], or NULL: every sequence has T tokens) holds the tokens of each sequence of a
+ * padded batch; values outside [0, T] are clamped on the device, the rows behind a sequence's end
+ * are not read for its results, and the output rows there are left as they were.  Values of live
+ * tokens must be finite: a NaN or an infinity may reach the other tokens of its block of 64.
+ */
+
+/*
+ * Short causal depthwise convolution of a prompt, in front of a mixer's inputs:
+ *
+ *     y[b, t, d] = act(bias[d] + sum_{j < W} w[d, j] x[b, t - (W - 1) + j, d])
+ *
+ * where inputs before the first token come from the history state_in.  Sums are fp32.
+ *
+ *   x          [B, T, D] dtype            row stride x_stride
+ *   w          [D, W]    dtype            taps, the last one on the current token
+ *   bias       [D]       dtype or NULL
+ *   state_in   [B, W - 1, D] dtype or NULL   the W - 1 inputs before the first token, oldest first
+ *                                            (NULL = zeros)
+ *   y          [B, T, D] dtype  (out)
+ *   state_out  [B, W - 1, D] dtype or NULL  (out)  the last W - 1 inputs of each sequence, for the
+ *                                            next call; may be exactly state_in
+ *   W          2, 3 or 4
+ *   silu       0: act is the identity, else x * sigmoid(x)
+ * T == 0 is valid: state_out receives state_in (or zeros).  B == 0 or D == 0 is a no-op.  Pointers
+ * need only the alignment of their elements; rows that all start on 16-byte boundaries run faster.
+ * B is at most 65535.
+ */
+kda_status_t kda_conv_prefill(const void *x, const void *w, const void *bias, const void *state_in,
+                              const int *lens, void *y, void *state_out, int B, int T, int D, int W,
+                              long long x_stride, int silu, kda_dtype_t dtype, void *stream);
+
+/*
+ * The same convolution for one new token of N sequences; the history is shifted in place.
+ *
+ *   x [N, D] (row stride x_stride), state [N, W - 1, D] in/out, y [N, D] (out); N at most 65535
+ */
+kda_status_t kda_conv_step(const void *x, const void *w, const void *bias, void *state, void *y, int N,
+                           int D, int W, long long x_stride, int silu, kda_dtype_t dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
