@@ -56,6 +56,11 @@ SIGNATURES = {
     "kda_conv_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp,
                               _i, _i, _i, _i, _ll, _i, _i, _vp]),
     "kda_conv_step": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _ll, _i, _i, _vp]),
+    "kda_ssm_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "kda_ssm_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                             _i, _i, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _ll, _i, _i, _vp, _sz, _vp]),
+    "kda_ssm_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                          _i, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _ll, _i, _vp]),
 }
 
 _lib = None

@@ -26,4 +26,34 @@ struct ConvArgs {
 hipError_t launch_conv_prefill(int W, bool f32, bool vec, const ConvArgs& a, hipStream_t s);
 hipError_t launch_conv_step(int W, bool f32, bool vec, const ConvArgs& a, hipStream_t s);
 
+struct SsmArgs {
+    const void* x;            // rows of H * p, stride x_stride elements
+    const void* dt;           // rows of H
+    const float* A;           // [H]
+    const void* Bm;           // rows of G * n
+    const void* Cm;           // rows of G * n
+    const float* D;           // [H] or nullptr
+    const void* z;            // rows of H * p or nullptr
+    const float* dt_bias;     // [H] or nullptr
+    const float* S0;          // [B, H, n, p] or nullptr (zeros)
+    const int* lens;          // [B] (device, clamped to [0, T]) or nullptr
+    void* y;                  // [rows, H, p]
+    float* S_T;               // [B, H, n, p] or nullptr; the token form reads and writes it
+    long long x_stride, dt_stride, b_stride, c_stride, z_stride;
+    long long T;
+    int H, G;
+    long long seg_len;        // tokens per segment (whole chunks)
+    int n_seg;                // segments of the sequence
+    int n_seg_launch;         // segments of this launch (the first ones)
+    long long n_units;        // sequences x heads x segments of this launch
+    long long per_xcd;
+    float* ws_state;          // [B * H, n_seg, n, p] entry states (slot 0 only with keep_S0)
+    float* ws_decay;          // [B * H, n_seg] exponents (base 2) of the decay over the segment before
+    int keep_S0;              // 1: the first pass copies S0 to slot 0, the second reads it there
+};
+
+enum class SsmPass { kStates, kOutputs, kToken };
+hipError_t launch_ssm(SsmPass pass, int n, int p, bool f32, const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_join(int n, int p, int bh, int n_seg, float* ws_state, const float* ws_decay, hipStream_t s);
+
 }  // namespace kda

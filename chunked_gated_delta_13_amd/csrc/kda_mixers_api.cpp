@@ -3,6 +3,8 @@
 // memory or synchronises the host with the device.
 #include <string.h>
 
+#include <atomic>
+
 #include <hip/hip_runtime.h>
 
 #include "../../include/kda.h"
@@ -57,6 +59,138 @@ bool conv_vec(const void* x, const void* bias, const void* s0, const void* s1, c
     const int v = dt == KDA_BF16 ? 8 : 4;
     return D % v == 0 && x_stride % v == 0 && aligned(x, 16) && aligned(bias, 16) && aligned(s0, 16) &&
            aligned(s1, 16) && aligned(y, 16);
+}
+
+constexpr int kSsmChunk = 64;
+
+// Compute units of the current device (256 where the runtime does not say).
+int cu_count() {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) {
+            (void)hipGetLastError();
+            n = 256;
+        }
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+kda_status_t check_ssm_shape(int rows_b, int T, int H, int G, int n, int p, kda_dtype_t dt) {
+    if (rows_b < 0 || T < 0 || H < 0 || G < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (dt != KDA_BF16 && dt != KDA_F32) return KDA_ERR_INVALID_ARGUMENT;
+    if (n <= 0 || p <= 0) return KDA_ERR_INVALID_ARGUMENT;
+    if ((n != 64 && n != 128) || (p != 64 && p != 128)) return KDA_ERR_UNSUPPORTED;
+    if (H > 0 && (G == 0 || H % G != 0)) return KDA_ERR_INVALID_ARGUMENT;
+    long long a = 0, b = 0;
+    if (!mul_ok((long long)rows_b * T, (long long)H * p, &a) || a >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!mul_ok((long long)rows_b * H, (long long)n * p, &b) || b >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)rows_b * H > (1LL << 24)) return KDA_ERR_UNSUPPORTED;   // units of a launch fit its grid
+    return KDA_OK;
+}
+
+// Segments of seg_in tokens (whole chunks), or chosen here (seg_in 0): enough of them that every
+// compute unit has two workgroups (one for fp32, whose tiles fill the LDS), each at least two chunks.
+kda_status_t ssm_plan(int B, int T, int H, kda_dtype_t dt, int seg_in, long long* seg_len, int* n_seg) {
+    if (seg_in < 0 || seg_in % kSsmChunk != 0) return KDA_ERR_INVALID_ARGUMENT;
+    const long long chunks = ((long long)T + kSsmChunk - 1) / kSsmChunk;
+    const long long units = (long long)B * H;
+    long long per = seg_in > 0 ? seg_in / kSsmChunk : chunks;
+    if (seg_in == 0 && units > 0) {
+        const long long want = (long long)cu_count() * (dt == KDA_F32 ? 1 : 2) / units;
+        if (want >= 2) per = (chunks + want - 1) / want;
+        if (per < 2) per = 2;
+    }
+    if (per < 1) per = 1;
+    const long long ns = chunks > 0 ? (chunks + per - 1) / per : 1;
+    if (units * ns > (1LL << 28)) return KDA_ERR_UNSUPPORTED;
+    *seg_len = per * kSsmChunk;
+    *n_seg = (int)ns;
+    return KDA_OK;
+}
+
+// Workspace of a split: the segments' entry states [B * H, n_seg, n, p], then decays [B * H, n_seg],
+// fp32, padded to 16 bytes.
+size_t ssm_workspace(int B, int H, int n, int p, int n_seg) {
+    if (n_seg <= 1) return 0;
+    const size_t slots = (size_t)B * H * (size_t)n_seg;
+    return slots * (size_t)n * p * sizeof(float) + (slots * sizeof(float) + 15) / 16 * 16;
+}
+
+// A strided row input that is read in 16-byte pieces.
+bool wide_rows_ok(const void* ptr, long long rows, long long width, long long stride, size_t esz) {
+    if (!stride_ok(rows, width, stride)) return false;
+    return aligned(ptr, 16) && (rows <= 1 || ((size_t)stride * esz) % 16 == 0);
+}
+
+struct SsmPtrs {
+    const void *x, *dt;
+    const float* A;
+    const void *Bm, *Cm;
+    const float* D;
+    const void* z;
+    const float* dt_bias;
+    const int* lens;
+    long long x_stride, dt_stride, b_stride, c_stride, z_stride;
+};
+
+// Pointer, stride and overlap checks shared by the prompt and the token form.  S_in is NULL where the
+// state is updated in place.
+kda_status_t check_ssm_ptrs(const SsmPtrs& q, const float* S_in, const void* y, const float* S_out, int rows_b, int T, int H,
+                            int G, int n, int p, kda_dtype_t dt) {
+    const size_t esz = elem_size(dt);
+    const long long rows = (long long)rows_b * T;
+    if (!q.A || (rows > 0 && (!q.x || !q.dt || !q.Bm || !q.Cm || !y))) return KDA_ERR_INVALID_ARGUMENT;
+    if (!wide_rows_ok(q.x, rows, (long long)H * p, q.x_stride, esz) ||
+        !wide_rows_ok(q.Bm, rows, (long long)G * n, q.b_stride, esz) ||
+        !wide_rows_ok(q.Cm, rows, (long long)G * n, q.c_stride, esz) ||
+        (q.z && !wide_rows_ok(q.z, rows, (long long)H * p, q.z_stride, esz)) || !stride_ok(rows, H, q.dt_stride))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned(q.dt, esz) || !aligned(q.A, 4) || !aligned(q.D, 4) || !aligned(q.dt_bias, 4) || !aligned(q.lens, 4) ||
+        !aligned(y, 16) || !aligned(S_in, 16) || !aligned(S_out, 16))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const size_t state = (size_t)rows_b * H * n * p * sizeof(float);
+    const Range ry = range_of(y, (size_t)rows * H * p * esz), rs = range_of(S_out, S_out ? state : 0);
+    const Range ri = range_of(S_in, S_in ? state : 0);
+    const Range ins[] = {rows_range(q.x, rows, (long long)H * p, q.x_stride, esz),
+                         rows_range(q.dt, rows, H, q.dt_stride, esz),
+                         rows_range(q.Bm, rows, (long long)G * n, q.b_stride, esz),
+                         rows_range(q.Cm, rows, (long long)G * n, q.c_stride, esz),
+                         rows_range(q.z, rows, (long long)H * p, q.z_stride, esz),
+                         range_of(q.A, (size_t)H * 4), range_of(q.D, q.D ? (size_t)H * 4 : 0),
+                         range_of(q.dt_bias, q.dt_bias ? (size_t)H * 4 : 0),
+                         range_of(q.lens, q.lens ? (size_t)rows_b * 4 : 0)};
+    for (const Range& r : ins)
+        if (overlap(ry, r) || overlap(rs, r)) return KDA_ERR_INVALID_ARGUMENT;
+    if (overlap(ry, ri) || overlap(ry, rs)) return KDA_ERR_INVALID_ARGUMENT;
+    if (S_in != S_out && overlap(rs, ri)) return KDA_ERR_INVALID_ARGUMENT;
+    return KDA_OK;
+}
+
+kda::SsmArgs ssm_args(const SsmPtrs& q) {
+    kda::SsmArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = q.x;
+    a.dt = q.dt;
+    a.A = q.A;
+    a.Bm = q.Bm;
+    a.Cm = q.Cm;
+    a.D = q.D;
+    a.z = q.z;
+    a.dt_bias = q.dt_bias;
+    a.lens = q.lens;
+    a.x_stride = q.x_stride;
+    a.dt_stride = q.dt_stride;
+    a.b_stride = q.b_stride;
+    a.c_stride = q.c_stride;
+    a.z_stride = q.z_stride;
+    return a;
 }
 
 }  // namespace
@@ -138,6 +272,96 @@ kda_status_t kda_conv_step(const void* x, const void* w, const void* bias, void*
     (void)hipGetLastError();
     if (kda::launch_conv_step(W, dt == KDA_F32, conv_vec(x, bias, state, state, y, D, x_stride, dt), a,
                               reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+        return KDA_ERR_DEVICE;
+    return KDA_OK;
+}
+
+size_t kda_ssm_prefill_workspace_bytes(int B, int T, int H, int G, int n, int p, kda_dtype_t dt, int seg_len) {
+    long long sl = 0;
+    int ns = 1;
+    if (check_ssm_shape(B, T, H, G, n, p, dt) != KDA_OK || ssm_plan(B, T, H, dt, seg_len, &sl, &ns) != KDA_OK) return 0;
+    return ssm_workspace(B, H, n, p, ns);
+}
+
+kda_status_t kda_ssm_prefill(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm, const float* D,
+                             const void* z, const float* dt_bias, const float* S0, const int* lens, void* y, float* S_T,
+                             int B, int T, int H, int G, int n, int p, long long x_stride, long long dt_stride,
+                             long long b_stride, long long c_stride, long long z_stride, kda_dtype_t dtype, int seg_len,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    kda_status_t st = check_ssm_shape(B, T, H, G, n, p, dtype);
+    if (st != KDA_OK) return st;
+    long long sl = 0;
+    int ns = 1;
+    st = ssm_plan(B, T, H, dtype, seg_len, &sl, &ns);
+    if (st != KDA_OK || B == 0 || H == 0) return st;
+    const SsmPtrs q = {x, dt, A, Bm, Cm, D, z, dt_bias, lens, x_stride, dt_stride, b_stride, c_stride, z_stride};
+    st = check_ssm_ptrs(q, S0, y, S_T, B, T, H, G, n, p, dtype);
+    if (st != KDA_OK) return st;
+    const size_t need = ssm_workspace(B, H, n, p, ns);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+        if (!aligned(workspace, 16)) return KDA_ERR_INVALID_ARGUMENT;
+        const size_t esz = elem_size(dtype);
+        const long long rows = (long long)B * T;
+        const size_t state = (size_t)B * H * n * p * sizeof(float);
+        const Range rw = range_of(workspace, need);
+        const Range others[] = {rows_range(x, rows, (long long)H * p, x_stride, esz), rows_range(dt, rows, H, dt_stride, esz),
+                                rows_range(Bm, rows, (long long)G * n, b_stride, esz),
+                                rows_range(Cm, rows, (long long)G * n, c_stride, esz),
+                                rows_range(z, rows, (long long)H * p, z_stride, esz), range_of(A, (size_t)H * 4),
+                                range_of(D, D ? (size_t)H * 4 : 0), range_of(dt_bias, dt_bias ? (size_t)H * 4 : 0),
+                                range_of(lens, lens ? (size_t)B * 4 : 0), range_of(y, (size_t)rows * H * p * esz),
+                                range_of(S0, S0 ? state : 0), range_of(S_T, S_T ? state : 0)};
+        for (const Range& r : others)
+            if (overlap(rw, r)) return KDA_ERR_INVALID_ARGUMENT;
+    }
+    if (T == 0 && !S_T) return KDA_OK;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const bool f32 = dtype == KDA_F32;
+    kda::SsmArgs a = ssm_args(q);
+    a.S0 = S0;
+    a.y = y;
+    a.S_T = S_T;
+    a.T = T;
+    a.H = H;
+    a.G = G;
+    a.seg_len = sl;
+    a.n_seg = ns;
+    (void)hipGetLastError();
+    if (ns > 1) {
+        a.ws_state = reinterpret_cast<float*>(workspace);
+        a.ws_decay = a.ws_state + (size_t)B * H * (size_t)ns * n * p;
+        a.keep_S0 = S_T && S_T == S0 ? 1 : 0;
+        a.n_seg_launch = ns - 1;
+        a.n_units = (long long)B * H * (ns - 1);
+        if (kda::launch_ssm(kda::SsmPass::kStates, n, p, f32, a, s) != hipSuccess) return KDA_ERR_DEVICE;
+        if (ns > 2 && kda::launch_ssm_join(n, p, B * H, ns, a.ws_state, a.ws_decay, s) != hipSuccess) return KDA_ERR_DEVICE;
+    }
+    a.n_seg_launch = ns;
+    a.n_units = (long long)B * H * ns;
+    if (kda::launch_ssm(kda::SsmPass::kOutputs, n, p, f32, a, s) != hipSuccess) return KDA_ERR_DEVICE;
+    return KDA_OK;
+}
+
+kda_status_t kda_ssm_step(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm, const float* D,
+                          const void* z, const float* dt_bias, float* S, void* y, int N, int H, int G, int n, int p,
+                          long long x_stride, long long dt_stride, long long b_stride, long long c_stride,
+                          long long z_stride, kda_dtype_t dtype, void* stream) {
+    kda_status_t st = check_ssm_shape(N, 1, H, G, n, p, dtype);
+    if (st != KDA_OK || N == 0 || H == 0) return st;
+    if (!S) return KDA_ERR_INVALID_ARGUMENT;
+    const SsmPtrs q = {x, dt, A, Bm, Cm, D, z, dt_bias, nullptr, x_stride, dt_stride, b_stride, c_stride, z_stride};
+    st = check_ssm_ptrs(q, nullptr, y, S, N, 1, H, G, n, p, dtype);
+    if (st != KDA_OK) return st;
+    kda::SsmArgs a = ssm_args(q);
+    a.y = y;
+    a.S_T = S;
+    a.T = 1;
+    a.H = H;
+    a.G = G;
+    a.n_units = (long long)N * H;
+    (void)hipGetLastError();
+    if (kda::launch_ssm(kda::SsmPass::kToken, n, p, dtype == KDA_F32, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
         return KDA_ERR_DEVICE;
     return KDA_OK;
 }

@@ -1,5 +1,4 @@
-"""Token mixers beside KDA: short causal convolution (further operators of this kind follow the
-same rules).
+"""Token mixers beside KDA: short causal convolution and selective state space scan.
 
 Argument marshalling only, like the rest of the binding.  Inputs may be slices of a projection's
 rows: tokens of one tensor lie a fixed stride apart and the elements of a token are contiguous.
@@ -65,14 +64,27 @@ def _device(t, where):
     return t.device
 
 
+class _Here:
+    """Stands for "this device is current already"."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(dev):
+    """A context in which `dev` is the current device."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
 def _call(fn, dev, *args):
-    """The library call on the current stream of the tensors' device, with that device current."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream)
+    """The library call on the current stream of the tensors' device (which is current)."""
+    st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _lib.check(st, fn.__name__)
 
@@ -110,8 +122,9 @@ def conv_prefill(x, w, bias=None, state=None, *, lens=None, silu=True, y=None, s
         _check("state_out", state_out, dt, keep, dev)
     elif return_state:
         state_out = torch.empty(keep, dtype=dt, device=dev)
-    _call(_lib.load().kda_conv_prefill, dev, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(lens), _ptr(y),
-          _ptr(state_out), B, T, D, W, x_stride, int(bool(silu)), code)
+    with _on(dev):
+        _call(_lib.load().kda_conv_prefill, dev, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(lens), _ptr(y),
+              _ptr(state_out), B, T, D, W, x_stride, int(bool(silu)), code)
     return y, state_out
 
 
@@ -134,6 +147,98 @@ def conv_step(x, w, state, bias=None, *, silu=True, y=None):
         y = torch.empty((N, D), dtype=dt, device=dev)
     else:
         _check("y", y, dt, (N, D), dev)
-    _call(_lib.load().kda_conv_step, dev, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y), N, D, W, x_stride,
-          int(bool(silu)), code)
+    with _on(dev):
+        _call(_lib.load().kda_conv_step, dev, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y), N, D, W, x_stride,
+              int(bool(silu)), code)
+    return y
+
+
+def _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, lead):
+    """Checks of the scan's inputs; returns the sizes and the row strides (x, dt, B, C, z)."""
+    dev, ty = x.device, x.dtype
+    rows = x.shape[:lead]
+    H, p = x.shape[lead:]
+    if Bm.dim() != lead + 2:
+        raise ValueError("Bm must have one axis of groups and one of state channels after the tokens")
+    G, n = Bm.shape[lead:]
+    xs = _rows("x", x, ty, x.shape, dev, lead)
+    ds = _rows("dt", dt, ty, (*rows, H), dev, lead)
+    bs = _rows("Bm", Bm, ty, (*rows, G, n), dev, lead)
+    cs = _rows("Cm", Cm, ty, (*rows, G, n), dev, lead)
+    zs = 0
+    if z is not None:
+        zs = _rows("z", z, ty, x.shape, dev, lead)
+    _check("A", A, torch.float32, (H,), dev)
+    if D is not None:
+        _check("D", D, torch.float32, (H,), dev)
+    if dt_bias is not None:
+        _check("dt_bias", dt_bias, torch.float32, (H,), dev)
+    return (H, G, n, p), (xs, ds, bs, cs, zs)
+
+
+def ssm_workspace_bytes(B, T, H, G, n, p, dtype=torch.bfloat16, seg_len=0):
+    """Device workspace bytes of ssm_prefill for this shape on the current device."""
+    return int(_lib.load().kda_ssm_prefill_workspace_bytes(B, T, H, G, n, p, _code(dtype), seg_len))
+
+
+def ssm_prefill(x, dt, A, Bm, Cm, S0=None, *, D=None, z=None, dt_bias=None, lens=None, seg_len=0, y=None,
+                S_T=None, return_state=True, workspace=None):
+    """Selective state space scan of a prompt batch.  Returns (y, S_T).
+
+    x, z [B, T, H, p]; dt [B, T, H] raw steps (softplus(dt + dt_bias) is applied); A, D, dt_bias [H]
+    fp32; Bm, Cm [B, T, G, n]; S0, S_T [B, H, n, p] fp32 (S_T may be S0; None when return_state is False).
+    x, dt, Bm, Cm and z may be slices of a projection's rows.  ``lens`` (int32 [B]) gives the tokens of
+    each sequence of a padded batch; rows of y behind them are left as they were.  ``seg_len`` forces the
+    tokens per segment of the sequence split (0 = the library's choice).
+    """
+    dev = _device(x, "ssm_prefill")
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, p]")
+    B, T = x.shape[:2]
+    ty = x.dtype
+    code = _code(ty)
+    (H, G, n, p), strides = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    state = (B, H, n, p)
+    if S0 is not None:
+        _check("S0", S0, torch.float32, state, dev)
+    if lens is not None:
+        _check("lens", lens, torch.int32, (B,), dev)
+    if y is None:
+        y = torch.empty((B, T, H, p), dtype=ty, device=dev)
+    else:
+        _check("y", y, ty, (B, T, H, p), dev)
+    if S_T is not None:
+        _check("S_T", S_T, torch.float32, state, dev)
+    elif return_state:
+        S_T = torch.empty(state, dtype=torch.float32, device=dev)
+    lib = _lib.load()
+    with _on(dev):
+        need = lib.kda_ssm_prefill_workspace_bytes(B, T, H, G, n, p, code, seg_len)
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _call(lib.kda_ssm_prefill, dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
+              _ptr(S0), _ptr(lens), _ptr(y), _ptr(S_T), B, T, H, G, n, p, *strides, code, seg_len, _ptr(workspace),
+              ws_bytes)
+    return y, S_T
+
+
+def ssm_step(x, dt, A, Bm, Cm, S, *, D=None, z=None, dt_bias=None, y=None):
+    """One token of the scan for N sequences: x, z [N, H, p], dt [N, H], Bm, Cm [N, G, n]; ``S``
+    [N, H, n, p] is updated in place.  Returns y [N, H, p]."""
+    dev = _device(x, "ssm_step")
+    if x.dim() != 3:
+        raise ValueError("x must be [N, H, p]")
+    N = x.shape[0]
+    ty = x.dtype
+    code = _code(ty)
+    (H, G, n, p), strides = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 1)
+    _check("S", S, torch.float32, (N, H, n, p), dev)
+    if y is None:
+        y = torch.empty((N, H, p), dtype=ty, device=dev)
+    else:
+        _check("y", y, ty, (N, H, p), dev)
+    with _on(dev):
+        _call(_lib.load().kda_ssm_step, dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
+              _ptr(dt_bias), _ptr(S), _ptr(y), N, H, G, n, p, *strides, code)
     return y

@@ -345,6 +345,53 @@ kda_status_t kda_conv_prefill(const void *x, const void *w, const void *bias, co
 kda_status_t kda_conv_step(const void *x, const void *w, const void *bias, void *state, void *y, int N,
                            int D, int W, long long x_stride, int silu, kda_dtype_t dtype, void *stream);
 
+/*
+ * Selective state space scan of a prompt: one decay per head and token, a state S (n x p, fp32) per
+ * sequence and head, input and output vectors B_t, C_t shared by the H / G heads of a group.
+ *
+ *     dt_t = softplus(dt[t] + dt_bias)
+ *     S   <- exp(dt_t A) S + dt_t B_t x_t^T
+ *     y_t  = (S^T C_t + D x_t) * silu(z_t)          read after the write
+ *
+ *   x          [B, T, H, p] dtype   row stride x_stride
+ *   dt         [B, T, H]    dtype   raw steps, row stride dt_stride (any alignment of its elements)
+ *   A          [H]          fp32    negative for a decaying state
+ *   Bm, Cm     [B, T, G, n] dtype   row strides b_stride, c_stride; G divides H
+ *   D          [H]          fp32 or NULL (no skip term)
+ *   z          [B, T, H, p] dtype or NULL (no gate), row stride z_stride
+ *   dt_bias    [H]          fp32 or NULL
+ *   S0         [B, H, n, p] fp32 or NULL (zeros)
+ *   y          [B, T, H, p] dtype  (out)
+ *   S_T        [B, H, n, p] fp32 or NULL  (out)  state after each sequence's last token; may be S0
+ *   n, p       64 or 128 each
+ *   seg_len    0: the library splits the sequence where that fills the GPU; else tokens per segment
+ *              (a multiple of 64; >= T = no split).  The result does not depend on it beyond rounding.
+ *   workspace  kda_ssm_prefill_workspace_bytes(...) bytes of device memory (may be NULL when that is 0),
+ *              written before it is read; calls that overlap in time need one each
+ * Rows of x, Bm, Cm and z start on 16-byte boundaries.  T == 0 is valid: S_T receives S0 (or zeros).
+ * B == 0 or H == 0 is a no-op.  States and exponents are fp32; with bf16 inputs the state is rounded to
+ * bf16 only as the operand of S^T C, never in its update.
+ */
+size_t kda_ssm_prefill_workspace_bytes(int B, int T, int H, int G, int n, int p, kda_dtype_t dtype,
+                                       int seg_len);
+kda_status_t kda_ssm_prefill(const void *x, const void *dt, const float *A, const void *Bm,
+                             const void *Cm, const float *D, const void *z, const float *dt_bias,
+                             const float *S0, const int *lens, void *y, float *S_T, int B, int T, int H,
+                             int G, int n, int p, long long x_stride, long long dt_stride,
+                             long long b_stride, long long c_stride, long long z_stride,
+                             kda_dtype_t dtype, int seg_len, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * One token of the scan for N sequences, S [N, H, n, p] updated in place: the same arguments without
+ * the time axis (x, z, y [N, H, p], dt [N, H], Bm, Cm [N, G, n]).
+ */
+kda_status_t kda_ssm_step(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                          const float *D, const void *z, const float *dt_bias, float *S, void *y, int N,
+                          int H, int G, int n, int p, long long x_stride, long long dt_stride,
+                          long long b_stride, long long c_stride, long long z_stride, kda_dtype_t dtype,
+                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -50,3 +50,33 @@ def conv(x, w, bias, state, lens, act):
             y[b, t], mag[b, t] = (silu(v) if act else v), sum(abs(u) for u in terms)
         kept[b] = line[ls[b]:]
     return y, mag, kept, ls
+
+
+def ssm(x, dt, A, Bm, Cm, S0=None, D=None, z=None, dt_bias=None, lens=None):
+    """(y, |terms| of y, S_T, |terms| of S_T, largest exponent of a 64-token chunk).  y rows behind a
+    sequence's end are NaN."""
+    x, dt, A, Bm, Cm, S0, D, z, dt_bias = (f64(t) for t in (x, dt, A, Bm, Cm, S0, D, z, dt_bias))
+    B, T, H, p = x.shape
+    G, n = Bm.shape[2:]
+    ls = lens_of(lens, B, T)
+    S = np.zeros((B, H, n, p)) if S0 is None else S0.copy()
+    M = np.abs(S)
+    y, mag = np.full(x.shape, np.nan), np.full(x.shape, np.nan)
+    cmax = 0.0
+    for b in range(B):
+        c = 0.0
+        for t in range(ls[b]):
+            d = softplus(dt[b, t] + (0 if dt_bias is None else dt_bias))
+            c = np.abs(d * A) + (0.0 if t % 64 == 0 else c)
+            cmax = max(cmax, float(c.max()))
+            k = np.repeat(Bm[b, t], H // G, 0)[:, :, None]
+            q = np.repeat(Cm[b, t], H // G, 0)[:, :, None]
+            e = np.exp(d * A)[:, None, None]
+            u = d[:, None, None] * k * x[b, t][:, None, :]
+            S[b] = e * S[b] + u
+            M[b] = e * M[b] + np.abs(u)
+            skip = 0 if D is None else D[:, None] * x[b, t]
+            gate = 1 if z is None else silu(z[b, t])
+            y[b, t] = ((S[b] * q).sum(1) + skip) * gate
+            mag[b, t] = ((M[b] * np.abs(q)).sum(1) + np.abs(skip)) * np.abs(gate)
+    return y, mag, S, M, cmax

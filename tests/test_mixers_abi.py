@@ -88,3 +88,75 @@ def test_conv_binding_refuses_what_it_cannot_run():
         kda.conv_prefill(x, w)
     with pytest.raises(ValueError, match="HIP device"):
         kda.conv_step(x[:, 0], w, torch.zeros(2, 3, 8))
+
+
+def _ssm(lib, B=2, T=200, H=4, G=2, n=128, p=64, dt=BF16, seg=0, ws=None, ws_bytes=0, strides=None, **ptr):
+    q = dict(x=_at(0), dt_=_at(1), A=_at(2), Bm=_at(3), Cm=_at(4), D=_at(5), z=_at(6), bias=_at(7), S0=_at(8), lens=_at(9),
+             y=_at(10), S_T=_at(11))
+    q.update(ptr)
+    st = strides or (H * p, H, G * n, G * n, H * p)
+    return lib.kda_ssm_prefill(*[_vp(v) for v in q.values()], B, T, H, G, n, p, *st, dt, seg, _vp(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(H=-1), INVALID), (dict(G=3), INVALID), (dict(G=0), INVALID),
+    (dict(dt=5), INVALID), (dict(n=0), INVALID), (dict(n=96), UNSUPPORTED), (dict(p=32), UNSUPPORTED),
+    (dict(seg=-64), INVALID), (dict(seg=100), INVALID),
+    (dict(B=1 << 20, H=1 << 10, G=1), UNSUPPORTED), (dict(B=1 << 30, T=1 << 30, H=1 << 20, G=1), INVALID),
+    (dict(x=None), INVALID), (dict(dt_=None), INVALID), (dict(A=None), INVALID), (dict(Bm=None), INVALID),
+    (dict(Cm=None), INVALID), (dict(y=None), INVALID),
+    (dict(x=_at(0) + 8), INVALID), (dict(Bm=_at(3) + 2), INVALID), (dict(z=_at(6) + 8), INVALID),
+    (dict(dt_=_at(1) + 1), INVALID), (dict(A=_at(2) + 2), INVALID), (dict(y=_at(10) + 8), INVALID),
+    (dict(S0=_at(8) + 4), INVALID), (dict(lens=_at(9) + 1), INVALID),
+    (dict(strides=(255, 4, 256, 256, 256)), INVALID),      # shorter than a row
+    (dict(strides=(260, 4, 256, 256, 256)), INVALID),      # rows off 16-byte boundaries
+    (dict(strides=(256, 3, 256, 256, 256)), INVALID),
+    (dict(strides=(256, 4, 256, 256, 0)), INVALID),
+    (dict(y=_at(0)), INVALID), (dict(y=_at(11)), INVALID), (dict(y=_at(8)), INVALID), (dict(S_T=_at(3)), INVALID),
+    (dict(S_T=_at(8) + 64), INVALID), (dict(S_T=_at(2)), INVALID),
+    (dict(seg=64), WORKSPACE), (dict(seg=64, ws=_at(12), ws_bytes=100), WORKSPACE),
+    (dict(seg=64, ws=_at(12) + 8, ws_bytes=1 << 30), INVALID), (dict(seg=64, ws=_at(0), ws_bytes=1 << 30), INVALID),
+    (dict(seg=64, ws=_at(11), ws_bytes=1 << 30), INVALID),
+])
+def test_ssm_prefill_refusals(lib, host_only, kw, expect):
+    assert _ssm(lib, **kw) == expect
+
+
+def test_ssm_workspace(lib):
+    need = lib.kda_ssm_prefill_workspace_bytes
+    assert need(2, 200, 4, 2, 128, 64, BF16, 64) == 8 * 4 * (128 * 64 * 4 + 4)   # 8 heads, 4 segments
+    assert need(2, 200, 4, 2, 128, 64, BF16, 256) == 0
+    assert need(2, 200, 4, 3, 128, 64, BF16, 64) == 0                             # a refused shape
+    assert need(2, 0, 4, 2, 128, 64, BF16, 64) == 0
+
+
+def test_ssm_noops(lib):
+    none = {k: None for k in ("x", "dt_", "A", "Bm", "Cm", "D", "z", "bias", "S0", "lens", "y", "S_T")}
+    assert _ssm(lib, B=0, **none) == OK
+    assert _ssm(lib, H=0, G=0, **none) == OK
+
+
+def _sstep(lib, N=2, H=4, G=2, n=128, p=64, dt=F32, strides=None, **ptr):
+    q = dict(x=_at(0), dt_=_at(1), A=_at(2), Bm=_at(3), Cm=_at(4), D=_at(5), z=_at(6), bias=_at(7), S=_at(8), y=_at(9))
+    q.update(ptr)
+    st = strides or (H * p, H, G * n, G * n, H * p)
+    return lib.kda_ssm_step(*[_vp(v) for v in q.values()], N, H, G, n, p, *st, dt, None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(N=-1), INVALID), (dict(G=3), INVALID), (dict(n=32), UNSUPPORTED), (dict(dt=2), INVALID),
+    (dict(S=None), INVALID), (dict(y=None), INVALID), (dict(x=None), INVALID), (dict(S=_at(8) + 4), INVALID),
+    (dict(y=_at(8)), INVALID), (dict(S=_at(0)), INVALID), (dict(strides=(256, 4, 255, 256, 256)), INVALID),
+    (dict(N=1 << 24), UNSUPPORTED),
+])
+def test_ssm_step_refusals(lib, host_only, kw, expect):
+    assert _sstep(lib, **kw) == expect
+
+
+def test_ssm_binding_refuses_what_it_cannot_run():
+    import torch
+    x, b = torch.zeros(2, 5, 2, 64), torch.zeros(2, 5, 1, 64)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.ssm_prefill(x, x[..., 0], torch.zeros(2), b, b)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.ssm_step(x[:, 0], x[:, 0, :, 0], torch.zeros(2), b[:, 0], b[:, 0], torch.zeros(2, 2, 64, 64))
