@@ -56,4 +56,26 @@ enum class SsmPass { kStates, kOutputs, kToken };
 hipError_t launch_ssm(SsmPass pass, int n, int p, bool f32, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_join(int n, int p, int bh, int n_seg, float* ws_state, const float* ws_decay, hipStream_t s);
 
+struct WindowArgs {
+    const void* q;            // rows of H * d, stride q_stride elements
+    const void* k;            // rows of Hkv * d
+    const void* v;
+    void* k_cache;            // [B, sinks + window, Hkv, d] or nullptr
+    void* v_cache;
+    const int* start;         // [B] tokens before the first new one (device) or nullptr (0)
+    const int* lens;          // [B] (device, clamped to [0, T]) or nullptr
+    void* o;                  // [rows, H, d]
+    long long q_stride, k_stride, v_stride;
+    int B, T, H, Hkv, window, sinks;
+    float scale;
+    int q_tiles;
+    int n_split, split_len;   // ranges of cache rows of the token form
+    long long n_units, per_xcd;
+    float* ws_o;              // [N * H, n_split, d] partial outputs of a split step
+    float* ws_ml;             // [N * H, n_split, 2] their maxima (base 2) and sums
+};
+
+hipError_t launch_window_prefill(int d, bool f32, const WindowArgs& a, hipStream_t s);
+hipError_t launch_window_step(int d, bool f32, const WindowArgs& a, hipStream_t s);
+
 }  // namespace kda

@@ -193,6 +193,70 @@ kda::SsmArgs ssm_args(const SsmPtrs& q) {
     return a;
 }
 
+kda_status_t check_window_shape(int rows_b, int T, int H, int Hkv, int d, int window, int sinks, kda_dtype_t dt) {
+    if (rows_b < 0 || T < 0 || H < 0 || Hkv < 0 || d <= 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (dt != KDA_BF16 && dt != KDA_F32) return KDA_ERR_INVALID_ARGUMENT;
+    if (window < 1 || sinks < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (d != 64 && d != 128) return KDA_ERR_UNSUPPORTED;
+    if (H > 0 && (Hkv == 0 || H % Hkv != 0)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)window + sinks > (1 << 29) || T > (1 << 29)) return KDA_ERR_UNSUPPORTED;   // 32-bit relative positions
+    if (rows_b > kMaxGridYZ || H > (1 << 16)) return KDA_ERR_UNSUPPORTED;
+    long long a = 0, b = 0;
+    if (!mul_ok((long long)rows_b * T, (long long)H * d, &a) || a >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!mul_ok((long long)rows_b * (window + sinks), (long long)Hkv * d, &b) || b >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)rows_b * H * (T / 64 + 1) > (1LL << 30)) return KDA_ERR_UNSUPPORTED;        // units of a launch
+    return KDA_OK;
+}
+
+// Pointer, stride and overlap checks shared by the prompt and the token form.
+kda_status_t check_window_ptrs(const void* q, const void* k, const void* v, const void* kc, const void* vc, const int* start,
+                               const int* lens, const void* o, const void* ws, size_t ws_bytes, int rows_b, int T, int H,
+                               int Hkv, int d, int window, int sinks, long long q_stride, long long k_stride,
+                               long long v_stride, kda_dtype_t dt) {
+    const size_t esz = elem_size(dt);
+    const long long rows = (long long)rows_b * T;
+    if (rows > 0 && (!q || !k || !v || !o)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((kc == nullptr) != (vc == nullptr)) return KDA_ERR_INVALID_ARGUMENT;
+    if (start && !kc) return KDA_ERR_INVALID_ARGUMENT;   // earlier tokens live in the cache only
+    if (!wide_rows_ok(q, rows, (long long)H * d, q_stride, esz) || !wide_rows_ok(k, rows, (long long)Hkv * d, k_stride, esz) ||
+        !wide_rows_ok(v, rows, (long long)Hkv * d, v_stride, esz))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(o, 16) || !aligned(start, 4) || !aligned(lens, 4) || !aligned(ws, 16))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const size_t cache = kc ? (size_t)rows_b * (window + sinks) * Hkv * d * esz : 0;
+    const Range outs[] = {range_of(o, (size_t)rows * H * d * esz), range_of(kc, cache), range_of(vc, cache),
+                          range_of(ws, ws ? ws_bytes : 0)};
+    const Range ins[] = {rows_range(q, rows, (long long)H * d, q_stride, esz),
+                         rows_range(k, rows, (long long)Hkv * d, k_stride, esz),
+                         rows_range(v, rows, (long long)Hkv * d, v_stride, esz),
+                         range_of(start, start ? (size_t)rows_b * 4 : 0), range_of(lens, lens ? (size_t)rows_b * 4 : 0)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : ins)
+            if (overlap(outs[i], r)) return KDA_ERR_INVALID_ARGUMENT;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j])) return KDA_ERR_INVALID_ARGUMENT;
+    }
+    return KDA_OK;
+}
+
+// Ranges of cache rows of a step: enough workgroups for two per compute unit, at least 256 rows each.
+void window_step_plan(int N, int H, int Hkv, int window, int sinks, int* n_split, int* split_len) {
+    const long long slots = (long long)window + sinks;
+    const long long units = (long long)N * Hkv * ((H / Hkv + 15) / 16);
+    long long want = units > 0 ? 2LL * cu_count() / units : 1;
+    if (want > slots / 256) want = slots / 256;
+    if (want < 1) want = 1;
+    const long long len = ((slots + want - 1) / want + 127) / 128 * 128;   // whole tiles of the four waves
+    *n_split = (int)((slots + len - 1) / len);
+    *split_len = (int)len;
+}
+
+size_t window_step_workspace(int N, int H, int d, int n_split) {
+    return n_split <= 1 ? 0 : (size_t)N * H * n_split * ((size_t)d + 4) * sizeof(float);
+}
+
+bool scale_ok(float scale) { return scale > 0.0f && scale <= 3.0e38f; }
+
 }  // namespace
 
 extern "C" {
@@ -362,6 +426,92 @@ kda_status_t kda_ssm_step(const void* x, const void* dt, const float* A, const v
     a.n_units = (long long)N * H;
     (void)hipGetLastError();
     if (kda::launch_ssm(kda::SsmPass::kToken, n, p, dtype == KDA_F32, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+        return KDA_ERR_DEVICE;
+    return KDA_OK;
+}
+
+kda_status_t kda_window_prefill(const void* q, const void* k, const void* v, void* k_cache, void* v_cache, const int* start,
+                                const int* lens, void* o, int B, int T, int H, int Hkv, int d, int window, int sinks,
+                                float scale, long long q_stride, long long k_stride, long long v_stride, kda_dtype_t dt,
+                                void* stream) {
+    kda_status_t st = check_window_shape(B, T, H, Hkv, d, window, sinks, dt);
+    if (st == KDA_OK && !scale_ok(scale)) st = KDA_ERR_INVALID_ARGUMENT;
+    if (st != KDA_OK || B == 0 || H == 0) return st;
+    st = check_window_ptrs(q, k, v, k_cache, v_cache, start, lens, o, nullptr, 0, B, T, H, Hkv, d, window, sinks, q_stride,
+                           k_stride, v_stride, dt);
+    if (st != KDA_OK || T == 0) return st;
+    kda::WindowArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.start = start;
+    a.lens = lens;
+    a.o = o;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.B = B;
+    a.T = T;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale;
+    (void)hipGetLastError();
+    if (kda::launch_window_prefill(d, dt == KDA_F32, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+        return KDA_ERR_DEVICE;
+    return KDA_OK;
+}
+
+size_t kda_window_step_workspace_bytes(int N, int H, int Hkv, int d, int window, int sinks, kda_dtype_t dt) {
+    if (check_window_shape(N, 1, H, Hkv, d, window, sinks, dt) != KDA_OK || N == 0 || H == 0) return 0;
+    int ns = 1, len = 0;
+    window_step_plan(N, H, Hkv, window, sinks, &ns, &len);
+    return window_step_workspace(N, H, d, ns);
+}
+
+kda_status_t kda_window_step(const void* q, const void* k, const void* v, void* k_cache, void* v_cache, const int* pos,
+                             void* o, int N, int H, int Hkv, int d, int window, int sinks, float scale,
+                             long long q_stride, long long k_stride, long long v_stride, kda_dtype_t dt, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    kda_status_t st = check_window_shape(N, 1, H, Hkv, d, window, sinks, dt);
+    if (st == KDA_OK && !scale_ok(scale)) st = KDA_ERR_INVALID_ARGUMENT;
+    if (st != KDA_OK || N == 0 || H == 0) return st;
+    if (!k_cache || !v_cache || !pos) return KDA_ERR_INVALID_ARGUMENT;
+    kda::WindowArgs a;
+    memset(&a, 0, sizeof(a));
+    window_step_plan(N, H, Hkv, window, sinks, &a.n_split, &a.split_len);
+    const size_t need = window_step_workspace(N, H, d, a.n_split);
+    st = check_window_ptrs(q, k, v, k_cache, v_cache, pos, nullptr, o, need ? workspace : nullptr, need, N, 1, H, Hkv, d,
+                           window, sinks, q_stride, k_stride, v_stride, dt);
+    if (st != KDA_OK) return st;
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+        a.ws_o = reinterpret_cast<float*>(workspace);
+        a.ws_ml = a.ws_o + (size_t)N * H * a.n_split * d;
+    }
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.start = pos;
+    a.o = o;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.B = N;
+    a.T = 1;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale;
+    (void)hipGetLastError();
+    if (kda::launch_window_step(d, dt == KDA_F32, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
         return KDA_ERR_DEVICE;
     return KDA_OK;
 }

@@ -1,0 +1,557 @@
+// Attention with a sliding window and a few first tokens that stay visible, for gfx950: prompts and
+// single tokens over a ring cache of fixed size.
+//
+// The query at position t sees key j <= t when t - j < window or j < sinks.  The cache of a sequence
+// holds sinks + window rows per kv head; token p lies in row p for p < sinks and in row
+// sinks + (p - sinks) mod window after that, so a row is overwritten just when it leaves the window.
+//
+// Both forms run one pass over the visible keys with the running maximum and sum of the softmax (fp32,
+// exponentials of base 2).  Scores are formed transposed, K Q^T with keys as rows: a lane then holds
+// four keys of one query, the statistics of a query stay in its lanes, and the probabilities are at
+// once the operand of V^T P^T, rounded to the input type for that product only.
+#include "kda_mixers.h"
+#include "kda_tile.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kKeys = 64;   // keys per tile of the prompt form
+
+// Row of the cache for position p.
+__device__ __forceinline__ long long ring_row(long long p, int sinks, int window) {
+    return p < sinks ? p : sinks + (p - sinks) % window;
+}
+
+__device__ __forceinline__ float max_over_groups(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum_over_groups(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// Eight slots of one row in global memory, p at slot 0 of the block (slots 4g.. and 16 + 4g..).
+__device__ __forceinline__ void global_frag(Frag<__bf16>& f, const __bf16* p) {
+    const bf16x4_t lo = *reinterpret_cast<const bf16x4_t*>(p);
+    const bf16x4_t hi = *reinterpret_cast<const bf16x4_t*>(p + 16);
+    f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ void global_frag(Frag<float>& f, const float* p) {
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(p);
+    const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(p + 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f.v[i] = lo[i];
+        f.v[4 + i] = hi[i];
+    }
+}
+// Eight consecutive elements of one row (slot order 8g .. 8g + 7; both operands use it).
+__device__ __forceinline__ void global_frag8(Frag<__bf16>& f, const __bf16* p) {
+    f.v = *reinterpret_cast<const bf16x8_t*>(p);
+}
+__device__ __forceinline__ void global_frag8(Frag<float>& f, const float* p) {
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(p);
+    const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f.v[i] = lo[i];
+        f.v[4 + i] = hi[i];
+    }
+}
+
+// LDS accesses of one wave run in program order; this keeps the compiler from reordering them.
+__device__ __forceinline__ void wave_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <typename T> __device__ __forceinline__ void store4(T* p, const f32x4_t& v) {
+    typedef __attribute__((ext_vector_type(4))) T vec4;
+    vec4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<vec4*>(p) = o;
+}
+
+}  // namespace
+
+// Prompt.  A workgroup of four waves runs 64 NQ queries of one (sequence, head); each wave holds
+// 16 NQ queries and their outputs in registers and takes the keys tile by tile from LDS.
+template <int D, typename T, int NQ>
+__global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArgs a) {
+    constexpr int BM = 64 * NQ;
+    constexpr int PER_ROW = D * (int)sizeof(T) / 16, EPP = 16 / (int)sizeof(T);
+    constexpr int NST = kKeys * PER_ROW / 256, ROWS = 256 / PER_ROW;
+    __shared__ __attribute__((aligned(16))) T sK_[kKeys * D], sV_[kKeys * D];
+    KDA_LDS T* sK = (KDA_LDS T*)sK_;
+    KDA_LDS T* sV = (KDA_LDS T*)sV_;
+
+    // unit = (b, kv head, query tile, head of the group): consecutive units share keys, and each XCD
+    // takes a contiguous range of them
+    long long unit = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
+    if (unit >= a.n_units) return;
+    const int R = a.H / a.Hkv;
+    const int hr = (int)(unit % R);
+    unit /= R;
+    const int q0 = (int)(unit % a.q_tiles) * BM;
+    unit /= a.q_tiles;
+    const int hk = (int)(unit % a.Hkv), b = (int)(unit / a.Hkv), h = hk * R + hr;
+
+    int len = a.T;
+    if (a.lens) {
+        const int l = a.lens[b];
+        len = l < 0 ? 0 : (l > a.T ? a.T : l);
+    }
+    if (q0 >= len) return;
+    int s = a.start ? a.start[b] : 0;
+    if (s < 0) s = 0;
+    const int window = a.window, sinks = a.sinks;
+
+    // Keys in relative positions (0 = the first new token): nsink first tokens, then lo .. hi
+    const int hi = (q0 + BM < len ? q0 + BM : len) - 1;
+    const int lo = sinks - s > q0 - window + 1 ? sinks - s : q0 - window + 1;
+    const int nsink = s >= sinks ? sinks : (sinks < hi + 1 + s ? sinks : hi + 1 + s);
+    const int total = nsink + (hi >= lo ? hi - lo + 1 : 0);
+    const int base0 = s > sinks ? (s - sinks) % window : 0;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, r = lane & 15;
+    TileLane<T, D> ld;
+    ld.set(lane);
+
+    const T* kn = reinterpret_cast<const T*>(a.k) + (long long)b * a.T * a.k_stride + (long long)hk * D;
+    const T* vn = reinterpret_cast<const T*>(a.v) + (long long)b * a.T * a.v_stride + (long long)hk * D;
+    const long long crow = (long long)a.Hkv * D;
+    const T* kc = reinterpret_cast<const T*>(a.k_cache);
+    const T* vc = reinterpret_cast<const T*>(a.v_cache);
+    if (kc) {
+        kc += (long long)b * (sinks + window) * crow + (long long)hk * D;
+        vc += (long long)b * (sinks + window) * crow + (long long)hk * D;
+    }
+
+    // queries of this wave
+    const int wq = q0 + wave * 16 * NQ;
+    Frag<T> fq[NQ][D / 32];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int i = wq + 16 * n + r;
+        const T* qp = reinterpret_cast<const T*>(a.q) + ((long long)b * a.T + i) * a.q_stride + (long long)h * D + 4 * g;
+#pragma unroll
+        for (int kb = 0; kb < D / 32; ++kb) {
+            if (i < len) global_frag(fq[n][kb], qp + 32 * kb);
+            else fq[n][kb].zero();
+        }
+    }
+
+    f32x4_t O[D / 16][NQ];
+    float m[NQ], l[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        m[n] = -INFINITY;
+        l[n] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) O[t][n] = zero4();
+    }
+
+    u32x4_t gk[NST], gv[NST];
+    const int pm = tid % PER_ROW, pr = tid / PER_ROW;
+    auto request = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < NST; ++i) {
+            const int idx = t0 + pr + i * ROWS;
+            gk[i] = gv[i] = u32x4_t{0, 0, 0, 0};
+            if (idx < total) {
+                const int rel = idx < nsink ? idx - s : lo + (idx - nsink);
+                const T *kp, *vp;
+                if (rel >= 0) {
+                    kp = kn + (long long)rel * a.k_stride;
+                    vp = vn + (long long)rel * a.v_stride;
+                } else {
+                    int row = idx;
+                    if (idx >= nsink) {
+                        row = base0 + rel;
+                        row = sinks + (row < 0 ? row + window : row);
+                    }
+                    kp = kc + row * crow;
+                    vp = vc + row * crow;
+                }
+                gk[i] = *reinterpret_cast<const u32x4_t*>(kp + pm * EPP);
+                gv[i] = *reinterpret_cast<const u32x4_t*>(vp + pm * EPP);
+            }
+        }
+    };
+    request(0);
+    const float sc = a.scale * kLog2e;
+
+    for (int t0 = 0; t0 < total; t0 += kKeys) {
+#pragma unroll
+        for (int i = 0; i < NST; ++i) {
+            const int row = pr + i * ROWS;
+            tile_put(sK + row * D, pm, row & 15, gk[i]);
+            tile_put(sV + row * D, pm, row & 15, gv[i]);
+        }
+        __syncthreads();
+        if (t0 + kKeys < total) request(t0 + kKeys);
+
+        // relative positions of the tile's window keys: first and last
+        const int w0 = lo + (t0 - nsink);
+        f32x4_t sT[4][NQ];
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) sT[kt][n] = zero4();
+#pragma unroll
+        for (int kb = 0; kb < D / 32; ++kb)
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                Frag<T> fk;
+                tile_row_frag<T, D>(fk, sK, ld, kt, kb);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) sT[kt][n] = mma(fk, fq[n][kb], sT[kt][n]);
+            }
+        const bool whole = t0 >= nsink && t0 + kKeys <= total && w0 + kKeys - 1 <= wq && wq + 16 * NQ - 1 - w0 < window;
+        if (!whole) {
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int idx = t0 + 16 * kt + 4 * g + j;
+                    const bool sink = idx < nsink;
+                    const int rel = sink ? idx - s : lo + (idx - nsink);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        const int i = wq + 16 * n + r;
+                        const bool see = idx < total && rel <= i && (sink || i - rel < window);
+                        sT[kt][n][j] = see ? sT[kt][n][j] : -INFINITY;
+                    }
+                }
+        }
+        Frag<T> fp[2][NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx = fmaxf(mx, sT[kt][n][j]);
+            mx = fmaxf(m[n], max_over_groups(mx) * sc);
+            const float base = mx == -INFINITY ? 0.0f : mx;   // nothing visible yet: all exponentials are 0
+            const float al = fast_exp2(m[n] - base);
+            m[n] = mx;
+            float sum = 0.0f;
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = fast_exp2(fmaf(sT[kt][n][j], sc, -base));
+                    sT[kt][n][j] = p;
+                    sum += p;
+                }
+            l[n] = l[n] * al + sum;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) O[t][n][j] *= al;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) acc_pair_frag<T>(fp[kb][n], sT[2 * kb][n], sT[2 * kb + 1][n], true);
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                Frag<T> fv;
+                tile_tr_frag<T, D>(fv, sV, ld, t, kb, lane);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) O[t][n] = mma(fv, fp[kb][n], O[t][n]);
+            }
+        __syncthreads();
+    }
+
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int i = wq + 16 * n + r;
+        const float inv = 1.0f / sum_over_groups(l[n]);
+        if (i < len) {
+            T* op = reinterpret_cast<T*>(a.o) + (((long long)b * a.T + i) * a.H + h) * D + 4 * g;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                f32x4_t v = O[t][n];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] *= inv;
+                store4<T>(op + 16 * t, v);
+            }
+        }
+    }
+}
+
+// The new tokens that stay in the cache: the first ones, and the last `window` ones.  It runs after
+// the attention, which reads the rows overwritten here.
+// grid: (pieces of the candidate rows / 256, sequences)
+template <typename T>
+__global__ __launch_bounds__(256) void kda_window_keep_kernel(const WindowArgs a, int D, int recent) {
+    const int b = blockIdx.y;
+    const int per_row = a.Hkv * D * (int)sizeof(T) / 16, epp = 16 / (int)sizeof(T);
+    const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long c = e / per_row;
+    const int m = (int)(e % per_row);
+    if (c >= a.sinks + recent) return;
+    int len = a.T;
+    if (a.lens) {
+        const int l = a.lens[b];
+        len = l < 0 ? 0 : (l > a.T ? a.T : l);
+    }
+    long long s = a.start ? a.start[b] : 0;
+    if (s < 0) s = 0;
+    const long long i = c < a.sinks ? c - s : len - recent + (c - a.sinks);
+    if (i < 0 || i >= len) return;
+    const long long p = s + i;
+    if (c >= a.sinks && p < a.sinks) return;   // a first token: written by its own candidate
+    const long long row = ring_row(p, a.sinks, a.window);
+    const long long width = (long long)a.Hkv * D;
+    const long long dst = ((long long)b * (a.sinks + a.window) + row) * width + m * epp;
+    const long long src = (long long)b * a.T + i;
+    *reinterpret_cast<u32x4_t*>(reinterpret_cast<T*>(a.k_cache) + dst) =
+        *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const T*>(a.k) + src * a.k_stride + m * epp);
+    *reinterpret_cast<u32x4_t*>(reinterpret_cast<T*>(a.v_cache) + dst) =
+        *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const T*>(a.v) + src * a.v_stride + m * epp);
+}
+
+// One token.  A workgroup of four waves runs up to 16 query heads of one (sequence, kv head) over one
+// range of cache rows; each wave takes every fourth tile of 32 rows with statistics of its own, and the
+// waves (then the ranges) are joined at the end.  Keys go from memory straight into the operand; values
+// pass through a tile of the wave's own in LDS to be transposed.
+template <int D, typename T>
+__global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a) {
+    constexpr int TK = 32;                                     // rows per tile
+    constexpr int PER_ROW = D * (int)sizeof(T) / 16, EPP = 16 / (int)sizeof(T);
+    constexpr int NST = TK * PER_ROW / 64, ROWS = 64 / PER_ROW;
+    constexpr int OP = D + 4;                                  // pitch of the partial outputs
+    constexpr int REGION = TK * D * (int)sizeof(T) > 16 * OP * 4 ? TK * D * (int)sizeof(T) : 16 * OP * 4;
+    __shared__ __attribute__((aligned(16))) char sV_[4][REGION];
+    __shared__ float sm[4][16], sl[4][16];
+
+    long long unit = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
+    if (unit >= a.n_units) return;
+    const int split = (int)(unit % a.n_split);
+    unit /= a.n_split;
+    const int R = a.H / a.Hkv, RT = (R + 15) / 16;
+    const int rt = (int)(unit % RT);
+    unit /= RT;
+    const int hk = (int)(unit % a.Hkv);
+    const long long b = unit / a.Hkv;
+    const int heads = R - 16 * rt < 16 ? R - 16 * rt : 16;
+    const int h0 = hk * R + 16 * rt;
+
+    long long pos = a.start[b];
+    if (pos < 0) pos = 0;
+    const int slots = a.sinks + a.window;
+    const int fresh = (int)ring_row(pos, a.sinks, a.window);   // the new token's row
+    const int filled = pos + 1 < slots ? (int)pos + 1 : slots;
+    const int k0 = split * a.split_len;
+    const int k1 = k0 + a.split_len < filled ? k0 + a.split_len : filled;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, r = lane & 15;
+    TileLane<T, D> ld;
+    ld.set(lane);
+    KDA_LDS T* sV = (KDA_LDS T*)(KDA_LDS char*)sV_[wave];
+
+    const T* kn = reinterpret_cast<const T*>(a.k) + b * a.k_stride + (long long)hk * D;
+    const T* vn = reinterpret_cast<const T*>(a.v) + b * a.v_stride + (long long)hk * D;
+    const long long crow = (long long)a.Hkv * D;
+    T* kc = reinterpret_cast<T*>(a.k_cache) + b * slots * crow + (long long)hk * D;
+    T* vc = reinterpret_cast<T*>(a.v_cache) + b * slots * crow + (long long)hk * D;
+    // The one workgroup whose range holds the new token's row writes it; nobody reads that row from the
+    // cache in this call.
+    if (rt == 0 && fresh >= k0 && fresh < k0 + a.split_len && tid < 2 * PER_ROW) {
+        const int m = tid % PER_ROW;
+        if (tid < PER_ROW) *reinterpret_cast<u32x4_t*>(kc + fresh * crow + m * EPP) = *reinterpret_cast<const u32x4_t*>(kn + m * EPP);
+        else *reinterpret_cast<u32x4_t*>(vc + fresh * crow + m * EPP) = *reinterpret_cast<const u32x4_t*>(vn + m * EPP);
+    }
+
+    Frag<T> fq[D / 32];
+    {
+        const T* qp = reinterpret_cast<const T*>(a.q) + b * a.q_stride + (long long)(h0 + r) * D + 8 * g;
+#pragma unroll
+        for (int kb = 0; kb < D / 32; ++kb) {
+            if (r < heads) global_frag8(fq[kb], qp + 32 * kb);
+            else fq[kb].zero();
+        }
+    }
+    f32x4_t O[D / 16];
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) O[t] = zero4();
+    float m = -INFINITY, l = 0.0f;
+    const float sc = a.scale * kLog2e;
+
+    for (int t0 = k0 + TK * wave; t0 < k1; t0 += 4 * TK) {
+        // rows past the filled ones stand for the new token and are masked: never read memory that no
+        // token has written
+        u32x4_t gv[NST];
+        const int pm = lane % PER_ROW, pr = lane / PER_ROW;
+#pragma unroll
+        for (int i = 0; i < NST; ++i) {
+            const int row = t0 + pr + i * ROWS;
+            const T* vp = row >= k1 || row == fresh ? vn : vc + row * crow;
+            gv[i] = *reinterpret_cast<const u32x4_t*>(vp + pm * EPP);
+        }
+        f32x4_t sT[2];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            const int row = t0 + 16 * kt + r;
+            const T* kp = (row >= k1 || row == fresh ? kn : kc + row * crow) + 8 * g;
+            Frag<T> fk[D / 32];
+#pragma unroll
+            for (int kb = 0; kb < D / 32; ++kb) global_frag8(fk[kb], kp + 32 * kb);
+            sT[kt] = zero4();
+#pragma unroll
+            for (int kb = 0; kb < D / 32; ++kb) sT[kt] = mma(fk[kb], fq[kb], sT[kt]);
+        }
+#pragma unroll
+        for (int i = 0; i < NST; ++i) {
+            const int row = pr + i * ROWS;
+            tile_put(sV + row * D, pm, row & 15, gv[i]);
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (t0 + 16 * kt + 4 * g + j >= k1) sT[kt][j] = -INFINITY;
+                mx = fmaxf(mx, sT[kt][j]);
+            }
+        mx = fmaxf(m, max_over_groups(mx) * sc);
+        const float al = fast_exp2(m - mx);   // the tile has a visible row: mx is a number
+        m = mx;
+        float sum = 0.0f;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sT[kt][j] = fast_exp2(fmaf(sT[kt][j], sc, -mx));
+                sum += sT[kt][j];
+            }
+        l = l * al + sum;
+        Frag<T> fp;
+        acc_pair_frag<T>(fp, sT[0], sT[1], true);
+        wave_order();
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+            Frag<T> fv;
+            tile_tr_frag<T, D>(fv, sV, ld, t, 0, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O[t][j] *= al;
+            O[t] = mma(fv, fp, O[t]);
+        }
+        wave_order();
+    }
+    l = sum_over_groups(l);
+
+    // join the waves: every wave's outputs go to its own region as [head][d]
+    KDA_LDS float* sO = (KDA_LDS float*)(KDA_LDS char*)sV_[wave];
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) *reinterpret_cast<KDA_LDS f32x4_t*>(sO + r * OP + 16 * t + 4 * g) = O[t];
+    if (g == 0) {
+        sm[wave][r] = m;
+        sl[wave][r] = l;
+    }
+    __syncthreads();
+    for (int e = tid; e < heads * (D / 4); e += 256) {
+        const int hh = e / (D / 4), d = (e % (D / 4)) * 4;
+        float M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w][hh]);
+        f32x4_t v = zero4();
+        const float base = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = fast_exp2(sm[w][hh] - base);
+            L = fmaf(f, sl[w][hh], L);
+            const f32x4_t x = *reinterpret_cast<const KDA_LDS f32x4_t*>((KDA_LDS float*)(KDA_LDS char*)sV_[w] + hh * OP + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = fmaf(f, x[j], v[j]);
+        }
+        const long long row = b * a.H + h0 + hh;
+        if (a.n_split == 1) {
+            const float inv = 1.0f / L;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] *= inv;
+            store4<T>(reinterpret_cast<T*>(a.o) + row * D + d, v);
+        } else {
+            *reinterpret_cast<f32x4_t*>(a.ws_o + (row * a.n_split + split) * D + d) = v;
+            if (d == 0) {
+                a.ws_ml[2 * (row * a.n_split + split)] = M;
+                a.ws_ml[2 * (row * a.n_split + split) + 1] = L;
+            }
+        }
+    }
+}
+
+// Joins the ranges of a split step.  grid: (sequence, head) rows; D / 4 threads
+template <int D, typename T>
+__global__ __launch_bounds__(64) void kda_window_join_kernel(const WindowArgs a) {
+    const long long row = blockIdx.x;
+    const int d = threadIdx.x * 4;
+    const float* ml = a.ws_ml + 2 * row * a.n_split;
+    const float* o = a.ws_o + row * a.n_split * D + d;
+    float M = -INFINITY;
+    for (int i = 0; i < a.n_split; ++i) M = fmaxf(M, ml[2 * i]);
+    float L = 0.0f;
+    f32x4_t v = zero4();
+    for (int i = 0; i < a.n_split; ++i) {
+        const float f = fast_exp2(ml[2 * i] - M);
+        L = fmaf(f, ml[2 * i + 1], L);
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(o + (long long)i * D);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(f, x[j], v[j]);
+    }
+    const float inv = 1.0f / L;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= inv;
+    store4<T>(reinterpret_cast<T*>(a.o) + row * D + d, v);
+}
+
+namespace {
+
+template <int D, typename T>
+hipError_t window_prefill_t(WindowArgs a, hipStream_t s) {
+    constexpr int NQ = sizeof(T) == 2 ? 2 : 1;   // fp32 operands take twice the registers
+    a.q_tiles = (a.T + 64 * NQ - 1) / (64 * NQ);
+    a.n_units = (long long)a.B * a.H * a.q_tiles;
+    a.per_xcd = (a.n_units + 7) / 8;
+    if (a.per_xcd > 0x0fffffff) return hipErrorInvalidValue;
+    kda_window_prefill_kernel<D, T, NQ><<<dim3((unsigned)(8 * a.per_xcd)), 256, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.k_cache) return e;
+    const int recent = a.window < a.T ? a.window : a.T;
+    const long long pieces = ((long long)a.sinks + recent) * (a.Hkv * D * (long long)sizeof(T) / 16);
+    kda_window_keep_kernel<T><<<dim3((unsigned)((pieces + 255) / 256), a.B), 256, 0, s>>>(a, D, recent);
+    return hipGetLastError();
+}
+
+template <int D, typename T>
+hipError_t window_step_t(WindowArgs a, hipStream_t s) {
+    a.n_units = (long long)a.B * a.Hkv * ((a.H / a.Hkv + 15) / 16) * a.n_split;
+    a.per_xcd = (a.n_units + 7) / 8;
+    if (a.per_xcd > 0x0fffffff) return hipErrorInvalidValue;
+    kda_window_step_kernel<D, T><<<dim3((unsigned)(8 * a.per_xcd)), 256, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.n_split == 1) return e;
+    kda_window_join_kernel<D, T><<<dim3((unsigned)((long long)a.B * a.H)), D / 4, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_window_prefill(int d, bool f32, const WindowArgs& a, hipStream_t s) {
+    if (d == 64) return f32 ? window_prefill_t<64, float>(a, s) : window_prefill_t<64, __bf16>(a, s);
+    return f32 ? window_prefill_t<128, float>(a, s) : window_prefill_t<128, __bf16>(a, s);
+}
+hipError_t launch_window_step(int d, bool f32, const WindowArgs& a, hipStream_t s) {
+    if (d == 64) return f32 ? window_step_t<64, float>(a, s) : window_step_t<64, __bf16>(a, s);
+    return f32 ? window_step_t<128, float>(a, s) : window_step_t<128, __bf16>(a, s);
+}
+
+}  // namespace kda

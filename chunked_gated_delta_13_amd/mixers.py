@@ -1,4 +1,5 @@
-"""Token mixers beside KDA: short causal convolution and selective state space scan.
+"""Token mixers beside KDA: short causal convolution, selective state space scan, and attention with a
+sliding window and a few first tokens that stay visible.
 
 Argument marshalling only, like the rest of the binding.  Inputs may be slices of a projection's
 rows: tokens of one tensor lie a fixed stride apart and the elements of a token are contiguous.
@@ -242,3 +243,85 @@ def ssm_step(x, dt, A, Bm, Cm, S, *, D=None, z=None, dt_bias=None, y=None):
         _call(_lib.load().kda_ssm_step, dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
               _ptr(dt_bias), _ptr(S), _ptr(y), N, H, G, n, p, *strides, code)
     return y
+
+
+def _window_inputs(q, k, v, lead):
+    dev, ty = q.device, q.dtype
+    rows = q.shape[:lead]
+    H, d = q.shape[lead:]
+    if k.dim() != lead + 2:
+        raise ValueError("k must have one axis of heads and one of channels after the tokens")
+    Hkv = k.shape[lead]
+    kv = (*rows, Hkv, d)
+    return (H, Hkv, d), (_rows("q", q, ty, q.shape, dev, lead), _rows("k", k, ty, kv, dev, lead),
+                         _rows("v", v, ty, kv, dev, lead))
+
+
+def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cache=None, start=None, lens=None,
+                   o=None):
+    """Attention of a prompt batch with a sliding window and ``sinks`` first tokens that stay visible: the
+    query at position t sees key j <= t where t - j < window or j < sinks.  Returns o [B, T, H, d].
+
+    q [B, T, H, d]; k, v [B, T, Hkv, d] with Hkv dividing H (all may be slices of a projection's rows).
+    ``k_cache`` / ``v_cache`` [B, sinks + window, Hkv, d] are the sequences' ring caches: earlier tokens
+    (``start`` [B] int32 of them, None = 0) are read from them and the new ones that stay visible are
+    written to them.  ``lens`` (int32 [B]) gives the new tokens of each sequence of a padded batch; rows
+    of o behind them are left as they were.  ``scale`` defaults to d ** -0.5.
+    """
+    dev = _device(q, "window_prefill")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, H, d]")
+    B, T = q.shape[:2]
+    ty = q.dtype
+    code = _code(ty)
+    (H, Hkv, d), strides = _window_inputs(q, k, v, 2)
+    if (k_cache is None) != (v_cache is None):
+        raise ValueError("k_cache and v_cache come together")
+    if k_cache is not None:
+        _check("k_cache", k_cache, ty, (B, sinks + window, Hkv, d), dev)
+        _check("v_cache", v_cache, ty, (B, sinks + window, Hkv, d), dev)
+    if start is not None:
+        _check("start", start, torch.int32, (B,), dev)
+    if lens is not None:
+        _check("lens", lens, torch.int32, (B,), dev)
+    if o is None:
+        o = torch.empty((B, T, H, d), dtype=ty, device=dev)
+    else:
+        _check("o", o, ty, (B, T, H, d), dev)
+    with _on(dev):
+        _call(_lib.load().kda_window_prefill, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(start),
+              _ptr(lens), _ptr(o), B, T, H, Hkv, d, window, sinks, d ** -0.5 if scale is None else scale, *strides, code)
+    return o
+
+
+def window_step_workspace_bytes(N, H, Hkv, d, window, sinks=0, dtype=torch.bfloat16):
+    """Device workspace bytes of window_step for this shape on the current device."""
+    return int(_lib.load().kda_window_step_workspace_bytes(N, H, Hkv, d, window, sinks, _code(dtype)))
+
+
+def window_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, o=None, workspace=None):
+    """The same attention for one new token of N sequences over their ring caches, which receive the
+    token's k and v: q [N, H, d], k, v [N, Hkv, d], ``pos`` (int32 [N]) the tokens before it.  Returns o."""
+    dev = _device(q, "window_step")
+    if q.dim() != 3:
+        raise ValueError("q must be [N, H, d]")
+    N = q.shape[0]
+    ty = q.dtype
+    code = _code(ty)
+    (H, Hkv, d), strides = _window_inputs(q, k, v, 1)
+    _check("k_cache", k_cache, ty, (N, sinks + window, Hkv, d), dev)
+    _check("v_cache", v_cache, ty, (N, sinks + window, Hkv, d), dev)
+    _check("pos", pos, torch.int32, (N,), dev)
+    if o is None:
+        o = torch.empty((N, H, d), dtype=ty, device=dev)
+    else:
+        _check("o", o, ty, (N, H, d), dev)
+    lib = _lib.load()
+    with _on(dev):
+        need = lib.kda_window_step_workspace_bytes(N, H, Hkv, d, window, sinks, code)
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _call(lib.kda_window_step, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(o), N, H,
+              Hkv, d, window, sinks, d ** -0.5 if scale is None else scale, *strides, code, _ptr(workspace), ws_bytes)
+    return o

@@ -392,6 +392,48 @@ kda_status_t kda_ssm_step(const void *x, const void *dt, const float *A, const v
                           long long b_stride, long long c_stride, long long z_stride, kda_dtype_t dtype,
                           void *stream);
 
+/*
+ * Attention of a prompt with a sliding window and a few first tokens that stay visible: the query at
+ * position t sees key j <= t where t - j < window or j < sinks, H / Hkv query heads share a kv head,
+ *
+ *     o_t = sum_j softmax_j(scale q_t . k_j) v_j        over the visible j
+ *
+ * Earlier tokens of a sequence are read from its ring cache, and the new ones that stay visible are
+ * written to it, so that a prompt can be run in pieces and be continued by kda_window_step.  Positions
+ * are counted from a sequence's first token; rotary or other encodings are the caller's.
+ *
+ *   q          [B, T, H, d]    dtype   row stride q_stride
+ *   k, v       [B, T, Hkv, d]  dtype   row strides k_stride, v_stride; Hkv divides H
+ *   k_cache, v_cache  [B, sinks + window, Hkv, d] dtype, in/out, or both NULL (no earlier tokens, none
+ *                     kept): token p lies in row p for p < sinks, else in row
+ *                     sinks + (p - sinks) mod window.  Rows no token has reached are never read.
+ *   start      [B] int32 DEVICE or NULL (0)   tokens of each sequence before this call (needs the caches)
+ *   o          [B, T, H, d]    dtype  (out)
+ *   d          64 or 128;  window >= 1;  sinks >= 0;  scale > 0
+ * Rows of q, k and v start on 16-byte boundaries.  T == 0, B == 0 or H == 0 is a no-op.  B is at most
+ * 65535.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded to bf16 as the
+ * operand of the product with v.
+ */
+kda_status_t kda_window_prefill(const void *q, const void *k, const void *v, void *k_cache,
+                                void *v_cache, const int *start, const int *lens, void *o, int B, int T,
+                                int H, int Hkv, int d, int window, int sinks, float scale,
+                                long long q_stride, long long k_stride, long long v_stride,
+                                kda_dtype_t dtype, void *stream);
+
+/*
+ * One new token of N sequences over their ring caches: q [N, H, d], k, v [N, Hkv, d], o [N, H, d].
+ * pos [N] int32 (DEVICE): tokens of each sequence before this one.  The token's k and v are written to
+ * their row of the caches and are visible to its own query.  The workspace holds
+ * kda_window_step_workspace_bytes(...) bytes (may be NULL when that is 0); calls that overlap in time
+ * need one each.
+ */
+size_t kda_window_step_workspace_bytes(int N, int H, int Hkv, int d, int window, int sinks,
+                                       kda_dtype_t dtype);
+kda_status_t kda_window_step(const void *q, const void *k, const void *v, void *k_cache, void *v_cache,
+                             const int *pos, void *o, int N, int H, int Hkv, int d, int window, int sinks,
+                             float scale, long long q_stride, long long k_stride, long long v_stride,
+                             kda_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -80,3 +80,40 @@ def ssm(x, dt, A, Bm, Cm, S0=None, D=None, z=None, dt_bias=None, lens=None):
             y[b, t] = ((S[b] * q).sum(1) + skip) * gate
             mag[b, t] = ((M[b] * np.abs(q)).sum(1) + np.abs(skip)) * np.abs(gate)
     return y, mag, S, M, cmax
+
+
+def ring_row(p, sinks, window):
+    return p if p < sinks else sinks + (p - sinks) % window
+
+
+def window(q, k, v, win, sinks, scale, k_cache=None, v_cache=None, start=None, lens=None):
+    """(o, |terms|, largest scale * sum |q k| per query, k_cache, v_cache): o rows behind a sequence's end
+    are NaN; the caches are copies with the new tokens written."""
+    q, k, v, kc, vc = (f64(t) for t in (q, k, v, k_cache, v_cache))
+    B, T, H, d = q.shape
+    Hkv = k.shape[2]
+    ls = lens_of(lens, B, T)
+    st = [0] * B if start is None else [int(n) for n in start.tolist()]
+    o, mag, a = np.full(q.shape, np.nan), np.full(q.shape, np.nan), np.zeros((B, T, H))
+    kc2, vc2 = (None if c is None else c.copy() for c in (kc, vc))
+    for b in range(B):
+        s = st[b]
+        for i in range(ls[b]):
+            t = s + i
+            see = sorted(set(range(min(sinks, t + 1))) | set(range(max(0, t - win + 1), t + 1)))
+            at = [(None, j - s) if j >= s else (ring_row(j, sinks, win), None) for j in see]
+            kk = np.stack([k[b, n] if n is not None else kc[b, c] for c, n in at])     # [keys, Hkv, d]
+            vv = np.stack([v[b, n] if n is not None else vc[b, c] for c, n in at])
+            for h in range(H):
+                g = h // (H // Hkv)
+                w = scale * (kk[:, g] @ q[b, i, h])
+                a[b, i, h] = scale * (np.abs(kk[:, g]) @ np.abs(q[b, i, h])).max()
+                p = np.exp(w - w.max())
+                p /= p.sum()
+                o[b, i, h] = p @ vv[:, g]
+                mag[b, i, h] = p @ np.abs(vv[:, g])
+        if kc is not None:
+            for i in range(ls[b]):
+                row = ring_row(s + i, sinks, win)
+                kc2[b, row], vc2[b, row] = k[b, i], v[b, i]
+    return o, mag, a, kc2, vc2

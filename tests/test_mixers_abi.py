@@ -160,3 +160,73 @@ def test_ssm_binding_refuses_what_it_cannot_run():
         kda.ssm_prefill(x, x[..., 0], torch.zeros(2), b, b)
     with pytest.raises(ValueError, match="HIP device"):
         kda.ssm_step(x[:, 0], x[:, 0, :, 0], torch.zeros(2), b[:, 0], b[:, 0], torch.zeros(2, 2, 64, 64))
+
+
+def _window(lib, B=2, T=50, H=4, Hkv=2, d=64, window=20, sinks=4, scale=0.125, dt=BF16, strides=None, **ptr):
+    q = dict(q=_at(0), k=_at(1), v=_at(2), kc=_at(3), vc=_at(4), start=_at(5), lens=_at(6), o=_at(7))
+    q.update(ptr)
+    st = strides or (H * d, Hkv * d, Hkv * d)
+    return lib.kda_window_prefill(*[_vp(x) for x in q.values()], B, T, H, Hkv, d, window, sinks, scale, *st, dt, None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(Hkv=3), INVALID), (dict(Hkv=0), INVALID), (dict(window=0), INVALID),
+    (dict(sinks=-1), INVALID), (dict(dt=3), INVALID), (dict(d=0), INVALID), (dict(d=96), UNSUPPORTED),
+    (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(B=65536), UNSUPPORTED), (dict(window=1 << 29), UNSUPPORTED),
+    (dict(B=65535, T=1 << 29, H=4), UNSUPPORTED),
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID),
+    (dict(kc=None), INVALID), (dict(vc=None), INVALID), (dict(kc=None, vc=None), INVALID),     # start without caches
+    (dict(q=_at(0) + 8), INVALID), (dict(v=_at(2) + 2), INVALID), (dict(o=_at(7) + 4), INVALID),
+    (dict(kc=_at(3) + 8), INVALID), (dict(start=_at(5) + 2), INVALID), (dict(lens=_at(6) + 1), INVALID),
+    (dict(strides=(255, 128, 128)), INVALID), (dict(strides=(260, 128, 128)), INVALID), (dict(strides=(256, 127, 128)), INVALID),
+    (dict(o=_at(0)), INVALID), (dict(o=_at(3)), INVALID), (dict(vc=_at(3)), INVALID), (dict(kc=_at(1)), INVALID),
+    (dict(vc=_at(5)), INVALID),
+])
+def test_window_prefill_refusals(lib, host_only, kw, expect):
+    assert _window(lib, **kw) == expect
+
+
+def test_window_noops(lib):
+    none = {x: None for x in ("q", "k", "v", "kc", "vc", "start", "lens", "o")}
+    assert _window(lib, B=0, **none) == OK
+    assert _window(lib, H=0, Hkv=0, **none) == OK
+    assert _window(lib, T=0, **none) == OK
+
+
+def _wstep(lib, N=2, H=4, Hkv=2, d=64, window=20, sinks=4, scale=0.125, dt=F32, strides=None, ws=None, ws_bytes=0, **ptr):
+    q = dict(q=_at(0), k=_at(1), v=_at(2), kc=_at(3), vc=_at(4), pos=_at(5), o=_at(6))
+    q.update(ptr)
+    st = strides or (H * d, Hkv * d, Hkv * d)
+    return lib.kda_window_step(*[_vp(x) for x in q.values()], N, H, Hkv, d, window, sinks, scale, *st, dt, _vp(ws), ws_bytes,
+                               None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(N=-1), INVALID), (dict(Hkv=3), INVALID), (dict(window=0), INVALID), (dict(d=32), UNSUPPORTED), (dict(dt=3), INVALID),
+    (dict(scale=0.0), INVALID), (dict(kc=None), INVALID), (dict(vc=None), INVALID), (dict(pos=None), INVALID),
+    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(o=_at(0)), INVALID), (dict(o=_at(4)), INVALID),
+    (dict(vc=_at(3) + 16), INVALID), (dict(pos=_at(5) + 2), INVALID), (dict(strides=(255, 128, 128)), INVALID),
+    (dict(window=5000), WORKSPACE), (dict(window=5000, ws=_at(7), ws_bytes=64), WORKSPACE),
+    (dict(window=5000, ws=_at(7) + 4, ws_bytes=1 << 30), INVALID), (dict(window=5000, ws=_at(3), ws_bytes=1 << 30), INVALID),
+])
+def test_window_step_refusals(lib, host_only, kw, expect):
+    assert _wstep(lib, **kw) == expect
+
+
+def test_window_step_noop_and_workspace(lib):
+    assert _wstep(lib, N=0, q=None, k=None, v=None, kc=None, vc=None, pos=None, o=None) == OK
+    need = lib.kda_window_step_workspace_bytes
+    assert need(1, 8, 2, 128, 100, 4, BF16) == 0 and need(0, 8, 2, 128, 5000, 4, BF16) == 0
+    assert need(1, 8, 3, 128, 5000, 4, BF16) == 0
+    per = 8 * (128 + 4) * 4
+    assert need(1, 8, 2, 128, 5000, 4, BF16) % per == 0 and need(1, 8, 2, 128, 5000, 4, BF16) >= 2 * per
+
+
+def test_window_binding_refuses_what_it_cannot_run():
+    import torch
+    q = torch.zeros(2, 5, 2, 64)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.window_prefill(q, q, q, 4)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.window_step(q[:, 0], q[:, 0], q[:, 0], q, q, torch.zeros(2, dtype=torch.int32), 4)
