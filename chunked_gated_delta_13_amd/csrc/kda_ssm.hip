@@ -32,74 +32,121 @@ constexpr float kDecayMin = -160;  // exponents of 2 at or below this give zero
 __device__ __forceinline__ float softplus_f32(float v) { return fmaxf(v, 0.0f) + log1pf(__expf(-fabsf(v))); }
 __device__ __forceinline__ float silu_f32(float x) { return x * __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
-// Running sum over the 64 lanes of a wave.
-__device__ __forceinline__ float wave_prefix(float v, int lane) {
+// Running sum over the 64 lanes of a wave.  In 64 bits: decays of neighbouring tokens are differences of
+// these sums, which may be large.
+__device__ __forceinline__ double wave_prefix(double v, int lane) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const float u = __shfl_up(v, o);
+        const double u = __shfl_up(v, o);
         if (lane >= o) v += u;
     }
     return v;
 }
 
-// v as a sum of NPART operands (bf16: three parts of 8 bits each; fp32: itself).
-__device__ __forceinline__ void split_parts(Frag<__bf16> (&f)[3], int j, float v) {
-    const __bf16 a = (__bf16)v;
-    const float r1 = v - (float)a;
-    const __bf16 b = (__bf16)r1;
-    f[0].v[j] = a;
-    f[1].v[j] = b;
-    f[2].v[j] = (__bf16)(r1 - (float)b);
+// x times w (per contraction slot) as a sum of operands.  bf16: the fp32 product is cut into three parts
+// of 8 bits, high halves of its bit pattern and of what is left, which loses nothing but the last bit.
+__device__ __forceinline__ void weigh(Frag<__bf16> (&f)[3], const Frag<__bf16>& x, const float (&w)[8]) {
+    union { bf16x8_t v; uint32_t u[4]; } in, out[3];
+    in.v = x.v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = __uint_as_float(in.u[j] << 16) * w[2 * j], b = __uint_as_float(in.u[j] & 0xffff0000u) * w[2 * j + 1];
+        const uint32_t a0 = __float_as_uint(a), b0 = __float_as_uint(b);
+        const float a1 = a - __uint_as_float(a0 & 0xffff0000u), b1 = b - __uint_as_float(b0 & 0xffff0000u);
+        const uint32_t a1u = __float_as_uint(a1), b1u = __float_as_uint(b1);
+        const float a2 = a1 - __uint_as_float(a1u & 0xffff0000u), b2 = b1 - __uint_as_float(b1u & 0xffff0000u);
+        out[0].u[j] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+        out[1].u[j] = __builtin_amdgcn_perm(b1u, a1u, 0x07060302u);
+        out[2].u[j] = __builtin_amdgcn_perm(__float_as_uint(b2), __float_as_uint(a2), 0x07060302u);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) f[i].v = out[i].v;
 }
-__device__ __forceinline__ void split_parts(Frag<float> (&f)[1], int j, float v) { f[0].v[j] = v; }
+__device__ __forceinline__ void weigh(Frag<float> (&f)[1], const Frag<float>& x, const float (&w)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[0].v[j] = x.v[j] * w[j];
+}
 
 template <typename T> struct Parts { static constexpr int n = 3; };
 template <> struct Parts<float> { static constexpr int n = 1; };
 
 // A wave's share of 64 rows of WIDTH elements: requested one chunk ahead into registers, put into the
-// tile when the last chunk's readers are done.
-template <typename T, int WIDTH> struct Stage {
-    static constexpr int PER_ROW = WIDTH * (int)sizeof(T) / 16;
-    static constexpr int N = kC * PER_ROW / 256;
-    static constexpr int ROWS = 256 / PER_ROW;   // rows per step
-    u32x4_t v[N];
-    __device__ __forceinline__ void load(const T* base, long long stride, int rows, int tid) {
-        const int m = tid % PER_ROW, r0 = tid / PER_ROW;
+// tile when the last chunk's readers are done.  Rows past a partial chunk's last one lie past the
+// buffer's end and come as zeros.
+template <typename T, int WIDTH, int NW> struct Stage {
+    typedef TileSteps<T, kC, WIDTH, NW> Steps;
+    static constexpr uint32_t ES = sizeof(T);
+    u32x4_t v[Steps::N];
+    __device__ __forceinline__ void load(const T* base, uint32_t step, int rows, int wave, int lane) {
+        const buffer_t buf = make_buffer(base, (uint32_t)(rows - 1) * step + WIDTH * ES);
+        const uint32_t off = TileStep<T>::row(lane) * step + 16u * TileStep<T>::piece(lane);
+        const uint32_t first = Steps::group0(wave) * TileStep<T>::ROWS * step + Steps::block0(wave) * 32 * ES;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = r0 + i * ROWS;
-            v[i] = u32x4_t{0, 0, 0, 0};
-            if (r < rows) v[i] = *reinterpret_cast<const u32x4_t*>(base + r * stride + m * (16 / (int)sizeof(T)));
-        }
+        for (int i = 0; i < Steps::N; ++i)
+            v[i] = buffer_load16(buf, off, first + Steps::group(i) * TileStep<T>::ROWS * step + Steps::block(i) * 32 * ES);
     }
-    __device__ __forceinline__ void put(KDA_LDS T* tile, int tid) const {
-        const int m = tid % PER_ROW, r0 = tid / PER_ROW;
+    __device__ __forceinline__ void put(KDA_LDS T* tile, int wave, int lane) const {
+        TilePut<T, kC> p;
+        p.set(tile + (Steps::block0(wave) * kC + Steps::group0(wave) * TileStep<T>::ROWS) * 32, lane);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = r0 + i * ROWS;
-            tile_put(tile + r * WIDTH, m, r & 15, v[i]);
-        }
+        for (int i = 0; i < Steps::N; ++i) p.put((Steps::block(i) * kC + Steps::group(i) * TileStep<T>::ROWS) * 32, v[i]);
     }
 };
+
+// The weights of token tiles kb and kb + 2 at this lane's slots.
+__device__ __forceinline__ void load_weights(float (&w)[8], const KDA_LDS float* p) {
+    const f32x4_t lo = *reinterpret_cast<const KDA_LDS f32x4_t*>(p);
+    const f32x4_t hi = *reinterpret_cast<const KDA_LDS f32x4_t*>(p + 32);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = lo[i];
+        w[4 + i] = hi[i];
+    }
+}
+
+// A uniform value that the compiler may not carry over from an earlier use.
+__device__ __forceinline__ int pinned_s(int x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
+// Per-token numbers of one chunk: sums of the exponents (base 2, high and low part), steps, and the
+// weights of the state's update; `last` is the sum over the whole chunk.
+struct ChunkDecay {
+    float hi[kC], lo[kC], dt[kC], w[kC];
+};
+
+__device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bool live, float A2, int lane) {
+    const float d = live ? softplus_f32(raw) : 0.0f;
+    const double s = wave_prefix(live ? (double)fmaxf(d * A2, kDecayMin) : 0.0, lane);
+    const double end = __shfl(s, 63);
+    const float hi = (float)s;
+    c->hi[lane] = hi;
+    c->lo[lane] = (float)(s - (double)hi);
+    c->dt[lane] = d;
+    c->w[lane] = fast_exp2((float)(end - s)) * d;
+}
 
 }  // namespace
 
 // OUT: with outputs (the pass that runs every segment from its entry state), else final states only.
-template <int N, int P, typename T, bool OUT>
-__global__ __launch_bounds__(256) void kda_ssm_prefill_kernel(const SsmArgs a) {
-    constexpr int WC = P / 4;        // state columns per wave
+template <int N, int P, typename T, bool OUT, int NW>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefill_kernel(const SsmArgs a) {
+    constexpr int NTH = 64 * NW;
+    constexpr int WC = P / NW;       // state columns per wave
     constexpr int NCT = WC / 16;     // column tiles per wave
     constexpr int NT = N / 16;       // row tiles of the state
     constexpr int NP = Parts<T>::n;
-    __shared__ __attribute__((aligned(16))) T sX_[kC * P], sB_[kC * N], sC_[OUT ? kC * N : 16], sM_[OUT ? kC * kC : 16];
-    __shared__ __attribute__((aligned(16))) float sCum_[kC], sDt_[kC], sW_[kC];
-    KDA_LDS T* sX = (KDA_LDS T*)sX_;
-    KDA_LDS T* sB = (KDA_LDS T*)sB_;
-    KDA_LDS T* sC = (KDA_LDS T*)sC_;
-    KDA_LDS T* sM = (KDA_LDS T*)sM_;
-    KDA_LDS float* sCum = (KDA_LDS float*)sCum_;
-    KDA_LDS float* sDt = (KDA_LDS float*)sDt_;
-    KDA_LDS float* sW = (KDA_LDS float*)sW_;
+    typedef __attribute__((ext_vector_type(4))) T vec4;
+    // LDS: B, C, M, x tiles (elements), then the decays of two chunks
+    constexpr int oC = kC * N, oM = OUT ? 2 * kC * N : kC * N, oX = oM + (OUT ? kC * kC : 0), oEnd = oX + kC * P;
+    __shared__ __attribute__((aligned(16))) T smem[oEnd];
+    __shared__ __attribute__((aligned(16))) ChunkDecay sD_[2];
+    KDA_LDS T* sB = (KDA_LDS T*)smem;
+    KDA_LDS T* sC = sB + oC;
+    KDA_LDS T* sM = sB + oM;
+    KDA_LDS T* sX = sB + oX;
+    KDA_LDS ChunkDecay* sD = (KDA_LDS ChunkDecay*)sD_;
 
     // unit = (b, segment, h), heads fastest: the heads of a segment share B and C, and each XCD takes a
     // contiguous range of units
@@ -126,20 +173,33 @@ __global__ __launch_bounds__(256) void kda_ssm_prefill_kernel(const SsmArgs a) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
-    TileLane<T, N> ln;
-    TileLane<T, P> lp;
-    TileLane<T, kC> lm;
-    ln.set(lane);
-    lp.set(lane);
-    if constexpr (OUT) lm.set(lane);
+    TileRows<T, kC, N> rn;    // rows of B (and of C, oC further)
+    TileCols<T, kC> cn;       // columns of B
+    TileRows<T, kC, kC> rm;   // rows of M
+    cn.set(sB, lane);
+    if constexpr (OUT) {
+        rn.set(sB, lane);
+        rm.set(sM, lane);
+    }
+    // this lane's four columns of row r of x, column tile ct of the wave
+    KDA_LDS T* xrow[NCT];
+#pragma unroll
+    for (int ct = 0; ct < NCT; ++ct) xrow[ct] = lds_pin(sX + tile_at<T, kC>(r, 4 * (wave * NCT + ct) + g));
 
-    const T* xb = reinterpret_cast<const T*>(a.x) + (long long)b * a.T * a.x_stride + (long long)h * P;
-    const T* bb = reinterpret_cast<const T*>(a.Bm) + (long long)b * a.T * a.b_stride + (long long)grp * N;
-    const T* cb = reinterpret_cast<const T*>(a.Cm) + (long long)b * a.T * a.c_stride + (long long)grp * N;
-    const T* zb = reinterpret_cast<const T*>(a.z);
-    if (OUT && zb) zb += (long long)b * a.T * a.z_stride + (long long)h * P;
-    const T* db = reinterpret_cast<const T*>(a.dt) + (long long)b * a.T * a.dt_stride + h;
-    T* yb = OUT ? reinterpret_cast<T*>(a.y) + ((long long)b * a.T * a.H + h) * P : nullptr;
+    // row t_begin of every input, and the bytes between rows
+    const long long row0 = (long long)b * a.T + t_begin;
+    const T* xp = reinterpret_cast<const T*>(a.x) + row0 * a.x_stride + (long long)h * P;
+    const T* bp = reinterpret_cast<const T*>(a.Bm) + row0 * a.b_stride + (long long)grp * N;
+    const T* cp = reinterpret_cast<const T*>(a.Cm) + row0 * a.c_stride + (long long)grp * N;
+    const T* dp = reinterpret_cast<const T*>(a.dt) + row0 * a.dt_stride + h;
+    const T* zp = reinterpret_cast<const T*>(a.z);
+    const bool gated = OUT && zp != nullptr;
+    if (gated) zp += row0 * a.z_stride + (long long)h * P;
+    T* yp = OUT ? reinterpret_cast<T*>(a.y) + (row0 * a.H + h) * P : nullptr;
+    constexpr uint32_t ES = sizeof(T), ROW_P = P * ES;
+    const uint32_t x_step = (uint32_t)a.x_stride * ES, b_step = (uint32_t)a.b_stride * ES, c_step = (uint32_t)a.c_stride * ES;
+    const uint32_t z_step = (uint32_t)a.z_stride * ES, y_step = (uint32_t)a.H * ROW_P;
+    const uint32_t z_off = r * z_step + (wave * WC + 4 * g) * ES, y_off = r * y_step + (wave * WC + 4 * g) * ES;
     const float A2 = a.A[h] * kLog2e;
     const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
     const float Dh = a.D ? a.D[h] : 0.0f;
@@ -155,10 +215,17 @@ __global__ __launch_bounds__(256) void kda_ssm_prefill_kernel(const SsmArgs a) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
+        for (int ct = 0; ct < NCT; ++ct) S[nt][ct] = zero4();
+    // this lane's element of row tile 0, column tile 0 of a state
+    const uint32_t s_off = (uint32_t)((4 * g * P + wave * WC + r) * sizeof(float));
+    if (sin) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                S[nt][ct][i] = sin ? sin[(16 * nt + 4 * g + i) * P + wave * WC + 16 * ct + r] : 0.0f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[nt][ct][i] = *at_byte(sin + (16 * nt + i) * P + 16 * ct, s_off);
+    }
     if (!OUT && s == 0 && a.keep_S0) {   // S_T is S0: the other pass's last segment overwrites it
         float* keep = a.ws_state + bh * a.n_seg * (long long)(N * P);
 #pragma unroll
@@ -166,139 +233,164 @@ __global__ __launch_bounds__(256) void kda_ssm_prefill_kernel(const SsmArgs a) {
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) keep[(16 * nt + 4 * g + i) * P + wave * WC + 16 * ct + r] = S[nt][ct][i];
+                for (int i = 0; i < 4; ++i) *at_byte(keep + (16 * nt + i) * P + 16 * ct, s_off) = S[nt][ct][i];
     }
     float total = 0.0f;   // exponent (base 2) of the segment's decay
 
-    Stage<T, P> gx;
-    Stage<T, N> gb, gc;
+    // Inputs are requested one chunk ahead, the raw steps (last wave) two chunks ahead: their running sum
+    // is a long chain, formed while the other waves work on M.
+    Stage<T, P, NW> gx;
+    Stage<T, N, NW> gb, gc;
     float gdt = 0.0f;
-    auto request = [&](long long t0) {
-        const int rows = t_end - t0 < kC ? (int)(t_end - t0) : kC;
-        gx.load(xb + t0 * a.x_stride, a.x_stride, rows, tid);
-        gb.load(bb + t0 * a.b_stride, a.b_stride, rows, tid);
-        if constexpr (OUT) gc.load(cb + t0 * a.c_stride, a.c_stride, rows, tid);
-        if (wave == 0) gdt = lane < rows ? to_f32<T>(db[(t0 + lane) * a.dt_stride]) : 0.0f;
+    // tokens left in the segment (32 bits: at most seg_len)
+    int left = (int)(t_end - t_begin);
+    auto request = [&](int rows) {   // the chunk at xp, bp, cp
+        gx.load(xp, x_step, rows, wave, lane);
+        gb.load(bp, b_step, rows, wave, lane);
+        if constexpr (OUT) gc.load(cp, c_step, rows, wave, lane);
     };
-    if (t_begin < t_end) request(t_begin);
-
-    for (long long t0 = t_begin; t0 < t_end; t0 += kC) {
-        const int rows = t_end - t0 < kC ? (int)(t_end - t0) : kC;
-        gx.put(sX, tid);
-        gb.put(sB, tid);
-        if constexpr (OUT) gc.put(sC, tid);
-        if (wave == 0) {
-            const float d = lane < rows ? softplus_f32(gdt + bias) : 0.0f;
-            const float c = wave_prefix(lane < rows ? fmaxf(d * A2, kDecayMin) : 0.0f, lane);
-            const float cl = __shfl(c, 63);
-            sCum[lane] = c;
-            sDt[lane] = d;
-            sW[lane] = fast_exp2(cl - c) * d;
+    auto request_dt = [&](int ahead) {
+        const int t = ahead + lane < left ? ahead + lane : left - 1;
+        gdt = to_f32<T>(dp[t * a.dt_stride]);
+    };
+    if (left > 0) {
+        if (wave == NW - 1) {
+            request_dt(0);
+            chunk_decay(sD, gdt + bias, lane < left, A2, lane);
+            request_dt(kC);
         }
-        __syncthreads();
-        if (t0 + kC < t_end) request(t0 + kC);
+        request(left < kC ? left : kC);
+    }
 
+    // columns 16 (wave NCT + ct) .. of x, transposed (the tile index is the wave's: addresses of its own)
+    TileCols<T, kC> cx[NCT];
+#pragma unroll
+    for (int ct = 0; ct < NCT; ++ct) cx[ct].set_tile(sX, lane, wave * NCT + ct);
+    auto cx_frag = [&](Frag<T>& f, int ct, int kb) { cx[ct].frag(f, 0, 0, kb); };
+
+    for (int par = 0; left > 0; left -= kC, par ^= 1) {
+        const int rows = left < kC ? left : kC;
+        const KDA_LDS ChunkDecay* cd = sD + par;
+        gx.put(sX, wave, lane);
+        gb.put(sB, wave, lane);
+        if constexpr (OUT) gc.put(sC, wave, lane);
+        __syncthreads();
+        vec4 zv[4][NCT];
+        if (gated) {
+            const buffer_t zbuf = make_buffer(zp, (uint32_t)(rows - 1) * z_step + ROW_P);
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) buffer_load4(zv[ti][ct], zbuf, z_off, 16 * ti * z_step + 16 * ct * ES);
+            zp += kC * a.z_stride;
+        }
         if constexpr (OUT) {
             // M[i][j] = e^{c_i - c_j} dt_j (C_i . B_j) for j <= i: the ten lower 16 x 16 tiles
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const int pair = wave + 4 * k;
-                if (pair < 10) {
+            // (the pair is taken as new in every chunk: its addresses are not worth registers)
+            for (int pair = pinned_s(wave); pair < 10; pair += NW) {
+                {
                     const int ti = pair < 1 ? 0 : (pair < 3 ? 1 : (pair < 6 ? 2 : 3));
                     const int tj = pair - ti * (ti + 1) / 2;
                     f32x4_t acc = zero4();
 #pragma unroll
                     for (int kb = 0; kb < N / 32; ++kb) {
                         Frag<T> fb, fc;
-                        tile_row_frag<T, N>(fb, sB, ln, tj, kb);
-                        tile_row_frag<T, N>(fc, sC, ln, ti, kb);
+                        rn.frag(fb, 16 * 32 * tj, 0, kb);
+                        rn.frag(fc, oC + 16 * 32 * ti, 0, kb);
                         acc = mma(fb, fc, acc);   // acc[q]: token j = 16 tj + 4 g + q against i = 16 ti + r
                     }
-                    const float ci = sCum[16 * ti + r];
-                    const f32x4_t cj = *reinterpret_cast<const KDA_LDS f32x4_t*>(sCum + 16 * tj + 4 * g);
-                    const f32x4_t dj = *reinterpret_cast<const KDA_LDS f32x4_t*>(sDt + 16 * tj + 4 * g);
+                    const float ci = cd->hi[16 * ti + r], cil = cd->lo[16 * ti + r];
+                    const f32x4_t cj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->hi + 16 * tj + 4 * g);
+                    const f32x4_t cjl = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->lo + 16 * tj + 4 * g);
+                    const f32x4_t dj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->dt + 16 * tj + 4 * g);
                     float m[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float v = acc[q] * (fast_exp2(ci - cj[q]) * dj[q]);
+                        const float v = acc[q] * (fast_exp2((ci - cj[q]) + (cil - cjl[q])) * dj[q]);
                         m[q] = tj < ti || 4 * g + q <= r ? v : 0.0f;
                     }
-                    lds_store_run<4>(sM + (16 * ti + r) * kC + (((4 * tj + g) ^ tile_f(r)) << 2), m);
+                    lds_store_run<4>(sM + 16 * 32 * ti + tile_at<T, kC>(r, 4 * tj + g), m);
                 }
             }
-            __syncthreads();
         }
+        if (left > kC && wave == NW - 1) {
+            chunk_decay(sD + (par ^ 1), gdt + bias, kC + lane < left, A2, lane);
+            request_dt(2 * kC);
+            dp += kC * a.dt_stride;
+        }
+        if constexpr (OUT) __syncthreads();
 
         // x of this wave's columns, transposed: contraction over tokens
         Frag<T> xt[2][NCT];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) tile_tr_frag<T, P>(xt[kb][ct], sX, lp, wave * NCT + ct, kb, lane);
+            for (int ct = 0; ct < NCT; ++ct) cx_frag(xt[kb][ct], ct, kb);
 
         if constexpr (OUT) {
             // y^T = (S^T C^T) e^{c_i} + x^T M^T: columns are tokens, rows p
             f32x4_t y[4][NCT];
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) y[ti][ct] = zero4();
+            const buffer_t ybuf = make_buffer(yp, (uint32_t)(rows - 1) * y_step + ROW_P);
+            yp += (long long)kC * a.H * P;
 #pragma unroll
             for (int kb = 0; kb < N / 32; ++kb) {
                 Frag<T> fs[NCT];
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) acc_pair_frag<T>(fs[ct], S[2 * kb][ct], S[2 * kb + 1][ct], true);
+                for (int ct = 0; ct < NCT; ++ct) acc_pair_frag<T>(fs[ct], S[kb][ct], S[kb + NT / 2][ct], true);
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) {
                     Frag<T> fc;
-                    tile_row_frag<T, N>(fc, sC, ln, ti, kb);
+                    rn.frag(fc, oC, ti, kb);
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) y[ti][ct] = mma(fs[ct], fc, y[ti][ct]);
+                    for (int ct = 0; ct < NCT; ++ct) y[ti][ct] = mma(fs[ct], fc, kb == 0 ? zero4() : y[ti][ct]);
                 }
             }
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
-                const float e = fast_exp2(sCum[16 * ti + r]);
+                __builtin_amdgcn_sched_barrier(0);
+                const float e = fast_exp2(cd->hi[16 * ti + r]);
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) y[ti][ct][q] *= e;
 #pragma unroll
-                for (int kb = 0; kb <= ti / 2; ++kb) {
+                for (int kb = 0; kb < (ti < 1 ? 1 : 2); ++kb) {   // token tiles kb and kb + 2, as far as they reach
                     Frag<T> fm;
-                    if (2 * kb + 1 > ti) tile_row_frag_lo<T, kC>(fm, sM, lm, ti, kb);
-                    else tile_row_frag<T, kC>(fm, sM, lm, ti, kb);
+                    if (kb + 2 > ti) rm.frag_lo(fm, 0, ti, kb);
+                    else rm.frag(fm, 0, ti, kb);
 #pragma unroll
                     for (int ct = 0; ct < NCT; ++ct) y[ti][ct] = mma(xt[kb][ct], fm, y[ti][ct]);
                 }
-                const int i = 16 * ti + r;
-                if (i < rows) {
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) {
-                        const int p0 = wave * WC + 16 * ct + 4 * g;
-                        const KDA_LDS T* xr = sX + i * P + (((p0 >> 2) ^ tile_f(r)) << 2);
-                        float o[4];
+                for (int ct = 0; ct < NCT; ++ct) {
+                    const vec4 xv = *reinterpret_cast<const KDA_LDS vec4*>(xrow[ct] + 16 * 32 * ti);
+                    f32x4_t o;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) o[q] = fmaf(Dh, to_f32<T>(xr[q]), y[ti][ct][q]);
-                        if (zb) {
-                            typedef __attribute__((ext_vector_type(4))) T vec4;
-                            const vec4 zv = *reinterpret_cast<const vec4*>(zb + (t0 + i) * a.z_stride + p0);
+                    for (int q = 0; q < 4; ++q) o[q] = fmaf(Dh, to_f32<T>((T)xv[q]), y[ti][ct][q]);
+                    if (gated) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) o[q] *= silu_f32(to_f32<T>((T)zv[q]));
-                        }
-                        typedef __attribute__((ext_vector_type(4))) T vec4;
-                        vec4 ov;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) ov[q] = from_f32<T>(o[q]);
-                        *reinterpret_cast<vec4*>(yb + (t0 + i) * (long long)a.H * P + p0) = ov;
+                        for (int q = 0; q < 4; ++q) o[q] *= silu_f32(to_f32<T>((T)zv[ti][ct][q]));
                     }
+                    vec4 ov;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) ov[q] = from_f32<T>(o[q]);
+                    buffer_store4(ov, ybuf, y_off, 16 * ti * y_step + 16 * ct * ES);
                 }
             }
         }
 
+        // the next chunk's rows are requested here, where the outputs' registers are free again
+        if (left > kC) {
+            xp += kC * a.x_stride;
+            bp += kC * a.b_stride;
+            cp += kC * a.c_stride;
+            request(left - kC < kC ? left - kC : kC);
+        }
+
         // S <- e^{c_63} S + B^T (w x)
+        __builtin_amdgcn_sched_barrier(0);
         {
-            const float cl = sCum[kC - 1];
+            const float cl = cd->hi[kC - 1];
             const float eL = fast_exp2(cl);
             total += cl;
 #pragma unroll
@@ -309,17 +401,16 @@ __global__ __launch_bounds__(256) void kda_ssm_prefill_kernel(const SsmArgs a) {
                     for (int q = 0; q < 4; ++q) S[nt][ct][q] *= eL;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
+                __builtin_amdgcn_sched_barrier(0);
                 float w[8];
-                f32x8_ld(w, sW + 32 * kb + 4 * g);
+                load_weights(w, cd->w + 16 * kb + 4 * g);
                 Frag<T> xs[NCT][NP];
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) split_parts(xs[ct], j, xt[kb][ct].get(j) * w[j]);
+                for (int ct = 0; ct < NCT; ++ct) weigh(xs[ct], xt[kb][ct], w);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     Frag<T> fb;
-                    tile_tr_frag<T, N>(fb, sB, ln, nt, kb, lane);
+                    cn.frag(fb, 0, nt, kb);
 #pragma unroll
                     for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
@@ -343,7 +434,7 @@ __global__ __launch_bounds__(256) void kda_ssm_prefill_kernel(const SsmArgs a) {
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) so[(16 * nt + 4 * g + i) * P + wave * WC + 16 * ct + r] = S[nt][ct][i];
+                for (int i = 0; i < 4; ++i) *at_byte(so + (16 * nt + i) * P + 16 * ct, s_off) = S[nt][ct][i];
     }
 }
 
@@ -436,11 +527,12 @@ namespace {
 
 template <int N, int P, typename T>
 hipError_t ssm_launch(SsmPass pass, SsmArgs a, hipStream_t s) {
+    constexpr int NW = P / 16;
     a.per_xcd = (a.n_units + 7) / 8;
     const dim3 grid((unsigned)(8 * a.per_xcd));
     switch (pass) {
-        case SsmPass::kStates: kda_ssm_prefill_kernel<N, P, T, false><<<grid, 256, 0, s>>>(a); break;
-        case SsmPass::kOutputs: kda_ssm_prefill_kernel<N, P, T, true><<<grid, 256, 0, s>>>(a); break;
+        case SsmPass::kStates: kda_ssm_prefill_kernel<N, P, T, false, NW><<<grid, 64 * NW, 0, s>>>(a); break;
+        case SsmPass::kOutputs: kda_ssm_prefill_kernel<N, P, T, true, NW><<<grid, 64 * NW, 0, s>>>(a); break;
         case SsmPass::kToken: kda_ssm_step_kernel<N, P, T><<<grid, 4 * P, 0, s>>>(a); break;
     }
     return hipGetLastError();

@@ -1,9 +1,14 @@
 // LDS tiles shared by the state space scan and the window attention (gfx950, wave64).
 //
-// A tile holds 64-bit (bf16) or 128-bit (fp32) chunks of four elements.  Chunk c of row r lies at
-// chunk c ^ f(r) of the row, f(r) = 4 (r & 3) + ((r >> 2) & 3): the sixteen rows of a matrix
-// operand, and the four rows by four chunks that one transposed read takes, then fall on different
-// banks, with no padding between rows.  Rows hold a multiple of 64 elements.
+// A tile of ROWS rows is stored in blocks of 32 columns, row after row inside a block, in chunks of four
+// elements (8 bytes of bf16, 16 of fp32).  Chunk c of row r lies at place c ^ f(r) of its 8: f is chosen
+// so that the 16 (bf16) or 8 (fp32) rows that one cycle of a row read takes, and the four rows by four
+// chunks of one transposed read, fall on different banks without padding.
+//
+// A matrix operand's 32 contraction slots are two stacked 16-wide tiles, as in kda_device.h, but tiles
+// half the contraction apart instead of neighbours: (a, a + n/2).  Both halves then lie a constant
+// distance apart, in reach of one two-address read with an immediate offset, and arrive in adjacent
+// registers; neighbours would differ by an exclusive-or of the lane's address.
 #pragma once
 
 #include "kda_device.h"
@@ -12,7 +17,13 @@ namespace kda {
 
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 
-__device__ __forceinline__ int tile_f(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+template <typename T> __device__ __forceinline__ int tile_f(int r);
+template <> __device__ __forceinline__ int tile_f<__bf16>(int r) { return ((r & 2) << 1) | ((r >> 2) & 3); }
+template <> __device__ __forceinline__ int tile_f<float>(int r) { return r & 7; }
+
+// Four elements as one vector.
+template <typename T> struct Vec4 { typedef bf16x4_t type; };
+template <> struct Vec4<float> { typedef f32x4_t type; };
 
 // Transposed read of bf16: within each 16-lane group, lane 4k + j names four elements of row k
 // (columns 4j .. 4j + 3) and lane i receives column i of rows 0 .. 3.  (Not a template: see lds_dma16.)
@@ -21,92 +32,175 @@ __device__ __forceinline__ bf16x4_t lds_read_tr(const KDA_LDS __bf16* p) {
     return __builtin_bit_cast(bf16x4_t, v);
 }
 
-// Lane offsets (elements) into a tile of rows of WIDTH elements.
-template <typename T, int WIDTH> struct TileLane {
-    int row[4];   // row operand: row r, chunk (g ^ 4x) ^ f(r), x = 2 (block & 1) + half
-    int tr[4];    // transposed operand: column tile t with t & 3 = x
-    __device__ __forceinline__ void set(int lane) {
-        const int g = lane >> 4, r = lane & 15, k = r >> 2, j = r & 3;
-        const int q = g ^ tile_f(r);
+__device__ __forceinline__ void frag_join(Frag<__bf16>& f, bf16x4_t lo, bf16x4_t hi) {
+    f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ void frag_join(Frag<float>& f, f32x4_t lo, f32x4_t hi) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            row[x] = r * WIDTH + ((q ^ (x << 2)) << 2);
-            tr[x] = (4 * g + k) * WIDTH + ((((x << 2) | j) ^ ((k << 2) | g)) << 2);
+    for (int i = 0; i < 4; ++i) {
+        f.v[i] = lo[i];
+        f.v[4 + i] = hi[i];
+    }
+}
+
+// Offset (elements) of chunk c (of the whole row) of row r in a tile.
+template <typename T, int ROWS> __device__ __forceinline__ int tile_at(int r, int c) {
+    return (c >> 3) * (ROWS * 32) + r * 32 + (((c & 7) ^ tile_f<T>(r)) << 2);
+}
+
+// Row operand of a tile of WIDTH columns (a multiple of 64): a lane's addresses, pinned in registers, so
+// that everything it reads lies at a constant offset from one of them.  `delta` arguments are constant
+// element offsets, by which tiles of one shape share the addresses.
+template <typename T, int ROWS, int WIDTH> struct TileRows {
+    typedef typename Vec4<T>::type vec4;
+    KDA_LDS T* at[2];   // row r, chunk 4 x + g of a block
+    __device__ __forceinline__ void set(KDA_LDS T* tile, int lane) {
+        const int g = lane >> 4, r = lane & 15;
+        at[0] = lds_pin(tile + tile_at<T, ROWS>(r, g));
+        at[1] = lds_pin(tile + tile_at<T, ROWS>(r, 4 + g));
+    }
+    // rows 16 a .. 16 a + 15, contraction block q: columns of tiles q and q + WIDTH/32
+    __device__ __forceinline__ void frag(Frag<T>& f, int delta, int a, int q) const {
+        const KDA_LDS T* p = at[q & 1] + delta + 16 * 32 * a + (q >> 1) * (ROWS * 32);
+        frag_join(f, *reinterpret_cast<const KDA_LDS vec4*>(p),
+                  *reinterpret_cast<const KDA_LDS vec4*>(p + (WIDTH / 64) * (ROWS * 32)));
+    }
+    // the first tile of the block, the second one zero
+    __device__ __forceinline__ void frag_lo(Frag<T>& f, int delta, int a, int q) const {
+        const KDA_LDS T* p = at[q & 1] + delta + 16 * 32 * a + (q >> 1) * (ROWS * 32);
+        const vec4 z = {(T)0.0f, (T)0.0f, (T)0.0f, (T)0.0f};
+        frag_join(f, *reinterpret_cast<const KDA_LDS vec4*>(p), z);
+    }
+};
+
+// Transposed operand: its row (or column) r is column 16 t + r of the tile, its contraction block q the
+// tile's rows 16 q .. and 16 q + ROWS/2 ..
+template <typename T, int ROWS> struct TileCols;
+
+template <int ROWS> struct TileCols<__bf16, ROWS> {
+    KDA_LDS __bf16* at[2];   // column tile t with t & 1 = x
+    __device__ __forceinline__ KDA_LDS __bf16* of(KDA_LDS __bf16* tile, int lane, int t) const {
+        return lds_pin(tile + tile_at<__bf16, ROWS>(4 * (lane >> 4) + ((lane & 15) >> 2), 4 * t + (lane & 3)));
+    }
+    __device__ __forceinline__ void set(KDA_LDS __bf16* tile, int lane) {
+        at[0] = of(tile, lane, 0);
+        at[1] = of(tile, lane, 1);
+    }
+    // addresses for column tile t only, which is then used as t = 0
+    __device__ __forceinline__ void set_tile(KDA_LDS __bf16* tile, int lane, int t) { at[0] = of(tile, lane, t); }
+    __device__ __forceinline__ void frag(Frag<__bf16>& f, int delta, int t, int q) const {
+        KDA_LDS __bf16* p = at[t & 1] + delta + (t >> 1) * (ROWS * 32) + 16 * 32 * q;
+        frag_join(f, lds_read_tr(p), lds_read_tr(p + (ROWS / 2) * 32));
+    }
+};
+
+template <int ROWS> struct TileCols<float, ROWS> {
+    KDA_LDS float* at[2][4];   // element r of column tile t with t & 1 = x, row 4 g + i
+    __device__ __forceinline__ KDA_LDS float* of(KDA_LDS float* tile, int lane, int t, int i) const {
+        const int g = lane >> 4, r = lane & 15;
+        return lds_pin(tile + tile_at<float, ROWS>(4 * g + i, 4 * t + (r >> 2)) + (r & 3));
+    }
+    __device__ __forceinline__ void set(KDA_LDS float* tile, int lane) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            at[0][i] = of(tile, lane, 0, i);
+            at[1][i] = of(tile, lane, 1, i);
+        }
+    }
+    __device__ __forceinline__ void set_tile(KDA_LDS float* tile, int lane, int t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[0][i] = of(tile, lane, t, i);
+    }
+    __device__ __forceinline__ void frag(Frag<float>& f, int delta, int t, int q) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const KDA_LDS float* p = at[t & 1][i] + delta + (t >> 1) * (ROWS * 32) + 16 * 32 * q;
+            f.v[i] = p[0];
+            f.v[4 + i] = p[(ROWS / 2) * 32];
         }
     }
 };
 
-// Row operand: rows 16 a .. 16 a + 15, contraction block kb of 32 columns.
-template <typename T, int WIDTH>
-__device__ __forceinline__ void tile_row_frag(Frag<T>& f, const KDA_LDS T* tile, const TileLane<T, WIDTH>& l, int a,
-                                              int kb) {
-    const KDA_LDS T* p = tile + 16 * a * WIDTH + (kb >> 1) * 64;
-    const int x = (kb & 1) * 2;
-    if constexpr (sizeof(T) == 2) {
-        const bf16x4_t lo = *reinterpret_cast<const KDA_LDS bf16x4_t*>(p + l.row[x]);
-        const bf16x4_t hi = *reinterpret_cast<const KDA_LDS bf16x4_t*>(p + l.row[x + 1]);
-        f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-        const f32x4_t lo = *reinterpret_cast<const KDA_LDS f32x4_t*>(p + l.row[x]);
-        const f32x4_t hi = *reinterpret_cast<const KDA_LDS f32x4_t*>(p + l.row[x + 1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f.v[i] = lo[i];
-            f.v[4 + i] = hi[i];
-        }
+// How a wave moves rows into a tile: one step is 16 bytes per lane, 16 rows (bf16) or 8 rows (fp32) of
+// one block of 32 columns.  The lanes' rows are ordered so that a step's stores fall on different banks.
+template <typename T> struct TileStep;
+template <> struct TileStep<__bf16> {
+    static constexpr int ROWS = 16;
+    static __device__ __forceinline__ int row(int lane) {
+        return ((lane >> 2) & 1) | ((lane >> 3) & 2) | ((lane >> 1) & 4) | ((lane >> 2) & 8);
     }
-}
+    static __device__ __forceinline__ int piece(int lane) { return lane & 3; }
+};
+template <> struct TileStep<float> {
+    static constexpr int ROWS = 8;
+    static __device__ __forceinline__ int row(int lane) { return lane >> 3; }
+    static __device__ __forceinline__ int piece(int lane) { return lane & 7; }
+};
 
-// The lower half of a row operand's block, the upper half zero.
-template <typename T, int WIDTH>
-__device__ __forceinline__ void tile_row_frag_lo(Frag<T>& f, const KDA_LDS T* tile, const TileLane<T, WIDTH>& l, int a,
-                                                 int kb) {
-    const KDA_LDS T* p = tile + 16 * a * WIDTH + (kb >> 1) * 64 + l.row[(kb & 1) * 2];
-    if constexpr (sizeof(T) == 2) {
-        const bf16x4_t lo = *reinterpret_cast<const KDA_LDS bf16x4_t*>(p);
-        const bf16x4_t z = {(__bf16)0.0f, (__bf16)0.0f, (__bf16)0.0f, (__bf16)0.0f};
-        f.v = __builtin_shufflevector(lo, z, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-        const f32x4_t lo = *reinterpret_cast<const KDA_LDS f32x4_t*>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f.v[i] = lo[i];
-            f.v[4 + i] = 0.0f;
-        }
+// A lane's place for its step: the two chunks of 8 bf16, or the one of 4 fp32.
+template <typename T, int ROWS> struct TilePut;
+template <int ROWS> struct TilePut<__bf16, ROWS> {
+    KDA_LDS __bf16 *lo, *hi;
+    __device__ __forceinline__ void set(KDA_LDS __bf16* tile, int lane) {
+        const int r = TileStep<__bf16>::row(lane), m = TileStep<__bf16>::piece(lane);
+        lo = lds_pin(tile + tile_at<__bf16, ROWS>(r, 2 * m));
+        hi = lds_pin(tile + tile_at<__bf16, ROWS>(r, 2 * m + 1));
     }
-}
-
-// Transposed operand: its row (or column) r is column 16 t + r of the tile, its contraction block the
-// tile's rows 32 kb .. 32 kb + 31.
-template <typename T, int WIDTH>
-__device__ __forceinline__ void tile_tr_frag(Frag<T>& f, const KDA_LDS T* tile, const TileLane<T, WIDTH>& l, int t,
-                                             int kb, int lane) {
-    const KDA_LDS T* p = tile + 32 * kb * WIDTH + (t >> 2) * 64;
-    if constexpr (sizeof(T) == 2) {
-        const bf16x4_t lo = lds_read_tr(p + l.tr[t & 3]);
-        const bf16x4_t hi = lds_read_tr(p + l.tr[t & 3] + 16 * WIDTH);
-        f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-        const int g = lane >> 4, r = lane & 15;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = (((t & 3) ^ i) << 2) | ((r >> 2) ^ g);
-            const KDA_LDS T* q = p + (4 * g + i) * WIDTH + (c << 2) + (r & 3);
-            f.v[i] = q[0];
-            f.v[4 + i] = q[16 * WIDTH];
-        }
+    __device__ __forceinline__ void put(int delta, u32x4_t v) const {
+        *reinterpret_cast<KDA_LDS u32x2_t*>(lo + delta) = u32x2_t{v[0], v[1]};
+        *reinterpret_cast<KDA_LDS u32x2_t*>(hi + delta) = u32x2_t{v[2], v[3]};
     }
-}
+};
+template <int ROWS> struct TilePut<float, ROWS> {
+    KDA_LDS float* at;
+    __device__ __forceinline__ void set(KDA_LDS float* tile, int lane) {
+        at = lds_pin(tile + tile_at<float, ROWS>(TileStep<float>::row(lane), TileStep<float>::piece(lane)));
+    }
+    __device__ __forceinline__ void put(int delta, u32x4_t v) const { *reinterpret_cast<KDA_LDS u32x4_t*>(at + delta) = v; }
+};
 
-// Sixteen bytes of a row (8 bf16 or 4 fp32, piece m of the row) into a tile.
-__device__ __forceinline__ void tile_put(KDA_LDS __bf16* row, int m, int r, u32x4_t v) {
-    const int f = tile_f(r);
-    const bool swap = f & 1;
-    const u32x4_t w = {swap ? v[2] : v[0], swap ? v[3] : v[1], swap ? v[0] : v[2], swap ? v[1] : v[3]};
-    *reinterpret_cast<KDA_LDS u32x4_t*>(row + (((2 * m) ^ (f & ~1)) << 2)) = w;
+// The steps of NW waves over a tile of ROWS x WIDTH: a wave's steps i = 0 .. N - 1 cover blocks of 32
+// columns of one row group, or whole row groups one after the other.
+template <typename T, int ROWS, int WIDTH, int NW> struct TileSteps {
+    static constexpr int NB = WIDTH / 32, TOTAL = NB * (ROWS / TileStep<T>::ROWS);
+    static constexpr int N = TOTAL / NW;
+    static_assert(TOTAL % NW == 0 && (N % NB == 0 || NB % N == 0), "waves share the steps evenly");
+    static __device__ __forceinline__ int group0(int wave) { return N >= NB ? wave * (N / NB) : wave / (NB / N); }
+    static __device__ __forceinline__ int block0(int wave) { return N >= NB ? 0 : (wave % (NB / N)) * N; }
+    static constexpr int group(int i) { return N >= NB ? i / NB : 0; }   // beyond group0
+    static constexpr int block(int i) { return N >= NB ? i % NB : i; }   // beyond block0
+};
+
+// A range of memory with bounds: loads past its end give zeros, stores past it are dropped.  The address
+// is a lane offset plus a uniform one, in bytes.  (Not templates: see lds_dma16.)
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+__device__ __forceinline__ buffer_t make_buffer(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
-__device__ __forceinline__ void tile_put(KDA_LDS float* row, int m, int r, u32x4_t v) {
-    *reinterpret_cast<KDA_LDS u32x4_t*>(row + ((m ^ tile_f(r)) << 2)) = v;
+__device__ __forceinline__ u32x4_t buffer_load16(buffer_t b, uint32_t lane_off, uint32_t off) {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane_off, (int)off, 0));
+}
+__device__ __forceinline__ u32x2_t buffer_load8(buffer_t b, uint32_t lane_off, uint32_t off) {
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(b, (int)lane_off, (int)off, 0));
+}
+__device__ __forceinline__ void buffer_store16(buffer_t b, uint32_t lane_off, uint32_t off, u32x4_t v) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, b, (int)lane_off, (int)off, 0);
+}
+__device__ __forceinline__ void buffer_store8(buffer_t b, uint32_t lane_off, uint32_t off, u32x2_t v) {
+    __builtin_amdgcn_raw_buffer_store_b64(v, b, (int)lane_off, (int)off, 0);
+}
+// Four elements.
+__device__ __forceinline__ void buffer_load4(bf16x4_t& v, buffer_t b, uint32_t lane_off, uint32_t off) {
+    v = __builtin_bit_cast(bf16x4_t, buffer_load8(b, lane_off, off));
+}
+__device__ __forceinline__ void buffer_load4(f32x4_t& v, buffer_t b, uint32_t lane_off, uint32_t off) {
+    v = __builtin_bit_cast(f32x4_t, buffer_load16(b, lane_off, off));
+}
+__device__ __forceinline__ void buffer_store4(bf16x4_t v, buffer_t b, uint32_t lane_off, uint32_t off) {
+    buffer_store8(b, lane_off, off, __builtin_bit_cast(u32x2_t, v));
+}
+__device__ __forceinline__ void buffer_store4(f32x4_t v, buffer_t b, uint32_t lane_off, uint32_t off) {
+    buffer_store16(b, lane_off, off, __builtin_bit_cast(u32x4_t, v));
 }
 
 }  // namespace kda

@@ -32,20 +32,12 @@ __device__ __forceinline__ float sum_over_groups(float v) {
     return v + __shfl_xor(v, 32);
 }
 
-// Eight slots of one row in global memory, p at slot 0 of the block (slots 4g.. and 16 + 4g..).
-__device__ __forceinline__ void global_frag(Frag<__bf16>& f, const __bf16* p) {
-    const bf16x4_t lo = *reinterpret_cast<const bf16x4_t*>(p);
-    const bf16x4_t hi = *reinterpret_cast<const bf16x4_t*>(p + 16);
-    f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+// Eight slots of one row in global memory, p at the first one: four at p and four half a row further.
+template <int D> __device__ __forceinline__ void global_frag(Frag<__bf16>& f, const __bf16* p) {
+    frag_join(f, *reinterpret_cast<const bf16x4_t*>(p), *reinterpret_cast<const bf16x4_t*>(p + D / 2));
 }
-__device__ __forceinline__ void global_frag(Frag<float>& f, const float* p) {
-    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(p);
-    const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(p + 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f.v[i] = lo[i];
-        f.v[4 + i] = hi[i];
-    }
+template <int D> __device__ __forceinline__ void global_frag(Frag<float>& f, const float* p) {
+    frag_join(f, *reinterpret_cast<const f32x4_t*>(p), *reinterpret_cast<const f32x4_t*>(p + D / 2));
 }
 // Eight consecutive elements of one row (slot order 8g .. 8g + 7; both operands use it).
 __device__ __forceinline__ void global_frag8(Frag<__bf16>& f, const __bf16* p) {
@@ -82,11 +74,12 @@ template <typename T> __device__ __forceinline__ void store4(T* p, const f32x4_t
 template <int D, typename T, int NQ>
 __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArgs a) {
     constexpr int BM = 64 * NQ;
-    constexpr int PER_ROW = D * (int)sizeof(T) / 16, EPP = 16 / (int)sizeof(T);
-    constexpr int NST = kKeys * PER_ROW / 256, ROWS = 256 / PER_ROW;
-    __shared__ __attribute__((aligned(16))) T sK_[kKeys * D], sV_[kKeys * D];
-    KDA_LDS T* sK = (KDA_LDS T*)sK_;
-    KDA_LDS T* sV = (KDA_LDS T*)sV_;
+    typedef TileSteps<T, kKeys, D, 4> Steps;
+    constexpr int NG = Steps::N / Steps::NB;   // row groups per wave
+    static_assert(NG * Steps::NB == Steps::N, "a wave takes whole rows");
+    __shared__ __attribute__((aligned(16))) T smem[2 * kKeys * D];   // a tile of keys, a tile of values
+    KDA_LDS T* sK = (KDA_LDS T*)smem;
+    KDA_LDS T* sV = sK + kKeys * D;
 
     // unit = (b, kv head, query tile, head of the group): consecutive units share keys, and each XCD
     // takes a contiguous range of them
@@ -118,8 +111,10 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
-    TileLane<T, D> ld;
-    ld.set(lane);
+    TileRows<T, kKeys, D> rk;
+    TileCols<T, kKeys> cv;
+    rk.set(sK, lane);
+    cv.set(sV, lane);
 
     const T* kn = reinterpret_cast<const T*>(a.k) + (long long)b * a.T * a.k_stride + (long long)hk * D;
     const T* vn = reinterpret_cast<const T*>(a.v) + (long long)b * a.T * a.v_stride + (long long)hk * D;
@@ -140,7 +135,7 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
         const T* qp = reinterpret_cast<const T*>(a.q) + ((long long)b * a.T + i) * a.q_stride + (long long)h * D + 4 * g;
 #pragma unroll
         for (int kb = 0; kb < D / 32; ++kb) {
-            if (i < len) global_frag(fq[n][kb], qp + 32 * kb);
+            if (i < len) global_frag<D>(fq[n][kb], qp + 16 * kb);
             else fq[n][kb].zero();
         }
     }
@@ -155,42 +150,46 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
         for (int t = 0; t < D / 16; ++t) O[t][n] = zero4();
     }
 
-    u32x4_t gk[NST], gv[NST];
-    const int pm = tid % PER_ROW, pr = tid / PER_ROW;
+    // A lane's key rows of a tile: one (bf16) or two (fp32) per wave, in pieces of 16 bytes per block
+    u32x4_t gk[Steps::N], gv[Steps::N];
+    const int prow = Steps::group0(wave) * TileStep<T>::ROWS + TileStep<T>::row(lane);
+    const int pcol = TileStep<T>::piece(lane) * (16 / (int)sizeof(T));
     auto request = [&](int t0) {
 #pragma unroll
-        for (int i = 0; i < NST; ++i) {
-            const int idx = t0 + pr + i * ROWS;
-            gk[i] = gv[i] = u32x4_t{0, 0, 0, 0};
-            if (idx < total) {
-                const int rel = idx < nsink ? idx - s : lo + (idx - nsink);
-                const T *kp, *vp;
-                if (rel >= 0) {
-                    kp = kn + (long long)rel * a.k_stride;
-                    vp = vn + (long long)rel * a.v_stride;
-                } else {
-                    int row = idx;
-                    if (idx >= nsink) {
-                        row = base0 + rel;
-                        row = sinks + (row < 0 ? row + window : row);
-                    }
-                    kp = kc + row * crow;
-                    vp = vc + row * crow;
+        for (int j = 0; j < NG; ++j) {
+            const int idx = t0 + prow + j * TileStep<T>::ROWS;
+            const int rel = idx < nsink ? idx - s : lo + (idx - nsink);
+            const T *kp = kn + (long long)rel * a.k_stride, *vp = vn + (long long)rel * a.v_stride;
+            if (rel < 0) {
+                int row = idx;
+                if (idx >= nsink) {
+                    row = base0 + rel;
+                    row = sinks + (row < 0 ? row + window : row);
                 }
-                gk[i] = *reinterpret_cast<const u32x4_t*>(kp + pm * EPP);
-                gv[i] = *reinterpret_cast<const u32x4_t*>(vp + pm * EPP);
+                kp = kc + row * crow;
+                vp = vc + row * crow;
+            }
+#pragma unroll
+            for (int i = 0; i < Steps::NB; ++i) {
+                gk[j * Steps::NB + i] = gv[j * Steps::NB + i] = u32x4_t{0, 0, 0, 0};
+                if (idx < total) {
+                    gk[j * Steps::NB + i] = *reinterpret_cast<const u32x4_t*>(kp + pcol + 32 * i);
+                    gv[j * Steps::NB + i] = *reinterpret_cast<const u32x4_t*>(vp + pcol + 32 * i);
+                }
             }
         }
     };
+    TilePut<T, kKeys> put;
+    put.set(sK + Steps::group0(wave) * TileStep<T>::ROWS * 32, lane);
     request(0);
     const float sc = a.scale * kLog2e;
 
     for (int t0 = 0; t0 < total; t0 += kKeys) {
 #pragma unroll
-        for (int i = 0; i < NST; ++i) {
-            const int row = pr + i * ROWS;
-            tile_put(sK + row * D, pm, row & 15, gk[i]);
-            tile_put(sV + row * D, pm, row & 15, gv[i]);
+        for (int i = 0; i < Steps::N; ++i) {
+            const int at = (Steps::block(i) * kKeys + Steps::group(i) * TileStep<T>::ROWS) * 32;
+            put.put(at, gk[i]);
+            put.put(at + kKeys * D, gv[i]);
         }
         __syncthreads();
         if (t0 + kKeys < total) request(t0 + kKeys);
@@ -207,7 +206,7 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt) {
                 Frag<T> fk;
-                tile_row_frag<T, D>(fk, sK, ld, kt, kb);
+                rk.frag(fk, 0, kt, kb);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) sT[kt][n] = mma(fk, fq[n][kb], sT[kt][n]);
             }
@@ -255,14 +254,14 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
 #pragma unroll
                 for (int j = 0; j < 4; ++j) O[t][n][j] *= al;
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) acc_pair_frag<T>(fp[kb][n], sT[2 * kb][n], sT[2 * kb + 1][n], true);
+            for (int kb = 0; kb < 2; ++kb) acc_pair_frag<T>(fp[kb][n], sT[kb][n], sT[kb + 2][n], true);
         }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) {
                 Frag<T> fv;
-                tile_tr_frag<T, D>(fv, sV, ld, t, kb, lane);
+                cv.frag(fv, 0, t, kb);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) O[t][n] = mma(fv, fp[kb][n], O[t][n]);
             }
@@ -326,7 +325,8 @@ template <int D, typename T>
 __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a) {
     constexpr int TK = 32;                                     // rows per tile
     constexpr int PER_ROW = D * (int)sizeof(T) / 16, EPP = 16 / (int)sizeof(T);
-    constexpr int NST = TK * PER_ROW / 64, ROWS = 64 / PER_ROW;
+    typedef TileSteps<T, TK, D, 1> Steps;
+    constexpr int NG = Steps::N / Steps::NB;                   // row groups per tile
     constexpr int OP = D + 4;                                  // pitch of the partial outputs
     constexpr int REGION = TK * D * (int)sizeof(T) > 16 * OP * 4 ? TK * D * (int)sizeof(T) : 16 * OP * 4;
     __shared__ __attribute__((aligned(16))) char sV_[4][REGION];
@@ -354,9 +354,11 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
-    TileLane<T, D> ld;
-    ld.set(lane);
     KDA_LDS T* sV = (KDA_LDS T*)(KDA_LDS char*)sV_[wave];
+    TileCols<T, TK> cv;
+    cv.set(sV, lane);
+    TilePut<T, TK> put;
+    put.set(sV, lane);
 
     const T* kn = reinterpret_cast<const T*>(a.k) + b * a.k_stride + (long long)hk * D;
     const T* vn = reinterpret_cast<const T*>(a.v) + b * a.v_stride + (long long)hk * D;
@@ -389,13 +391,13 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
     for (int t0 = k0 + TK * wave; t0 < k1; t0 += 4 * TK) {
         // rows past the filled ones stand for the new token and are masked: never read memory that no
         // token has written
-        u32x4_t gv[NST];
-        const int pm = lane % PER_ROW, pr = lane / PER_ROW;
+        u32x4_t gv[Steps::N];
 #pragma unroll
-        for (int i = 0; i < NST; ++i) {
-            const int row = t0 + pr + i * ROWS;
-            const T* vp = row >= k1 || row == fresh ? vn : vc + row * crow;
-            gv[i] = *reinterpret_cast<const u32x4_t*>(vp + pm * EPP);
+        for (int j = 0; j < NG; ++j) {
+            const int row = t0 + j * TileStep<T>::ROWS + TileStep<T>::row(lane);
+            const T* vp = (row >= k1 || row == fresh ? vn : vc + row * crow) + TileStep<T>::piece(lane) * EPP;
+#pragma unroll
+            for (int i = 0; i < Steps::NB; ++i) gv[j * Steps::NB + i] = *reinterpret_cast<const u32x4_t*>(vp + 32 * i);
         }
         f32x4_t sT[2];
 #pragma unroll
@@ -410,10 +412,7 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
             for (int kb = 0; kb < D / 32; ++kb) sT[kt] = mma(fk[kb], fq[kb], sT[kt]);
         }
 #pragma unroll
-        for (int i = 0; i < NST; ++i) {
-            const int row = pr + i * ROWS;
-            tile_put(sV + row * D, pm, row & 15, gv[i]);
-        }
+        for (int i = 0; i < Steps::N; ++i) put.put((Steps::block(i) * TK + Steps::group(i) * TileStep<T>::ROWS) * 32, gv[i]);
         float mx = -INFINITY;
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
@@ -440,7 +439,7 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) {
             Frag<T> fv;
-            tile_tr_frag<T, D>(fv, sV, ld, t, 0, lane);
+            cv.frag(fv, 0, t, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) O[t][j] *= al;
             O[t] = mma(fv, fp, O[t]);
