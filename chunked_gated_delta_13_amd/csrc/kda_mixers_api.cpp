@@ -96,14 +96,15 @@ kda_status_t check_ssm_shape(int rows_b, int T, int H, int G, int n, int p, kda_
 }
 
 // Segments of seg_in tokens (whole chunks), or chosen here (seg_in 0): enough of them that every
-// compute unit has two workgroups (one for fp32, whose tiles fill the LDS), each at least two chunks.
-kda_status_t ssm_plan(int B, int T, int H, kda_dtype_t dt, int seg_in, long long* seg_len, int* n_seg) {
+// compute unit has two workgroups (one where its tiles fill the LDS: fp32, or p = 128), each at least two
+// chunks.
+kda_status_t ssm_plan(int B, int T, int H, int p, kda_dtype_t dt, int seg_in, long long* seg_len, int* n_seg) {
     if (seg_in < 0 || seg_in % kSsmChunk != 0) return KDA_ERR_INVALID_ARGUMENT;
     const long long chunks = ((long long)T + kSsmChunk - 1) / kSsmChunk;
     const long long units = (long long)B * H;
     long long per = seg_in > 0 ? seg_in / kSsmChunk : chunks;
     if (seg_in == 0 && units > 0) {
-        const long long want = (long long)cu_count() * (dt == KDA_F32 ? 1 : 2) / units;
+        const long long want = (long long)cu_count() * (dt == KDA_F32 || p == 128 ? 1 : 2) / units;
         if (want >= 2) per = (chunks + want - 1) / want;
         if (per < 2) per = 2;
     }
@@ -152,6 +153,11 @@ kda_status_t check_ssm_ptrs(const SsmPtrs& q, const float* S_in, const void* y, 
         !wide_rows_ok(q.Cm, rows, (long long)G * n, q.c_stride, esz) ||
         (q.z && !wide_rows_ok(q.z, rows, (long long)H * p, q.z_stride, esz)) || !stride_ok(rows, H, q.dt_stride))
         return KDA_ERR_INVALID_ARGUMENT;
+    // offsets inside a chunk are 32-bit: 64 rows of at most 2^22 elements
+    const long long widest = 1LL << 22;
+    if ((long long)H * p > widest || (rows > 1 && (q.x_stride > widest || q.b_stride > widest || q.c_stride > widest ||
+                                                   q.dt_stride > widest || (q.z && q.z_stride > widest))))
+        return KDA_ERR_UNSUPPORTED;
     if (!aligned(q.dt, esz) || !aligned(q.A, 4) || !aligned(q.D, 4) || !aligned(q.dt_bias, 4) || !aligned(q.lens, 4) ||
         !aligned(y, 16) || !aligned(S_in, 16) || !aligned(S_out, 16))
         return KDA_ERR_INVALID_ARGUMENT;
@@ -343,7 +349,7 @@ kda_status_t kda_conv_step(const void* x, const void* w, const void* bias, void*
 size_t kda_ssm_prefill_workspace_bytes(int B, int T, int H, int G, int n, int p, kda_dtype_t dt, int seg_len) {
     long long sl = 0;
     int ns = 1;
-    if (check_ssm_shape(B, T, H, G, n, p, dt) != KDA_OK || ssm_plan(B, T, H, dt, seg_len, &sl, &ns) != KDA_OK) return 0;
+    if (check_ssm_shape(B, T, H, G, n, p, dt) != KDA_OK || ssm_plan(B, T, H, p, dt, seg_len, &sl, &ns) != KDA_OK) return 0;
     return ssm_workspace(B, H, n, p, ns);
 }
 
@@ -356,7 +362,7 @@ kda_status_t kda_ssm_prefill(const void* x, const void* dt, const float* A, cons
     if (st != KDA_OK) return st;
     long long sl = 0;
     int ns = 1;
-    st = ssm_plan(B, T, H, dtype, seg_len, &sl, &ns);
+    st = ssm_plan(B, T, H, p, dtype, seg_len, &sl, &ns);
     if (st != KDA_OK || B == 0 || H == 0) return st;
     const SsmPtrs q = {x, dt, A, Bm, Cm, D, z, dt_bias, lens, x_stride, dt_stride, b_stride, c_stride, z_stride};
     st = check_ssm_ptrs(q, S0, y, S_T, B, T, H, G, n, p, dtype);

@@ -29,7 +29,12 @@ namespace {
 constexpr int kC = 64;             // tokens per chunk
 constexpr float kDecayMin = -160;  // exponents of 2 at or below this give zero
 
-__device__ __forceinline__ float softplus_f32(float v) { return fmaxf(v, 0.0f) + log1pf(__expf(-fabsf(v))); }
+// log(1 + e^v).  With w = 1 + u rounded, log(w) u / (w - 1) is log(1 + u) to fp32 also for small u.
+__device__ __forceinline__ float softplus_f32(float v) {
+    const float u = __expf(-fabsf(v)), w = 1.0f + u;
+    const float l = w == 1.0f ? u : __logf(w) * (u * __builtin_amdgcn_rcpf(w - 1.0f));
+    return fmaxf(v, 0.0f) + l;
+}
 __device__ __forceinline__ float silu_f32(float x) { return x * __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 // Running sum over the 64 lanes of a wave.  In 64 bits: decays of neighbouring tokens are differences of
@@ -78,7 +83,7 @@ template <typename T, int WIDTH, int NW> struct Stage {
     static constexpr uint32_t ES = sizeof(T);
     u32x4_t v[Steps::N];
     __device__ __forceinline__ void load(const T* base, uint32_t step, int rows, int wave, int lane) {
-        const buffer_t buf = make_buffer(base, (uint32_t)(rows - 1) * step + WIDTH * ES);
+        const buffer_t buf = make_rows(base, rows, step, WIDTH * ES);
         const uint32_t off = TileStep<T>::row(lane) * step + 16u * TileStep<T>::piece(lane);
         const uint32_t first = Steps::group0(wave) * TileStep<T>::ROWS * step + Steps::block0(wave) * 32 * ES;
 #pragma unroll
@@ -87,9 +92,9 @@ template <typename T, int WIDTH, int NW> struct Stage {
     }
     __device__ __forceinline__ void put(KDA_LDS T* tile, int wave, int lane) const {
         TilePut<T, kC> p;
-        p.set(tile + (Steps::block0(wave) * kC + Steps::group0(wave) * TileStep<T>::ROWS) * 32, lane);
+        p.set(tile + Steps::block0(wave) * kC * 32, Steps::group0(wave), lane);
 #pragma unroll
-        for (int i = 0; i < Steps::N; ++i) p.put((Steps::block(i) * kC + Steps::group(i) * TileStep<T>::ROWS) * 32, v[i]);
+        for (int i = 0; i < Steps::N; ++i) p.put(Steps::group(i), Steps::block(i), v[i]);
     }
 };
 
@@ -110,38 +115,276 @@ __device__ __forceinline__ int pinned_s(int x) {
     return x;
 }
 
-// Per-token numbers of one chunk: sums of the exponents (base 2, high and low part), steps, and the
-// weights of the state's update; `last` is the sum over the whole chunk.
+// Numbers of one chunk.  The state is held as 2^scale times the registers' values, so that a chunk whose
+// decay is mild costs no multiplication of the state: it is rescaled only when the exponent leaves
+// +-kScaleMax (values up to 2^(127 - kScaleMax) stay finite).
+constexpr float kScaleMax = 24.0f;
 struct ChunkDecay {
-    float hi[kC], lo[kC], dt[kC], w[kC];
+    float hi[kC];      // sum of the exponents (base 2) up to this token
+    float lo[kC];      // fp32: what `hi` leaves of that sum; bf16: hi - log2 dt
+    float dt[kC];      // (fp32)
+    float e[kC];       // factor of S^T C: 2^(sum + scale)
+    float w[kC];       // weight of the token in the state's update
+    float sum;         // of the whole chunk
+    float factor;      // the state's factor before the update, 1 when `rescale` is 0
+    float scale;       // the state's exponent after the chunk
+    int rescale;
 };
 
-__device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bool live, float A2, int lane) {
+// By one wave, lane = token; `scale` is the state's exponent before the chunk and after it.
+template <typename T>
+__device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bool live, float A2, float& scale, int lane) {
     const float d = live ? softplus_f32(raw) : 0.0f;
     const double s = wave_prefix(live ? (double)fmaxf(d * A2, kDecayMin) : 0.0, lane);
-    const double end = __shfl(s, 63);
-    const float hi = (float)s;
+    const float end = (float)__shfl(s, 63), hi = (float)s;
+    const float next = scale + end;
+    const bool rescale = fabsf(next) > kScaleMax;
     c->hi[lane] = hi;
-    c->lo[lane] = (float)(s - (double)hi);
-    c->dt[lane] = d;
-    c->w[lane] = fast_exp2((float)(end - s)) * d;
+    if constexpr (sizeof(T) == 4) {
+        c->lo[lane] = (float)(s - (double)hi);
+        c->dt[lane] = d;
+    } else {
+        // 2^(c_i - c_j) dt_j as one exponential; dt = 0 gives +inf here and a factor of 0
+        c->lo[lane] = hi - __log2f(d);
+    }
+    c->e[lane] = fast_exp2(hi + scale);
+    // 2^(end - s), over 2^next unless the state is brought to the exponent 0
+    c->w[lane] = fast_exp2((float)((rescale ? (double)end : -(double)scale) - s)) * d;
+    if (lane == 0) {
+        c->sum = end;
+        c->factor = rescale ? fast_exp2(next) : 1.0f;
+        c->scale = rescale ? 0.0f : next;
+        c->rescale = rescale ? 1 : 0;
+    }
+    scale = rescale ? 0.0f : next;
 }
+
+// A lane's place in the tiles of one workgroup, and the three parts of a chunk's work.  N x P state, NW
+// waves of P / NW columns each.  LDS tiles have kC rows.
+template <int N, int P, typename T, int NW> struct Mixer {
+    static constexpr int WC = P / NW, NCT = WC / 16, NT = N / 16, NP = Parts<T>::n;
+    typedef typename Vec4<T>::type vec4;
+    typedef f32x4_t State[NT][NCT];
+    TileRows<T, kC, N> rb, rc;    // rows of B and of C
+    TileCols<T, kC> cb;           // columns of B
+    TileRows<T, kC, kC> rm;       // rows of M
+    TileCols<T, kC> cx[NCT];      // this wave's column tiles of x
+    KDA_LDS T* xrow[NCT];         // its four columns of row r of x
+
+    __device__ __forceinline__ void set_bc(KDA_LDS T* sB, KDA_LDS T* sC, int lane) {
+        rb.set(sB, lane);
+        rc.set(sC, lane);
+    }
+    __device__ __forceinline__ void set_x(KDA_LDS T* sX, int wave, int lane) {
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            cx[ct].set_tile(sX, lane, wave * NCT + ct);
+            xrow[ct] = lds_pin(sX + tile_at<T, kC>(lane & 15, 4 * (wave * NCT + ct) + (lane >> 4)));
+        }
+    }
+
+    // M[i][j] = e^{c_i - c_j} dt_j (C_i . B_j) for j <= i, tile pair 0 .. 9 of the ten lower 16 x 16 tiles
+    __device__ __forceinline__ void mix(KDA_LDS T* sM, const KDA_LDS ChunkDecay* cd, int pair, int lane) const {
+        const int g = lane >> 4, r = lane & 15;
+        const int ti = pair < 1 ? 0 : (pair < 3 ? 1 : (pair < 6 ? 2 : 3));
+        const int tj = pair - ti * (ti + 1) / 2;
+        Frag<T> fb[N / 32], fc[N / 32];
+#pragma unroll
+        for (int q = 0; q < N / 32; ++q) {
+            rb.frag(fb[q], 16 * 32 * tj, 0, q);
+            rc.frag(fc[q], 16 * 32 * ti, 0, q);
+        }
+        const float ci = cd->hi[16 * ti + r];
+        const f32x4_t lj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->lo + 16 * tj + 4 * g);
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4_t acc = zero4();   // acc[k]: token j = 16 tj + 4 g + k against i = 16 ti + r
+#pragma unroll
+        for (int q = 0; q < N / 32; ++q) acc = mma(fb[q], fc[q], acc);
+        float m[4];
+        if constexpr (sizeof(T) == 4) {
+            const float li = cd->lo[16 * ti + r];
+            const f32x4_t cj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->hi + 16 * tj + 4 * g);
+            const f32x4_t dj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->dt + 16 * tj + 4 * g);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m[k] = acc[k] * (fast_exp2((ci - cj[k]) + (li - lj[k])) * dj[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m[k] = acc[k] * fast_exp2(ci - lj[k]);
+        }
+        if (ti == tj) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m[k] = 4 * g + k <= r ? m[k] : 0.0f;
+        }
+        lds_store_run<4>(sM + 16 * 32 * ti + tile_at<T, kC>(r, 4 * tj + g), m);
+    }
+
+    // x of this wave's columns, transposed: contraction over tokens
+    __device__ __forceinline__ void load_x(Frag<T> (&xt)[2][NCT]) const {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) cx[ct].frag(xt[q][ct], 0, 0, q);
+    }
+
+    // y^T = (S^T C^T) e^{c_i} + x^T M^T, the skip term and the gate: columns are tokens, rows p
+    __device__ __forceinline__ void outputs(const State& S, const Frag<T> (&xt)[2][NCT], const vec4 (&zv)[4][NCT], bool gated,
+                                            float Dh, const KDA_LDS ChunkDecay* cd, buffer_t ybuf, uint32_t y_off,
+                                            uint32_t y_step, int lane) const {
+        const int r = lane & 15;
+        constexpr int Q = N / 32;
+        f32x4_t y[4][NCT];
+        Frag<T> fc[2][4], fm[4][2];
+        float e[4];
+        vec4 xv[4][NCT];
+        // operands are requested one block ahead of the products that use them
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) rc.frag(fc[0][ti], 0, ti, 0);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (q + 1 < Q) {
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) rc.frag(fc[(q + 1) & 1][ti], 0, ti, q + 1);
+            } else {
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) {
+                    e[ti] = cd->e[16 * ti + r];
+                    // token tiles 0 and 2, then 1 and 3, as far as they reach
+                    if (ti < 2) rm.frag_lo(fm[ti][0], 0, ti, 0);
+                    else rm.frag(fm[ti][0], 0, ti, 0);
+                    if (ti == 3) rm.frag(fm[ti][1], 0, ti, 1);
+                    else if (ti > 0) rm.frag_lo(fm[ti][1], 0, ti, 1);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            Frag<T> fs[NCT];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) acc_pair_frag<T>(fs[ct], S[q][ct], S[q + NT / 2][ct], true);
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) y[ti][ct] = mma(fs[ct], fc[q & 1][ti], q == 0 ? zero4() : y[ti][ct]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) xv[ti][ct] = *reinterpret_cast<const volatile KDA_LDS vec4*>(xrow[ct] + 16 * 32 * ti);
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[ti][ct][k] *= e[ti];
+                y[ti][ct] = mma(xt[0][ct], fm[ti][0], y[ti][ct]);
+                if (ti > 0) y[ti][ct] = mma(xt[1][ct], fm[ti][1], y[ti][ct]);
+            }
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                f32x4_t o;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = fmaf(Dh, to_f32<T>((T)xv[ti][ct][k]), y[ti][ct][k]);
+                if (gated) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] *= silu_f32(to_f32<T>((T)zv[ti][ct][k]));
+                }
+                vec4 ov;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ov[k] = from_f32<T>(o[k]);
+                buffer_store4(ov, ybuf, y_off, 16 * ti * y_step + 16 * ct * (uint32_t)sizeof(T));
+            }
+    }
+
+    // S <- e^{c_63} S + B^T (w x)
+    __device__ __forceinline__ void update(State& S, const Frag<T> (&xt)[2][NCT], const KDA_LDS ChunkDecay* cd, int lane) const {
+        if (cd->rescale) {
+            const float f = cd->factor;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) S[nt][ct][k] *= f;
+        }
+        // groups of NG row tiles of the state, token tiles (0, 2) then (1, 3); a group's columns of B are
+        // requested while the products of the group before run
+        constexpr int NG = NT < 4 ? NT : 4, NGR = 2 * NT / NG;
+        Frag<T> fb[2][NG], xs[NCT][NP];
+        float w[2][8];
+        load_weights(w[0], cd->w + 4 * (lane >> 4));
+        load_weights(w[1], cd->w + 16 + 4 * (lane >> 4));
+#pragma unroll
+        for (int i = 0; i < NG; ++i) cb.frag(fb[0][i], 0, i, 0);
+#pragma unroll
+        for (int j = 0; j < NGR; ++j) {
+            const int q = j / (NGR / 2), n0 = (j % (NGR / 2)) * NG;
+            if (j + 1 < NGR) {
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+                    cb.frag(fb[(j + 1) & 1][i], 0, ((j + 1) % (NGR / 2)) * NG + i, (j + 1) / (NGR / 2));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (n0 == 0) {
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) weigh(xs[ct], xt[q][ct], w[q]);
+            }
+#pragma unroll
+            for (int k = NP - 1; k >= 0; --k)
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct) S[n0 + i][ct] = mma(fb[j & 1][i], xs[ct][k], S[n0 + i][ct]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // A state in memory, p as the lane's element of row tile 0, column tile 0 (byte offset `off`).
+    __device__ __forceinline__ static uint32_t state_off(int wave, int lane) {
+        return (uint32_t)((4 * (lane >> 4) * P + wave * WC + (lane & 15)) * sizeof(float));
+    }
+    __device__ __forceinline__ static void load_state(State& S, const float* p, uint32_t off) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[nt][ct] = zero4();
+        if (p) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) S[nt][ct][k] = *at_byte(p + (16 * nt + k) * P + 16 * ct, off);
+        }
+    }
+    __device__ __forceinline__ static void store_state(const State& S, float factor, float* p, uint32_t off) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) *at_byte(p + (16 * nt + k) * P + 16 * ct, off) = S[nt][ct][k] * factor;
+    }
+};
 
 }  // namespace
 
 // OUT: with outputs (the pass that runs every segment from its entry state), else final states only.
-template <int N, int P, typename T, bool OUT, int NW>
+// AHEAD: M of the next chunk is formed beside the outputs of this one, over three sets of B and C tiles,
+// two of x and two of M: one barrier per chunk, and every wave has independent work for the matrix
+// cores, the vector unit and the LDS all through it.  It takes most of the LDS, so one workgroup runs per
+// compute unit; the plain schedule (three barriers) leaves room for two or three.
+template <int N, int P, typename T, bool OUT, int NW, bool AHEAD>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefill_kernel(const SsmArgs a) {
-    constexpr int NTH = 64 * NW;
-    constexpr int WC = P / NW;       // state columns per wave
-    constexpr int NCT = WC / 16;     // column tiles per wave
-    constexpr int NT = N / 16;       // row tiles of the state
-    constexpr int NP = Parts<T>::n;
-    typedef __attribute__((ext_vector_type(4))) T vec4;
-    // LDS: B, C, M, x tiles (elements), then the decays of two chunks
-    constexpr int oC = kC * N, oM = OUT ? 2 * kC * N : kC * N, oX = oM + (OUT ? kC * kC : 0), oEnd = oX + kC * P;
+    typedef Mixer<N, P, T, NW> Mix;
+    typedef typename Mix::vec4 vec4;
+    constexpr int WC = Mix::WC, NCT = Mix::NCT;
+    constexpr uint32_t ES = sizeof(T), ROW_P = P * ES;
+    constexpr int NBC = AHEAD ? 3 : 1, NXM = AHEAD ? 2 : 1, ND = AHEAD ? 3 : 2;
+    // LDS: B, C (with outputs), M (likewise), x tiles (elements), then the numbers of two or three chunks
+    constexpr int oC = NBC * kC * N, oM = OUT ? 2 * oC : oC, oX = oM + (OUT ? NXM * kC * kC : 0), oEnd = oX + NXM * kC * P;
     __shared__ __attribute__((aligned(16))) T smem[oEnd];
-    __shared__ __attribute__((aligned(16))) ChunkDecay sD_[2];
+    __shared__ __attribute__((aligned(16))) ChunkDecay sD_[ND];
     KDA_LDS T* sB = (KDA_LDS T*)smem;
     KDA_LDS T* sC = sB + oC;
     KDA_LDS T* sM = sB + oM;
@@ -173,20 +416,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
-    TileRows<T, kC, N> rn;    // rows of B (and of C, oC further)
-    TileCols<T, kC> cn;       // columns of B
-    TileRows<T, kC, kC> rm;   // rows of M
-    cn.set(sB, lane);
-    if constexpr (OUT) {
-        rn.set(sB, lane);
-        rm.set(sM, lane);
-    }
-    // this lane's four columns of row r of x, column tile ct of the wave
-    KDA_LDS T* xrow[NCT];
-#pragma unroll
-    for (int ct = 0; ct < NCT; ++ct) xrow[ct] = lds_pin(sX + tile_at<T, kC>(r, 4 * (wave * NCT + ct) + g));
 
-    // row t_begin of every input, and the bytes between rows
+    // the current row of every input, and the bytes between rows
     const long long row0 = (long long)b * a.T + t_begin;
     const T* xp = reinterpret_cast<const T*>(a.x) + row0 * a.x_stride + (long long)h * P;
     const T* bp = reinterpret_cast<const T*>(a.Bm) + row0 * a.b_stride + (long long)grp * N;
@@ -196,229 +427,169 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
     const bool gated = OUT && zp != nullptr;
     if (gated) zp += row0 * a.z_stride + (long long)h * P;
     T* yp = OUT ? reinterpret_cast<T*>(a.y) + (row0 * a.H + h) * P : nullptr;
-    constexpr uint32_t ES = sizeof(T), ROW_P = P * ES;
     const uint32_t x_step = (uint32_t)a.x_stride * ES, b_step = (uint32_t)a.b_stride * ES, c_step = (uint32_t)a.c_stride * ES;
-    const uint32_t z_step = (uint32_t)a.z_stride * ES, y_step = (uint32_t)a.H * ROW_P;
+    const uint32_t dt_step = (uint32_t)a.dt_stride * ES, z_step = (uint32_t)a.z_stride * ES, y_step = (uint32_t)a.H * ROW_P;
     const uint32_t z_off = r * z_step + (wave * WC + 4 * g) * ES, y_off = r * y_step + (wave * WC + 4 * g) * ES;
     const float A2 = a.A[h] * kLog2e;
     const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
     const float Dh = a.D ? a.D[h] : 0.0f;
 
     // entry state
-    f32x4_t S[NT][NCT];
+    typename Mix::State S;
+    const uint32_t s_off = Mix::state_off(wave, lane);
     const float* sin = nullptr;
     if (s == 0 && !(OUT && a.keep_S0)) {
         if (a.S0) sin = a.S0 + bh * (long long)(N * P);
     } else if (OUT) {
         sin = a.ws_state + (bh * a.n_seg + s) * (long long)(N * P);
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) S[nt][ct] = zero4();
-    // this lane's element of row tile 0, column tile 0 of a state
-    const uint32_t s_off = (uint32_t)((4 * g * P + wave * WC + r) * sizeof(float));
-    if (sin) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[nt][ct][i] = *at_byte(sin + (16 * nt + i) * P + 16 * ct, s_off);
-    }
-    if (!OUT && s == 0 && a.keep_S0) {   // S_T is S0: the other pass's last segment overwrites it
-        float* keep = a.ws_state + bh * a.n_seg * (long long)(N * P);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) *at_byte(keep + (16 * nt + i) * P + 16 * ct, s_off) = S[nt][ct][i];
-    }
-    float total = 0.0f;   // exponent (base 2) of the segment's decay
+    Mix::load_state(S, sin, s_off);
+    // S_T is S0: the other pass's last segment overwrites it
+    if (!OUT && s == 0 && a.keep_S0) Mix::store_state(S, 1.0f, a.ws_state + bh * a.n_seg * (long long)(N * P), s_off);
 
-    // Inputs are requested one chunk ahead, the raw steps (last wave) two chunks ahead: their running sum
-    // is a long chain, formed while the other waves work on M.
+    float total = 0.0f;   // exponent (base 2) of the segment's decay
+    float final_scale = 0.0f;
+    Mix mx;
+    // Rows of B, C and x are requested into registers a chunk or more before they are put into their
+    // tiles; the raw steps (one wave) a chunk before their sums, a long chain that this wave forms while
+    // others work on M.  Requests past the end name empty buffers instead of being skipped: straight code
+    // lets every wait count the requests behind it.
     Stage<T, P, NW> gx;
     Stage<T, N, NW> gb, gc;
-    float gdt = 0.0f;
-    // tokens left in the segment (32 bits: at most seg_len)
-    int left = (int)(t_end - t_begin);
-    auto request = [&](int rows) {   // the chunk at xp, bp, cp
-        gx.load(xp, x_step, rows, wave, lane);
-        gb.load(bp, b_step, rows, wave, lane);
-        if constexpr (OUT) gc.load(cp, c_step, rows, wave, lane);
+    float gdt = 0.0f, scale = 0.0f;
+    int left = (int)(t_end - t_begin);   // tokens left, from the chunk at hand on
+    auto rows_at = [&](int ahead) { return left - ahead < kC ? left - ahead : kC; };
+    auto request_bc = [&](int ahead) {   // the chunk `ahead` tokens from the one at hand
+        gb.load(bp + ahead * a.b_stride, b_step, rows_at(ahead), wave, lane);
+        if constexpr (OUT) gc.load(cp + ahead * a.c_stride, c_step, rows_at(ahead), wave, lane);
     };
+    auto put_bc = [&](int buf) {
+        gb.put(sB + buf * kC * N, wave, lane);
+        if constexpr (OUT) gc.put(sC + buf * kC * N, wave, lane);
+    };
+    auto request_x = [&](int ahead) { gx.load(xp + ahead * a.x_stride, x_step, rows_at(ahead), wave, lane); };
     auto request_dt = [&](int ahead) {
-        const int t = ahead + lane < left ? ahead + lane : left - 1;
-        gdt = to_f32<T>(dp[t * a.dt_stride]);
+        gdt = buffer_load1(dp, make_rows(dp + ahead * a.dt_stride, rows_at(ahead), dt_step, ES), lane * dt_step);
     };
-    if (left > 0) {
-        if (wave == NW - 1) {
+    auto decay = [&](int ahead, int buf) { chunk_decay<T>(sD + buf, gdt + bias, ahead + lane < left, A2, scale, lane); };
+    vec4 zv[4][NCT];
+    auto request_z = [&](int ahead) {
+        const buffer_t zbuf = make_rows(zp + ahead * a.z_stride, gated ? rows_at(ahead) : 0, z_step, ROW_P);
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) buffer_load4(zv[ti][ct], zbuf, z_off, 16 * ti * z_step + 16 * ct * ES);
+    };
+    auto y_buffer = [&]() { return make_rows(yp, rows_at(0), y_step, ROW_P); };
+    auto advance = [&]() {
+        xp += kC * a.x_stride;
+        bp += kC * a.b_stride;
+        cp += kC * a.c_stride;
+        dp += kC * a.dt_stride;
+        if (gated) zp += kC * a.z_stride;
+        if constexpr (OUT) yp += (long long)kC * a.H * P;
+        left -= kC;
+    };
+    // Waves that form M, the last of them the decays too.  Of two waves on a SIMD the older one is served
+    // first and has time left at the barrier: with all eight sharing this work, waves 0 - 3 waited 3000 of
+    // 9300 cycles a chunk for waves 4 - 7.
+    constexpr int MW = AHEAD ? NW / 2 : NW;
+
+    if constexpr (!AHEAD) {
+        mx.set_bc(sB, sC, lane);
+        mx.cb.set(sB, lane);
+        mx.rm.set(sM, lane);
+        mx.set_x(sX, wave, lane);
+        if (left > 0) {
+            if (wave == MW - 1) {
+                request_dt(0);
+                decay(0, 0);
+                request_dt(kC);
+            }
+            request_bc(0);
+            request_x(0);
+        }
+        for (int par = 0; left > 0; par ^= 1) {
+            const KDA_LDS ChunkDecay* cd = sD + par;
+            put_bc(0);
+            gx.put(sX, wave, lane);
+            __syncthreads();
+            if constexpr (OUT) {
+                request_z(0);
+                // (the pair is taken as new in every chunk: its addresses are not worth registers)
+                for (int pair = pinned_s(wave); pair < 10; pair += MW) mx.mix(sM, cd, pair, lane);
+            }
+            if (wave == MW - 1) {
+                decay(kC, par ^ 1);
+                request_dt(2 * kC);
+            }
+            if constexpr (OUT) __syncthreads();
+            Frag<T> xt[2][NCT];
+            mx.load_x(xt);
+            if constexpr (OUT) mx.outputs(S, xt, zv, gated, Dh, cd, y_buffer(), y_off, y_step, lane);
+            // requested here, where the outputs' registers are free again
+            request_bc(kC);
+            request_x(kC);
+            mx.update(S, xt, cd, lane);
+            total += cd->sum;
+            final_scale = cd->scale;
+            __syncthreads();
+            advance();
+        }
+    } else if (left > 0) {
+        // chunks 0 and 1 of B and C, chunk 0 of x, M of chunk 0
+        request_bc(0);
+        request_x(0);
+        if (wave == MW - 1) {
             request_dt(0);
-            chunk_decay(sD, gdt + bias, lane < left, A2, lane);
+            decay(0, 0);
             request_dt(kC);
-        }
-        request(left < kC ? left : kC);
-    }
-
-    // columns 16 (wave NCT + ct) .. of x, transposed (the tile index is the wave's: addresses of its own)
-    TileCols<T, kC> cx[NCT];
-#pragma unroll
-    for (int ct = 0; ct < NCT; ++ct) cx[ct].set_tile(sX, lane, wave * NCT + ct);
-    auto cx_frag = [&](Frag<T>& f, int ct, int kb) { cx[ct].frag(f, 0, 0, kb); };
-
-    for (int par = 0; left > 0; left -= kC, par ^= 1) {
-        const int rows = left < kC ? left : kC;
-        const KDA_LDS ChunkDecay* cd = sD + par;
-        gx.put(sX, wave, lane);
-        gb.put(sB, wave, lane);
-        if constexpr (OUT) gc.put(sC, wave, lane);
-        __syncthreads();
-        vec4 zv[4][NCT];
-        if (gated) {
-            const buffer_t zbuf = make_buffer(zp, (uint32_t)(rows - 1) * z_step + ROW_P);
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) buffer_load4(zv[ti][ct], zbuf, z_off, 16 * ti * z_step + 16 * ct * ES);
-            zp += kC * a.z_stride;
-        }
-        if constexpr (OUT) {
-            // M[i][j] = e^{c_i - c_j} dt_j (C_i . B_j) for j <= i: the ten lower 16 x 16 tiles
-            // (the pair is taken as new in every chunk: its addresses are not worth registers)
-            for (int pair = pinned_s(wave); pair < 10; pair += NW) {
-                {
-                    const int ti = pair < 1 ? 0 : (pair < 3 ? 1 : (pair < 6 ? 2 : 3));
-                    const int tj = pair - ti * (ti + 1) / 2;
-                    f32x4_t acc = zero4();
-#pragma unroll
-                    for (int kb = 0; kb < N / 32; ++kb) {
-                        Frag<T> fb, fc;
-                        rn.frag(fb, 16 * 32 * tj, 0, kb);
-                        rn.frag(fc, oC + 16 * 32 * ti, 0, kb);
-                        acc = mma(fb, fc, acc);   // acc[q]: token j = 16 tj + 4 g + q against i = 16 ti + r
-                    }
-                    const float ci = cd->hi[16 * ti + r], cil = cd->lo[16 * ti + r];
-                    const f32x4_t cj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->hi + 16 * tj + 4 * g);
-                    const f32x4_t cjl = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->lo + 16 * tj + 4 * g);
-                    const f32x4_t dj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->dt + 16 * tj + 4 * g);
-                    float m[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float v = acc[q] * (fast_exp2((ci - cj[q]) + (cil - cjl[q])) * dj[q]);
-                        m[q] = tj < ti || 4 * g + q <= r ? v : 0.0f;
-                    }
-                    lds_store_run<4>(sM + 16 * 32 * ti + tile_at<T, kC>(r, 4 * tj + g), m);
-                }
-            }
-        }
-        if (left > kC && wave == NW - 1) {
-            chunk_decay(sD + (par ^ 1), gdt + bias, kC + lane < left, A2, lane);
+            decay(kC, 1);
             request_dt(2 * kC);
-            dp += kC * a.dt_stride;
         }
-        if constexpr (OUT) __syncthreads();
-
-        // x of this wave's columns, transposed: contraction over tokens
-        Frag<T> xt[2][NCT];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) cx_frag(xt[kb][ct], ct, kb);
-
-        if constexpr (OUT) {
-            // y^T = (S^T C^T) e^{c_i} + x^T M^T: columns are tokens, rows p
-            f32x4_t y[4][NCT];
-            const buffer_t ybuf = make_buffer(yp, (uint32_t)(rows - 1) * y_step + ROW_P);
-            yp += (long long)kC * a.H * P;
-#pragma unroll
-            for (int kb = 0; kb < N / 32; ++kb) {
-                Frag<T> fs[NCT];
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) acc_pair_frag<T>(fs[ct], S[kb][ct], S[kb + NT / 2][ct], true);
-#pragma unroll
-                for (int ti = 0; ti < 4; ++ti) {
-                    Frag<T> fc;
-                    rn.frag(fc, oC, ti, kb);
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) y[ti][ct] = mma(fs[ct], fc, kb == 0 ? zero4() : y[ti][ct]);
-                }
-            }
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti) {
-                __builtin_amdgcn_sched_barrier(0);
-                const float e = fast_exp2(cd->hi[16 * ti + r]);
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) y[ti][ct][q] *= e;
-#pragma unroll
-                for (int kb = 0; kb < (ti < 1 ? 1 : 2); ++kb) {   // token tiles kb and kb + 2, as far as they reach
-                    Frag<T> fm;
-                    if (kb + 2 > ti) rm.frag_lo(fm, 0, ti, kb);
-                    else rm.frag(fm, 0, ti, kb);
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) y[ti][ct] = mma(xt[kb][ct], fm, y[ti][ct]);
-                }
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    const vec4 xv = *reinterpret_cast<const KDA_LDS vec4*>(xrow[ct] + 16 * 32 * ti);
-                    f32x4_t o;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) o[q] = fmaf(Dh, to_f32<T>((T)xv[q]), y[ti][ct][q]);
-                    if (gated) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) o[q] *= silu_f32(to_f32<T>((T)zv[ti][ct][q]));
-                    }
-                    vec4 ov;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) ov[q] = from_f32<T>(o[q]);
-                    buffer_store4(ov, ybuf, y_off, 16 * ti * y_step + 16 * ct * ES);
-                }
-            }
-        }
-
-        // the next chunk's rows are requested here, where the outputs' registers are free again
-        if (left > kC) {
-            xp += kC * a.x_stride;
-            bp += kC * a.b_stride;
-            cp += kC * a.c_stride;
-            request(left - kC < kC ? left - kC : kC);
-        }
-
-        // S <- e^{c_63} S + B^T (w x)
-        __builtin_amdgcn_sched_barrier(0);
-        {
-            const float cl = cd->hi[kC - 1];
-            const float eL = fast_exp2(cl);
-            total += cl;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) S[nt][ct][q] *= eL;
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                __builtin_amdgcn_sched_barrier(0);
-                float w[8];
-                load_weights(w, cd->w + 16 * kb + 4 * g);
-                Frag<T> xs[NCT][NP];
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) weigh(xs[ct], xt[kb][ct], w);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    Frag<T> fb;
-                    cn.frag(fb, 0, nt, kb);
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                        for (int q = NP - 1; q >= 0; --q) S[nt][ct] = mma(fb, xs[ct][q], S[nt][ct]);
-                }
-            }
-        }
+        put_bc(0);
+        gx.put(sX, wave, lane);
+        request_bc(kC);
+        request_x(kC);
+        put_bc(1);
         __syncthreads();
+        mx.set_bc(sB, sC, lane);
+        for (int pair = wave; pair < 10; pair += NW) mx.mix(sM, sD, pair, lane);
+        request_bc(2 * kC);
+        request_z(0);
+        __syncthreads();
+        int c3 = 0, n3 = 1, f3 = 2;   // tiles of this chunk, the next one, and the one after it
+        for (int par = 0; left > 0; par ^= 1) {
+            const KDA_LDS ChunkDecay* cd = sD + c3;
+            put_bc(f3);
+            gx.put(sX + (par ^ 1) * kC * P, wave, lane);
+            request_bc(3 * kC);
+            request_x(2 * kC);
+            mx.rc.set(sC + c3 * kC * N, lane);
+            mx.cb.set(sB + c3 * kC * N, lane);
+            mx.rm.set(sM + par * kC * kC, lane);
+            mx.set_x(sX + par * kC * P, wave, lane);
+            Frag<T> xt[2][NCT];
+            mx.load_x(xt);
+            mx.outputs(S, xt, zv, gated, Dh, cd, y_buffer(), y_off, y_step, lane);
+            request_z(kC);
+            mx.update(S, xt, cd, lane);
+            total += cd->sum;
+            final_scale = cd->scale;
+            mx.set_bc(sB + n3 * kC * N, sC + n3 * kC * N, lane);
+            if (wave < MW)
+                for (int pair = pinned_s(wave); pair < 10; pair += MW) mx.mix(sM + (par ^ 1) * kC * kC, sD + n3, pair, lane);
+            if (wave == MW - 1) {
+                decay(2 * kC, f3);
+                request_dt(3 * kC);
+            }
+            __syncthreads();
+            advance();
+            const int t3 = c3;
+            c3 = n3;
+            n3 = f3;
+            f3 = t3;
+        }
     }
 
     float* so = nullptr;
@@ -428,14 +599,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
         so = a.ws_state + (bh * a.n_seg + s + 1) * (long long)(N * P);
         if (tid == 0) a.ws_decay[bh * a.n_seg + s + 1] = total;
     }
-    if (so) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) *at_byte(so + (16 * nt + i) * P + 16 * ct, s_off) = S[nt][ct][i];
-    }
+    if (so) Mix::store_state(S, fast_exp2(final_scale), so, s_off);
 }
 
 // Entry states from the segments' final states, in place: slot s + 1 holds the final state of segment s
@@ -528,11 +692,12 @@ namespace {
 template <int N, int P, typename T>
 hipError_t ssm_launch(SsmPass pass, SsmArgs a, hipStream_t s) {
     constexpr int NW = P / 16;
+    constexpr bool AHEAD = P == 128 && sizeof(T) == 2;
     a.per_xcd = (a.n_units + 7) / 8;
     const dim3 grid((unsigned)(8 * a.per_xcd));
     switch (pass) {
-        case SsmPass::kStates: kda_ssm_prefill_kernel<N, P, T, false, NW><<<grid, 64 * NW, 0, s>>>(a); break;
-        case SsmPass::kOutputs: kda_ssm_prefill_kernel<N, P, T, true, NW><<<grid, 64 * NW, 0, s>>>(a); break;
+        case SsmPass::kStates: kda_ssm_prefill_kernel<N, P, T, false, NW, false><<<grid, 64 * NW, 0, s>>>(a); break;
+        case SsmPass::kOutputs: kda_ssm_prefill_kernel<N, P, T, true, NW, AHEAD><<<grid, 64 * NW, 0, s>>>(a); break;
         case SsmPass::kToken: kda_ssm_step_kernel<N, P, T><<<grid, 4 * P, 0, s>>>(a); break;
     }
     return hipGetLastError();

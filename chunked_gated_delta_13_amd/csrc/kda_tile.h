@@ -1,9 +1,11 @@
 // LDS tiles shared by the state space scan and the window attention (gfx950, wave64).
 //
 // A tile of ROWS rows is stored in blocks of 32 columns, row after row inside a block, in chunks of four
-// elements (8 bytes of bf16, 16 of fp32).  Chunk c of row r lies at place c ^ f(r) of its 8: f is chosen
-// so that the 16 (bf16) or 8 (fp32) rows that one cycle of a row read takes, and the four rows by four
-// chunks of one transposed read, fall on different banks without padding.
+// elements (8 bytes of bf16, 16 of fp32).  Chunk c of row r lies at place c ^ f(r) of its 8.  One cycle
+// reads 256 bytes from 64 banks (measured with the bank conflict counter): f spreads the 16 rows by two
+// chunks (bf16) or the 16 rows of one chunk (fp32) that a cycle of a row read takes, and the eight rows
+// by four chunks of a transposed read of bf16, over all banks without padding.  f is even for bf16, so 16
+// bytes of a row stay together.
 //
 // A matrix operand's 32 contraction slots are two stacked 16-wide tiles, as in kda_device.h, but tiles
 // half the contraction apart instead of neighbours: (a, a + n/2).  Both halves then lie a constant
@@ -18,8 +20,8 @@ namespace kda {
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 
 template <typename T> __device__ __forceinline__ int tile_f(int r);
-template <> __device__ __forceinline__ int tile_f<__bf16>(int r) { return ((r & 2) << 1) | ((r >> 2) & 3); }
-template <> __device__ __forceinline__ int tile_f<float>(int r) { return r & 7; }
+template <> __device__ __forceinline__ int tile_f<__bf16>(int r) { return (r & 4) | ((r >> 2) & 2); }
+template <> __device__ __forceinline__ int tile_f<float>(int r) { return (r >> 1) & 7; }
 
 // Four elements as one vector.
 template <typename T> struct Vec4 { typedef bf16x4_t type; };
@@ -62,8 +64,8 @@ template <typename T, int ROWS, int WIDTH> struct TileRows {
     // rows 16 a .. 16 a + 15, contraction block q: columns of tiles q and q + WIDTH/32
     __device__ __forceinline__ void frag(Frag<T>& f, int delta, int a, int q) const {
         const KDA_LDS T* p = at[q & 1] + delta + 16 * 32 * a + (q >> 1) * (ROWS * 32);
-        frag_join(f, *reinterpret_cast<const KDA_LDS vec4*>(p),
-                  *reinterpret_cast<const KDA_LDS vec4*>(p + (WIDTH / 64) * (ROWS * 32)));
+        frag_join(f, *reinterpret_cast<const volatile KDA_LDS vec4*>(p),
+                  *reinterpret_cast<const volatile KDA_LDS vec4*>(p + (WIDTH / 64) * (ROWS * 32)));
     }
     // the first tile of the block, the second one zero
     __device__ __forceinline__ void frag_lo(Frag<T>& f, int delta, int a, int q) const {
@@ -122,41 +124,27 @@ template <int ROWS> struct TileCols<float, ROWS> {
 };
 
 // How a wave moves rows into a tile: one step is 16 bytes per lane, 16 rows (bf16) or 8 rows (fp32) of
-// one block of 32 columns.  The lanes' rows are ordered so that a step's stores fall on different banks.
-template <typename T> struct TileStep;
-template <> struct TileStep<__bf16> {
-    static constexpr int ROWS = 16;
-    static __device__ __forceinline__ int row(int lane) {
-        return ((lane >> 2) & 1) | ((lane >> 3) & 2) | ((lane >> 1) & 4) | ((lane >> 2) & 8);
-    }
-    static __device__ __forceinline__ int piece(int lane) { return lane & 3; }
-};
-template <> struct TileStep<float> {
-    static constexpr int ROWS = 8;
-    static __device__ __forceinline__ int row(int lane) { return lane >> 3; }
-    static __device__ __forceinline__ int piece(int lane) { return lane & 7; }
+// one block of 32 columns.
+template <typename T> struct TileStep {
+    static constexpr int PIECES = 2 * (int)sizeof(T), ROWS = 64 / PIECES, ELEMS = 16 / (int)sizeof(T);
+    static __device__ __forceinline__ int row(int lane) { return lane / PIECES; }
+    static __device__ __forceinline__ int piece(int lane) { return lane % PIECES; }
 };
 
-// A lane's place for its step: the two chunks of 8 bf16, or the one of 4 fp32.
-template <typename T, int ROWS> struct TilePut;
-template <int ROWS> struct TilePut<__bf16, ROWS> {
-    KDA_LDS __bf16 *lo, *hi;
-    __device__ __forceinline__ void set(KDA_LDS __bf16* tile, int lane) {
-        const int r = TileStep<__bf16>::row(lane), m = TileStep<__bf16>::piece(lane);
-        lo = lds_pin(tile + tile_at<__bf16, ROWS>(r, 2 * m));
-        hi = lds_pin(tile + tile_at<__bf16, ROWS>(r, 2 * m + 1));
+// A lane's places for its steps from row group `group0` on (places repeat every 16 rows).
+template <typename T, int ROWS> struct TilePut {
+    typedef TileStep<T> S;
+    static constexpr int PER16 = 16 / S::ROWS;
+    KDA_LDS T* at[PER16];
+    __device__ __forceinline__ void set(KDA_LDS T* tile, int group0, int lane) {
+#pragma unroll
+        for (int x = 0; x < PER16; ++x)
+            at[x] = lds_pin(tile + tile_at<T, ROWS>((group0 + x) * S::ROWS + S::row(lane), S::piece(lane) * (S::ELEMS / 4)));
     }
-    __device__ __forceinline__ void put(int delta, u32x4_t v) const {
-        *reinterpret_cast<KDA_LDS u32x2_t*>(lo + delta) = u32x2_t{v[0], v[1]};
-        *reinterpret_cast<KDA_LDS u32x2_t*>(hi + delta) = u32x2_t{v[2], v[3]};
+    // `group` row groups and `block` blocks further (constants)
+    __device__ __forceinline__ void put(int group, int block, u32x4_t v) const {
+        *reinterpret_cast<KDA_LDS u32x4_t*>(at[group % PER16] + (group / PER16) * 16 * 32 + block * ROWS * 32) = v;
     }
-};
-template <int ROWS> struct TilePut<float, ROWS> {
-    KDA_LDS float* at;
-    __device__ __forceinline__ void set(KDA_LDS float* tile, int lane) {
-        at = lds_pin(tile + tile_at<float, ROWS>(TileStep<float>::row(lane), TileStep<float>::piece(lane)));
-    }
-    __device__ __forceinline__ void put(int delta, u32x4_t v) const { *reinterpret_cast<KDA_LDS u32x4_t*>(at + delta) = v; }
 };
 
 // The steps of NW waves over a tile of ROWS x WIDTH: a wave's steps i = 0 .. N - 1 cover blocks of 32
@@ -177,6 +165,10 @@ typedef __amdgpu_buffer_rsrc_t buffer_t;
 __device__ __forceinline__ buffer_t make_buffer(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
+// `rows` rows of `width` bytes that start `step` bytes apart; no rows give an empty buffer.
+__device__ __forceinline__ buffer_t make_rows(const void* p, int rows, uint32_t step, uint32_t width) {
+    return make_buffer(p, rows > 0 ? (uint32_t)(rows - 1) * step + width : 0u);
+}
 __device__ __forceinline__ u32x4_t buffer_load16(buffer_t b, uint32_t lane_off, uint32_t off) {
     return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane_off, (int)off, 0));
 }
@@ -188,6 +180,14 @@ __device__ __forceinline__ void buffer_store16(buffer_t b, uint32_t lane_off, ui
 }
 __device__ __forceinline__ void buffer_store8(buffer_t b, uint32_t lane_off, uint32_t off, u32x2_t v) {
     __builtin_amdgcn_raw_buffer_store_b64(v, b, (int)lane_off, (int)off, 0);
+}
+// One element, widened.
+__device__ __forceinline__ float buffer_load1(const __bf16*, buffer_t b, uint32_t lane_off) {
+    const unsigned short u = __builtin_amdgcn_raw_buffer_load_b16(b, (int)lane_off, 0, 0);
+    return __uint_as_float((uint32_t)u << 16);
+}
+__device__ __forceinline__ float buffer_load1(const float*, buffer_t b, uint32_t lane_off) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (int)lane_off, 0, 0));
 }
 // Four elements.
 __device__ __forceinline__ void buffer_load4(bf16x4_t& v, buffer_t b, uint32_t lane_off, uint32_t off) {

@@ -179,17 +179,16 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
             }
         }
     };
-    TilePut<T, kKeys> put;
-    put.set(sK + Steps::group0(wave) * TileStep<T>::ROWS * 32, lane);
+    TilePut<T, kKeys> put;   // (values lie kKeys * D elements, D / 32 blocks, behind keys)
+    put.set(sK, Steps::group0(wave), lane);
     request(0);
     const float sc = a.scale * kLog2e;
 
     for (int t0 = 0; t0 < total; t0 += kKeys) {
 #pragma unroll
         for (int i = 0; i < Steps::N; ++i) {
-            const int at = (Steps::block(i) * kKeys + Steps::group(i) * TileStep<T>::ROWS) * 32;
-            put.put(at, gk[i]);
-            put.put(at + kKeys * D, gv[i]);
+            put.put(Steps::group(i), Steps::block(i), gk[i]);
+            put.put(Steps::group(i), Steps::block(i) + Steps::NB, gv[i]);
         }
         __syncthreads();
         if (t0 + kKeys < total) request(t0 + kKeys);
@@ -358,7 +357,7 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
     TileCols<T, TK> cv;
     cv.set(sV, lane);
     TilePut<T, TK> put;
-    put.set(sV, lane);
+    put.set(sV, 0, lane);
 
     const T* kn = reinterpret_cast<const T*>(a.k) + b * a.k_stride + (long long)hk * D;
     const T* vn = reinterpret_cast<const T*>(a.v) + b * a.v_stride + (long long)hk * D;
@@ -412,7 +411,7 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
             for (int kb = 0; kb < D / 32; ++kb) sT[kt] = mma(fk[kb], fq[kb], sT[kt]);
         }
 #pragma unroll
-        for (int i = 0; i < Steps::N; ++i) put.put((Steps::block(i) * TK + Steps::group(i) * TileStep<T>::ROWS) * 32, gv[i]);
+        for (int i = 0; i < Steps::N; ++i) put.put(Steps::group(i), Steps::block(i), gv[i]);
         float mx = -INFINITY;
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)

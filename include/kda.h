@@ -368,7 +368,8 @@ kda_status_t kda_conv_step(const void *x, const void *w, const void *bias, void 
  *              (a multiple of 64; >= T = no split).  The result does not depend on it beyond rounding.
  *   workspace  kda_ssm_prefill_workspace_bytes(...) bytes of device memory (may be NULL when that is 0),
  *              written before it is read; calls that overlap in time need one each
- * Rows of x, Bm, Cm and z start on 16-byte boundaries.  T == 0 is valid: S_T receives S0 (or zeros).
+ * Rows of x, Bm, Cm and z start on 16-byte boundaries; H * p and the strides of these inputs are at most
+ * 2^22 elements.  T == 0 is valid: S_T receives S0 (or zeros).
  * B == 0 or H == 0 is a no-op.  States and exponents are fp32; with bf16 inputs the state is rounded to
  * bf16 only as the operand of S^T C, never in its update.
  */

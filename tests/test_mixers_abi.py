@@ -112,6 +112,7 @@ def _ssm(lib, B=2, T=200, H=4, G=2, n=128, p=64, dt=BF16, seg=0, ws=None, ws_byt
     (dict(strides=(260, 4, 256, 256, 256)), INVALID),      # rows off 16-byte boundaries
     (dict(strides=(256, 3, 256, 256, 256)), INVALID),
     (dict(strides=(256, 4, 256, 256, 0)), INVALID),
+    (dict(strides=(1 << 23, 4, 256, 256, 256)), UNSUPPORTED),   # 64 rows past 32-bit offsets
     (dict(y=_at(0)), INVALID), (dict(y=_at(11)), INVALID), (dict(y=_at(8)), INVALID), (dict(S_T=_at(3)), INVALID),
     (dict(S_T=_at(8) + 64), INVALID), (dict(S_T=_at(2)), INVALID),
     (dict(seg=64), WORKSPACE), (dict(seg=64, ws=_at(12), ws_bytes=100), WORKSPACE),
