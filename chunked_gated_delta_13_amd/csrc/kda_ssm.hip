@@ -37,15 +37,30 @@ __device__ __forceinline__ float softplus_f32(float v) {
 }
 __device__ __forceinline__ float silu_f32(float x) { return x * __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
-// Running sum over the 64 lanes of a wave.  In 64 bits: decays of neighbouring tokens are differences of
-// these sums, which may be large.
-__device__ __forceinline__ double wave_prefix(double v, int lane) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double u = __shfl_up(v, o);
-        if (lane >= o) v += u;
-    }
+// v of the lane that a DPP control names, 0 where there is none (or where the row mask leaves out).
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_f64(double v) {
+    const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
+    const u32x2_t w = {(unsigned)__builtin_amdgcn_update_dpp(0, (int)u[0], CTRL, ROWS, 0xF, true),
+                       (unsigned)__builtin_amdgcn_update_dpp(0, (int)u[1], CTRL, ROWS, 0xF, true)};
+    return __builtin_bit_cast(double, w);
+}
+
+// Running sum over the 64 lanes of a wave, by data-parallel moves: inside rows of 16 lanes (shifts by 1, 2,
+// 4, 8), then the last lane of a row into the next row, and of the lower half into the upper one.  In 64
+// bits: decays of neighbouring tokens are differences of these sums, which may be large.
+__device__ __forceinline__ double wave_prefix(double v) {
+    v += dpp_f64<0x111, 0xF>(v);
+    v += dpp_f64<0x112, 0xF>(v);
+    v += dpp_f64<0x114, 0xF>(v);
+    v += dpp_f64<0x118, 0xF>(v);
+    v += dpp_f64<0x142, 0xA>(v);
+    v += dpp_f64<0x143, 0xC>(v);
     return v;
+}
+__device__ __forceinline__ double last_lane(double v) {
+    const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
+    const u32x2_t w = {(unsigned)__builtin_amdgcn_readlane((int)u[0], 63), (unsigned)__builtin_amdgcn_readlane((int)u[1], 63)};
+    return __builtin_bit_cast(double, w);
 }
 
 // x times w (per contraction slot) as a sum of operands.  bf16: the fp32 product is cut into three parts
@@ -135,8 +150,8 @@ struct ChunkDecay {
 template <typename T>
 __device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bool live, float A2, float& scale, int lane) {
     const float d = live ? softplus_f32(raw) : 0.0f;
-    const double s = wave_prefix(live ? (double)fmaxf(d * A2, kDecayMin) : 0.0, lane);
-    const float end = (float)__shfl(s, 63), hi = (float)s;
+    const double s = wave_prefix(live ? (double)fmaxf(d * A2, kDecayMin) : 0.0);
+    const float end = (float)last_lane(s), hi = (float)s;
     const float next = scale + end;
     const bool rescale = fabsf(next) > kScaleMax;
     c->hi[lane] = hi;
@@ -490,10 +505,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
         if constexpr (OUT) yp += (long long)kC * a.H * P;
         left -= kC;
     };
-    // Waves that form M, the last of them the decays too.  Of two waves on a SIMD the older one is served
-    // first and has time left at the barrier: with all eight sharing this work, waves 0 - 3 waited 3000 of
-    // 9300 cycles a chunk for waves 4 - 7.
-    constexpr int MW = AHEAD ? NW / 2 : NW;
+    // The wave that forms the decays, and the waves 0 .. MW - 1 that form M.  Of two waves on a SIMD the
+    // older one is served first and has time left at the barrier: with all eight sharing this work, waves
+    // 0 - 3 waited 3000 of 9300 cycles a chunk for waves 4 - 7.
+    constexpr int DW = AHEAD ? NW / 2 - 1 : NW - 1, MW = AHEAD ? NW / 2 - 1 : NW;
 
     if constexpr (!AHEAD) {
         mx.set_bc(sB, sC, lane);
@@ -501,7 +516,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
         mx.rm.set(sM, lane);
         mx.set_x(sX, wave, lane);
         if (left > 0) {
-            if (wave == MW - 1) {
+            if (wave == DW) {
                 request_dt(0);
                 decay(0, 0);
                 request_dt(kC);
@@ -519,7 +534,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
                 // (the pair is taken as new in every chunk: its addresses are not worth registers)
                 for (int pair = pinned_s(wave); pair < 10; pair += MW) mx.mix(sM, cd, pair, lane);
             }
-            if (wave == MW - 1) {
+            if (wave == DW) {
                 decay(kC, par ^ 1);
                 request_dt(2 * kC);
             }
@@ -540,7 +555,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
         // chunks 0 and 1 of B and C, chunk 0 of x, M of chunk 0
         request_bc(0);
         request_x(0);
-        if (wave == MW - 1) {
+        if (wave == DW) {
             request_dt(0);
             decay(0, 0);
             request_dt(kC);
@@ -579,7 +594,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
             mx.set_bc(sB + n3 * kC * N, sC + n3 * kC * N, lane);
             if (wave < MW)
                 for (int pair = pinned_s(wave); pair < 10; pair += MW) mx.mix(sM + (par ^ 1) * kC * kC, sD + n3, pair, lane);
-            if (wave == MW - 1) {
+            if (wave == DW) {
                 decay(2 * kC, f3);
                 request_dt(3 * kC);
             }
