@@ -61,6 +61,13 @@ template <typename T, int ROWS, int WIDTH> struct TileRows {
         at[0] = lds_pin(tile + tile_at<T, ROWS>(r, g));
         at[1] = lds_pin(tile + tile_at<T, ROWS>(r, 4 + g));
     }
+    // the same lane's addresses `delta` elements (not a constant) further
+    __device__ __forceinline__ TileRows at_delta(int delta) const {
+        TileRows o;
+        o.at[0] = lds_pin(at[0] + delta);
+        o.at[1] = lds_pin(at[1] + delta);
+        return o;
+    }
     // rows 16 a .. 16 a + 15, contraction block q: columns of tiles q and q + WIDTH/32
     __device__ __forceinline__ void frag(Frag<T>& f, int delta, int a, int q) const {
         const KDA_LDS T* p = at[q & 1] + delta + 16 * 32 * a + (q >> 1) * (ROWS * 32);
@@ -88,6 +95,12 @@ template <int ROWS> struct TileCols<__bf16, ROWS> {
         at[0] = of(tile, lane, 0);
         at[1] = of(tile, lane, 1);
     }
+    __device__ __forceinline__ TileCols at_delta(int delta) const {
+        TileCols o;
+        o.at[0] = lds_pin(at[0] + delta);
+        o.at[1] = lds_pin(at[1] + delta);
+        return o;
+    }
     // addresses for column tile t only, which is then used as t = 0
     __device__ __forceinline__ void set_tile(KDA_LDS __bf16* tile, int lane, int t) { at[0] = of(tile, lane, t); }
     __device__ __forceinline__ void frag(Frag<__bf16>& f, int delta, int t, int q) const {
@@ -108,6 +121,15 @@ template <int ROWS> struct TileCols<float, ROWS> {
             at[0][i] = of(tile, lane, 0, i);
             at[1][i] = of(tile, lane, 1, i);
         }
+    }
+    __device__ __forceinline__ TileCols at_delta(int delta) const {
+        TileCols o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o.at[0][i] = lds_pin(at[0][i] + delta);
+            o.at[1][i] = lds_pin(at[1][i] + delta);
+        }
+        return o;
     }
     __device__ __forceinline__ void set_tile(KDA_LDS float* tile, int lane, int t) {
 #pragma unroll
@@ -146,6 +168,13 @@ template <typename T, int ROWS> struct TilePut {
         *reinterpret_cast<KDA_LDS u32x4_t*>(at[group % PER16] + (group / PER16) * 16 * 32 + block * ROWS * 32) = v;
     }
 };
+
+// The 16-byte piece of its row that a lane fetches when a step goes straight from memory to LDS, lane by
+// lane: the one whose place in the block is the lane's.
+template <typename T> __device__ __forceinline__ int tile_dma_piece(int row, int lane) {
+    constexpr int CH = TileStep<T>::ELEMS / 4;   // chunks per piece
+    return ((TileStep<T>::piece(lane) * CH) ^ tile_f<T>(row)) / CH;
+}
 
 // The steps of NW waves over a tile of ROWS x WIDTH: a wave's steps i = 0 .. N - 1 cover blocks of 32
 // columns of one row group, or whole row groups one after the other.

@@ -70,16 +70,23 @@ template <typename T> __device__ __forceinline__ void store4(T* p, const f32x4_t
 }  // namespace
 
 // Prompt.  A workgroup of four waves runs 64 NQ queries of one (sequence, head); each wave holds
-// 16 NQ queries and their outputs in registers and takes the keys tile by tile from LDS.
+// 16 NQ queries and their outputs in registers.  The keys come tile by tile straight from memory into
+// one of two LDS tiles, one tile ahead, and two workgroups share a compute unit: while one wave of a
+// SIMD forms exponentials, the other feeds the matrix cores.
+//
+// The running maximum only has to keep exponentials in range.  A tile that every query of the wave sees
+// whole is taken with the maximum at hand, without forming its own; only if a sum of its exponentials
+// passes kSumMax (a score far above that maximum) is the maximum brought up to date.
+constexpr float kSumMax = 16384.0f;
+
 template <int D, typename T, int NQ>
-__global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArgs a) {
-    constexpr int BM = 64 * NQ;
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefill_kernel(const WindowArgs a) {
+    constexpr int BM = 64 * NQ, TILE = kKeys * D;
     typedef TileSteps<T, kKeys, D, 4> Steps;
     constexpr int NG = Steps::N / Steps::NB;   // row groups per wave
     static_assert(NG * Steps::NB == Steps::N, "a wave takes whole rows");
-    __shared__ __attribute__((aligned(16))) T smem[2 * kKeys * D];   // a tile of keys, a tile of values
+    __shared__ __attribute__((aligned(16))) T smem[2 * 2 * TILE];   // two pairs of a tile of keys and one of values
     KDA_LDS T* sK = (KDA_LDS T*)smem;
-    KDA_LDS T* sV = sK + kKeys * D;
 
     // unit = (b, kv head, query tile, head of the group): consecutive units share keys, and each XCD
     // takes a contiguous range of them
@@ -111,10 +118,10 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
-    TileRows<T, kKeys, D> rk;
-    TileCols<T, kKeys> cv;
-    rk.set(sK, lane);
-    cv.set(sV, lane);
+    TileRows<T, kKeys, D> rk0;
+    TileCols<T, kKeys> cv0;
+    rk0.set(sK, lane);
+    cv0.set(sK + TILE, lane);
 
     const T* kn = reinterpret_cast<const T*>(a.k) + (long long)b * a.T * a.k_stride + (long long)hk * D;
     const T* vn = reinterpret_cast<const T*>(a.v) + (long long)b * a.T * a.v_stride + (long long)hk * D;
@@ -125,6 +132,35 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
         kc += (long long)b * (sinks + window) * crow + (long long)hk * D;
         vc += (long long)b * (sinks + window) * crow + (long long)hk * D;
     }
+
+    // A lane's key rows of a tile: one (bf16) or two (fp32) per wave, 16 bytes of each block of 32 columns.
+    // Places past the last key take the last key again: they are masked, and their values are finite.
+    auto fetch = [&](int t0, int buf) {
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const int row16 = (Steps::group0(wave) + j) * TileStep<T>::ROWS + TileStep<T>::row(lane);
+            const int pcol = tile_dma_piece<T>(row16, lane) * TileStep<T>::ELEMS;
+            const int at = t0 + row16, idx = at < total ? at : total - 1;
+            const int rel = idx < nsink ? idx - s : lo + (idx - nsink);
+            const T *kp = kn + (long long)rel * a.k_stride, *vp = vn + (long long)rel * a.v_stride;
+            if (rel < 0) {
+                int row = idx;
+                if (idx >= nsink) {
+                    row = base0 + rel;
+                    row = sinks + (row < 0 ? row + window : row);
+                }
+                kp = kc + row * crow;
+                vp = vc + row * crow;
+            }
+            KDA_LDS T* dst = sK + buf * (2 * TILE) + (Steps::group0(wave) + j) * TileStep<T>::ROWS * 32;
+#pragma unroll
+            for (int i = 0; i < Steps::NB; ++i) {
+                lds_dma16(reinterpret_cast<const float*>(kp + pcol + 32 * i), dst + i * kKeys * 32);
+                lds_dma16(reinterpret_cast<const float*>(vp + pcol + 32 * i), dst + TILE + i * kKeys * 32);
+            }
+        }
+    };
+    fetch(0, 0);
 
     // queries of this wave
     const int wq = q0 + wave * 16 * NQ;
@@ -149,122 +185,134 @@ __global__ __launch_bounds__(256) void kda_window_prefill_kernel(const WindowArg
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) O[t][n] = zero4();
     }
-
-    // A lane's key rows of a tile: one (bf16) or two (fp32) per wave, in pieces of 16 bytes per block
-    u32x4_t gk[Steps::N], gv[Steps::N];
-    const int prow = Steps::group0(wave) * TileStep<T>::ROWS + TileStep<T>::row(lane);
-    const int pcol = TileStep<T>::piece(lane) * (16 / (int)sizeof(T));
-    auto request = [&](int t0) {
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            const int idx = t0 + prow + j * TileStep<T>::ROWS;
-            const int rel = idx < nsink ? idx - s : lo + (idx - nsink);
-            const T *kp = kn + (long long)rel * a.k_stride, *vp = vn + (long long)rel * a.v_stride;
-            if (rel < 0) {
-                int row = idx;
-                if (idx >= nsink) {
-                    row = base0 + rel;
-                    row = sinks + (row < 0 ? row + window : row);
-                }
-                kp = kc + row * crow;
-                vp = vc + row * crow;
-            }
-#pragma unroll
-            for (int i = 0; i < Steps::NB; ++i) {
-                gk[j * Steps::NB + i] = gv[j * Steps::NB + i] = u32x4_t{0, 0, 0, 0};
-                if (idx < total) {
-                    gk[j * Steps::NB + i] = *reinterpret_cast<const u32x4_t*>(kp + pcol + 32 * i);
-                    gv[j * Steps::NB + i] = *reinterpret_cast<const u32x4_t*>(vp + pcol + 32 * i);
-                }
-            }
-        }
-    };
-    TilePut<T, kKeys> put;   // (values lie kKeys * D elements, D / 32 blocks, behind keys)
-    put.set(sK, Steps::group0(wave), lane);
-    request(0);
     const float sc = a.scale * kLog2e;
+    bool ready = false;   // every query of the wave has a maximum
+    barrier_all();
 
-    for (int t0 = 0; t0 < total; t0 += kKeys) {
-#pragma unroll
-        for (int i = 0; i < Steps::N; ++i) {
-            put.put(Steps::group(i), Steps::block(i), gk[i]);
-            put.put(Steps::group(i), Steps::block(i) + Steps::NB, gv[i]);
-        }
-        __syncthreads();
-        if (t0 + kKeys < total) request(t0 + kKeys);
+    for (int t0 = 0, buf = 0; t0 < total; t0 += kKeys, buf ^= 1) {
+        if (t0 + kKeys < total) fetch(t0 + kKeys, buf ^ 1);
+        const TileRows<T, kKeys, D> rk = rk0.at_delta(buf * (2 * TILE));
+        const TileCols<T, kKeys> cv = cv0.at_delta(buf * (2 * TILE));
 
-        // relative positions of the tile's window keys: first and last
-        const int w0 = lo + (t0 - nsink);
+        // scores, operands one contraction block ahead
         f32x4_t sT[4][NQ];
+        Frag<T> fk[2][4];
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int kt = 0; kt < 4; ++kt) rk.frag(fk[0][kt], 0, kt, 0);
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) sT[kt][n] = zero4();
+        for (int kb = 0; kb < D / 32; ++kb) {
+            if (kb + 1 < D / 32) {
 #pragma unroll
-        for (int kb = 0; kb < D / 32; ++kb)
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                Frag<T> fk;
-                rk.frag(fk, 0, kt, kb);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) sT[kt][n] = mma(fk, fq[n][kb], sT[kt][n]);
+                for (int kt = 0; kt < 4; ++kt) rk.frag(fk[(kb + 1) & 1][kt], 0, kt, kb + 1);
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) sT[kt][n] = mma(fk[kb & 1][kt], fq[n][kb], kb == 0 ? zero4() : sT[kt][n]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // the first values are requested ahead of the exponentials
+        Frag<T> fv[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cv.frag(fv[0][i], 0, i, 0);
+
+        const int w0 = lo + (t0 - nsink);   // relative position of the tile's first window key
         const bool whole = t0 >= nsink && t0 + kKeys <= total && w0 + kKeys - 1 <= wq && wq + 16 * NQ - 1 - w0 < window;
-        if (!whole) {
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int idx = t0 + 16 * kt + 4 * g + j;
-                    const bool sink = idx < nsink;
-                    const int rel = sink ? idx - s : lo + (idx - nsink);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        const int i = wq + 16 * n + r;
-                        const bool see = idx < total && rel <= i && (sink || i - rel < window);
-                        sT[kt][n][j] = see ? sT[kt][n][j] : -INFINITY;
-                    }
-                }
-        }
         Frag<T> fp[2][NQ];
+        bool done = false;
+        if (whole && ready) {
+            float sum[NQ];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            float mx = -INFINITY;
+            for (int n = 0; n < NQ; ++n) {
+                f32x4_t p[4];
+                sum[n] = 0.0f;
 #pragma unroll
-            for (int kt = 0; kt < 4; ++kt)
+                for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mx = fmaxf(mx, sT[kt][n][j]);
-            mx = fmaxf(m[n], max_over_groups(mx) * sc);
-            const float base = mx == -INFINITY ? 0.0f : mx;   // nothing visible yet: all exponentials are 0
-            const float al = fast_exp2(m[n] - base);
-            m[n] = mx;
-            float sum = 0.0f;
+                    for (int j = 0; j < 4; ++j) {
+                        p[kt][j] = fast_exp2(fmaf(sT[kt][n][j], sc, -m[n]));
+                        sum[n] += p[kt][j];
+                    }
 #pragma unroll
-            for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p = fast_exp2(fmaf(sT[kt][n][j], sc, -base));
-                    sT[kt][n][j] = p;
-                    sum += p;
-                }
-            l[n] = l[n] * al + sum;
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) O[t][n][j] *= al;
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) acc_pair_frag<T>(fp[kb][n], sT[kb][n], sT[kb + 2][n], true);
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t) {
-                Frag<T> fv;
-                cv.frag(fv, 0, t, kb);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) O[t][n] = mma(fv, fp[kb][n], O[t][n]);
+                for (int kb = 0; kb < 2; ++kb) acc_pair_frag<T>(fp[kb][n], p[kb], p[kb + 2], true);
             }
-        __syncthreads();
+            float big = sum[0];
+#pragma unroll
+            for (int n = 1; n < NQ; ++n) big += sum[n];
+            done = !__any(!(big < kSumMax));
+            if (done) {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) l[n] += sum[n];
+            }
+        }
+        if (!done) {
+            if (!whole) {
+#pragma unroll
+                for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int idx = t0 + 16 * kt + 4 * g + j;
+                        const bool sink = idx < nsink;
+                        const int rel = sink ? idx - s : lo + (idx - nsink);
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            const int i = wq + 16 * n + r;
+                            const bool see = idx < total && rel <= i && (sink || i - rel < window);
+                            sT[kt][n][j] = see ? sT[kt][n][j] : -INFINITY;
+                        }
+                    }
+            }
+            bool got = true;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx = fmaxf(mx, sT[kt][n][j]);
+                mx = fmaxf(m[n], max_over_groups(mx) * sc);
+                const float base = mx == -INFINITY ? 0.0f : mx;   // nothing visible yet: all exponentials are 0
+                const float al = fast_exp2(m[n] - base);
+                m[n] = mx;
+                got = got && mx != -INFINITY;
+                float sum = 0.0f;
+#pragma unroll
+                for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float p = fast_exp2(fmaf(sT[kt][n][j], sc, -base));
+                        sT[kt][n][j] = p;
+                        sum += p;
+                    }
+                l[n] = l[n] * al + sum;
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) O[t][n][j] *= al;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) acc_pair_frag<T>(fp[kb][n], sT[kb][n], sT[kb + 2][n], true);
+            }
+            ready = __all(got);
+        }
+
+        // groups of four tiles of the head's channels, keys (0, 2) then (1, 3), a group ahead
+        constexpr int GR = D / 64;
+#pragma unroll
+        for (int j = 0; j < 2 * GR; ++j) {
+            const int kb = j / GR, d0 = (j % GR) * 4;
+            if (j + 1 < 2 * GR) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cv.frag(fv[(j + 1) & 1][i], 0, ((j + 1) % GR) * 4 + i, (j + 1) / GR);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) O[d0 + i][n] = mma(fv[j & 1][i], fp[kb][n], O[d0 + i][n]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        barrier_all();   // the next tile has arrived, and nobody reads this one any more
     }
 
 #pragma unroll
