@@ -7,6 +7,8 @@ Outputs and states are contiguous.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -25,67 +27,64 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check(name, t, dtype, shape, device):
-    """A contiguous tensor of exactly this type, shape and device."""
+def _refuse(name, t, dtype, shape, device):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _check(name, t, dtype, shape, device):
+    """A contiguous tensor of exactly this type, shape and device."""
+    if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        _refuse(name, t, dtype, shape, device)
 
 
 def _rows(name, t, dtype, shape, device, lead):
-    """Checks a tensor whose first `lead` axes are rows and whose other axes are contiguous inside a
-    row; returns the stride between rows in elements."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    width = 1
-    for size, stride in zip(reversed(shape[lead:]), reversed(t.stride()[lead:])):
-        if size > 1 and stride != width:
-            raise ValueError(f"{name}: the elements of a token must be contiguous")
-        width *= size
+    """Checks a tensor whose first `lead` axes are rows and whose other axes (one or two) are contiguous
+    inside a row; returns the stride between rows in elements."""
+    if not (t.dtype is dtype and t.shape == shape and t.device == device):
+        _refuse(name, t, dtype, shape, device)
+    stride = t.stride()
+    width = shape[-1]
+    inner = stride[-1] == 1 or width <= 1
+    if len(stride) - lead == 2:
+        inner = inner and (stride[-2] == width or shape[-2] <= 1)
+        width *= shape[-2]
+    if not inner and width > 0:
+        raise ValueError(f"{name}: the elements of a token must be contiguous")
     if lead == 1:
-        return t.stride(0) if shape[0] > 1 else width
-    step = t.stride(1) if shape[1] > 1 else (t.stride(0) if shape[0] > 1 else width)
-    if shape[0] > 1 and shape[1] > 0 and t.stride(0) != step * shape[1]:
+        return stride[0] if shape[0] > 1 else width
+    B, T = shape[0], shape[1]
+    step = stride[1] if T > 1 else (stride[0] if B > 1 else width)
+    if B > 1 and T > 0 and stride[0] != step * T:
         raise ValueError(f"{name}: sequence b must start at row b * T of evenly spaced rows")
     return step
 
 
-def _device(t, where):
-    if t.device.type != "cuda":
-        raise ValueError(f"{where} runs on a HIP device; got a tensor on {t.device}")
-    return t.device
+def _hip(t, where):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{where} runs on a HIP device; got a tensor on {dev}")
+    return dev
 
 
-class _Here:
-    """Stands for "this device is current already"."""
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
-
-
-def _on(dev):
-    """A context in which `dev` is the current device."""
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+# the current stream of a device as a number, without a stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(fn, dev, *args):
-    """The library call on the current stream of the tensors' device (which is current)."""
-    st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    """The library call on the current stream of the tensors' device, with that device current."""
+    index = dev.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(index))
     if st:
         _lib.check(st, fn.__name__)
 
@@ -99,7 +98,7 @@ def conv_prefill(x, w, bias=None, state=None, *, lens=None, silu=True, y=None, s
     sequence (may be ``state`` itself; None when return_state is False).  ``lens`` (int32 [B]) gives
     the tokens of each sequence of a padded batch; rows of y behind them are left as they were.
     """
-    dev = _device(x, "conv_prefill")
+    dev = _hip(x, "conv_prefill")
     if x.dim() != 3 or w.dim() != 2:
         raise ValueError("x must be [B, T, D] and w [D, W]")
     B, T, D = x.shape
@@ -116,23 +115,22 @@ def conv_prefill(x, w, bias=None, state=None, *, lens=None, silu=True, y=None, s
     if lens is not None:
         _check("lens", lens, torch.int32, (B,), dev)
     if y is None:
-        y = torch.empty((B, T, D), dtype=dt, device=dev)
+        y = x.new_empty((B, T, D))
     else:
         _check("y", y, dt, (B, T, D), dev)
     if state_out is not None:
         _check("state_out", state_out, dt, keep, dev)
     elif return_state:
-        state_out = torch.empty(keep, dtype=dt, device=dev)
-    with _on(dev):
-        _call(_lib.load().kda_conv_prefill, dev, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(lens), _ptr(y),
-              _ptr(state_out), B, T, D, W, x_stride, int(bool(silu)), code)
+        state_out = x.new_empty(keep)
+    _call(_lib.load().kda_conv_prefill, dev, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(lens), _ptr(y),
+          _ptr(state_out), B, T, D, W, x_stride, int(bool(silu)), code)
     return y, state_out
 
 
 def conv_step(x, w, state, bias=None, *, silu=True, y=None):
     """The convolution for one new token of N sequences: x [N, D] (rows may be strided), ``state``
     [N, W-1, D] shifted in place.  Returns y [N, D]."""
-    dev = _device(x, "conv_step")
+    dev = _hip(x, "conv_step")
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [N, D] and w [D, W]")
     N, D = x.shape
@@ -145,12 +143,11 @@ def conv_step(x, w, state, bias=None, *, silu=True, y=None):
         _check("bias", bias, dt, (D,), dev)
     _check("state", state, dt, (N, W - 1, D), dev)
     if y is None:
-        y = torch.empty((N, D), dtype=dt, device=dev)
+        y = x.new_empty((N, D))
     else:
         _check("y", y, dt, (N, D), dev)
-    with _on(dev):
-        _call(_lib.load().kda_conv_step, dev, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y), N, D, W, x_stride,
-              int(bool(silu)), code)
+    _call(_lib.load().kda_conv_step, dev, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y), N, D, W, x_stride,
+          int(bool(silu)), code)
     return y
 
 
@@ -177,6 +174,12 @@ def _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, lead):
     return (H, G, n, p), (xs, ds, bs, cs, zs)
 
 
+@functools.lru_cache(maxsize=1024)
+def _ssm_bytes(device, *shape):   # a plan depends on the shape and the device's compute units only
+    with torch.cuda.device(device):
+        return int(_lib.load().kda_ssm_prefill_workspace_bytes(*shape))
+
+
 def ssm_workspace_bytes(B, T, H, G, n, p, dtype=torch.bfloat16, seg_len=0):
     """Device workspace bytes of ssm_prefill for this shape on the current device."""
     return int(_lib.load().kda_ssm_prefill_workspace_bytes(B, T, H, G, n, p, _code(dtype), seg_len))
@@ -192,7 +195,7 @@ def ssm_prefill(x, dt, A, Bm, Cm, S0=None, *, D=None, z=None, dt_bias=None, lens
     each sequence of a padded batch; rows of y behind them are left as they were.  ``seg_len`` forces the
     tokens per segment of the sequence split (0 = the library's choice).
     """
-    dev = _device(x, "ssm_prefill")
+    dev = _hip(x, "ssm_prefill")
     if x.dim() != 4:
         raise ValueError("x must be [B, T, H, p]")
     B, T = x.shape[:2]
@@ -205,7 +208,7 @@ def ssm_prefill(x, dt, A, Bm, Cm, S0=None, *, D=None, z=None, dt_bias=None, lens
     if lens is not None:
         _check("lens", lens, torch.int32, (B,), dev)
     if y is None:
-        y = torch.empty((B, T, H, p), dtype=ty, device=dev)
+        y = x.new_empty((B, T, H, p))
     else:
         _check("y", y, ty, (B, T, H, p), dev)
     if S_T is not None:
@@ -213,21 +216,20 @@ def ssm_prefill(x, dt, A, Bm, Cm, S0=None, *, D=None, z=None, dt_bias=None, lens
     elif return_state:
         S_T = torch.empty(state, dtype=torch.float32, device=dev)
     lib = _lib.load()
-    with _on(dev):
-        need = lib.kda_ssm_prefill_workspace_bytes(B, T, H, G, n, p, code, seg_len)
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _call(lib.kda_ssm_prefill, dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
-              _ptr(S0), _ptr(lens), _ptr(y), _ptr(S_T), B, T, H, G, n, p, *strides, code, seg_len, _ptr(workspace),
-              ws_bytes)
+    need = _ssm_bytes(dev.index, B, T, H, G, n, p, code, seg_len)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(lib.kda_ssm_prefill, dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
+          _ptr(S0), _ptr(lens), _ptr(y), _ptr(S_T), B, T, H, G, n, p, *strides, code, seg_len, _ptr(workspace),
+          ws_bytes)
     return y, S_T
 
 
 def ssm_step(x, dt, A, Bm, Cm, S, *, D=None, z=None, dt_bias=None, y=None):
     """One token of the scan for N sequences: x, z [N, H, p], dt [N, H], Bm, Cm [N, G, n]; ``S``
     [N, H, n, p] is updated in place.  Returns y [N, H, p]."""
-    dev = _device(x, "ssm_step")
+    dev = _hip(x, "ssm_step")
     if x.dim() != 3:
         raise ValueError("x must be [N, H, p]")
     N = x.shape[0]
@@ -236,12 +238,11 @@ def ssm_step(x, dt, A, Bm, Cm, S, *, D=None, z=None, dt_bias=None, y=None):
     (H, G, n, p), strides = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 1)
     _check("S", S, torch.float32, (N, H, n, p), dev)
     if y is None:
-        y = torch.empty((N, H, p), dtype=ty, device=dev)
+        y = x.new_empty((N, H, p))
     else:
         _check("y", y, ty, (N, H, p), dev)
-    with _on(dev):
-        _call(_lib.load().kda_ssm_step, dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
-              _ptr(dt_bias), _ptr(S), _ptr(y), N, H, G, n, p, *strides, code)
+    _call(_lib.load().kda_ssm_step, dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
+          _ptr(dt_bias), _ptr(S), _ptr(y), N, H, G, n, p, *strides, code)
     return y
 
 
@@ -268,7 +269,7 @@ def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cach
     written to them.  ``lens`` (int32 [B]) gives the new tokens of each sequence of a padded batch; rows
     of o behind them are left as they were.  ``scale`` defaults to d ** -0.5.
     """
-    dev = _device(q, "window_prefill")
+    dev = _hip(q, "window_prefill")
     if q.dim() != 4:
         raise ValueError("q must be [B, T, H, d]")
     B, T = q.shape[:2]
@@ -285,13 +286,18 @@ def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cach
     if lens is not None:
         _check("lens", lens, torch.int32, (B,), dev)
     if o is None:
-        o = torch.empty((B, T, H, d), dtype=ty, device=dev)
+        o = q.new_empty((B, T, H, d))
     else:
         _check("o", o, ty, (B, T, H, d), dev)
-    with _on(dev):
-        _call(_lib.load().kda_window_prefill, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(start),
-              _ptr(lens), _ptr(o), B, T, H, Hkv, d, window, sinks, d ** -0.5 if scale is None else scale, *strides, code)
+    _call(_lib.load().kda_window_prefill, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(start),
+          _ptr(lens), _ptr(o), B, T, H, Hkv, d, window, sinks, d ** -0.5 if scale is None else scale, *strides, code)
     return o
+
+
+@functools.lru_cache(maxsize=1024)
+def _window_bytes(device, *shape):
+    with torch.cuda.device(device):
+        return int(_lib.load().kda_window_step_workspace_bytes(*shape))
 
 
 def window_step_workspace_bytes(N, H, Hkv, d, window, sinks=0, dtype=torch.bfloat16):
@@ -302,7 +308,7 @@ def window_step_workspace_bytes(N, H, Hkv, d, window, sinks=0, dtype=torch.bfloa
 def window_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, o=None, workspace=None):
     """The same attention for one new token of N sequences over their ring caches, which receive the
     token's k and v: q [N, H, d], k, v [N, Hkv, d], ``pos`` (int32 [N]) the tokens before it.  Returns o."""
-    dev = _device(q, "window_step")
+    dev = _hip(q, "window_step")
     if q.dim() != 3:
         raise ValueError("q must be [N, H, d]")
     N = q.shape[0]
@@ -313,15 +319,14 @@ def window_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, 
     _check("v_cache", v_cache, ty, (N, sinks + window, Hkv, d), dev)
     _check("pos", pos, torch.int32, (N,), dev)
     if o is None:
-        o = torch.empty((N, H, d), dtype=ty, device=dev)
+        o = q.new_empty((N, H, d))
     else:
         _check("o", o, ty, (N, H, d), dev)
     lib = _lib.load()
-    with _on(dev):
-        need = lib.kda_window_step_workspace_bytes(N, H, Hkv, d, window, sinks, code)
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _call(lib.kda_window_step, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(o), N, H,
-              Hkv, d, window, sinks, d ** -0.5 if scale is None else scale, *strides, code, _ptr(workspace), ws_bytes)
+    need = _window_bytes(dev.index, N, H, Hkv, d, window, sinks, code)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(lib.kda_window_step, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(o), N, H,
+          Hkv, d, window, sinks, d ** -0.5 if scale is None else scale, *strides, code, _ptr(workspace), ws_bytes)
     return o
