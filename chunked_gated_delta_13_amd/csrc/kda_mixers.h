@@ -68,6 +68,7 @@ struct WindowArgs {
     long long q_stride, k_stride, v_stride;
     int B, T, H, Hkv, window, sinks;
     float scale;
+    int cus;                  // compute units of the device
     int q_tiles;
     int n_split, split_len;   // ranges of cache rows of the token form
     long long n_units, per_xcd;

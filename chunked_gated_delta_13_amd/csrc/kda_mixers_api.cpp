@@ -466,6 +466,7 @@ kda_status_t kda_window_prefill(const void* q, const void* k, const void* v, voi
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
+    a.cus = cu_count();
     (void)hipGetLastError();
     if (kda::launch_window_prefill(d, dt == KDA_F32, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
         return KDA_ERR_DEVICE;

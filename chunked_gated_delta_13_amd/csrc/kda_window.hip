@@ -18,9 +18,9 @@ namespace {
 
 constexpr int kKeys = 64;   // keys per tile of the prompt form
 
-// Row of the cache for position p.
-__device__ __forceinline__ long long ring_row(long long p, int sinks, int window) {
-    return p < sinks ? p : sinks + (p - sinks) % window;
+// Row of the cache for position p (32 bits hold every position: starts are int32, prompts at most 2^29).
+__device__ __forceinline__ int ring_row(uint32_t p, int sinks, int window) {
+    return p < (uint32_t)sinks ? (int)p : sinks + (int)((p - (uint32_t)sinks) % (uint32_t)window);
 }
 
 __device__ __forceinline__ float max_over_groups(float v) {
@@ -334,34 +334,34 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
 
 // The new tokens that stay in the cache: the first ones, and the last `window` ones.  It runs after
 // the attention, which reads the rows overwritten here.
-// grid: (pieces of the candidate rows / 256, sequences)
+// grid: (candidate rows / rows per workgroup, sequences); a row is 2^k or more threads wide
 template <typename T>
-__global__ __launch_bounds__(256) void kda_window_keep_kernel(const WindowArgs a, int D, int recent) {
+__global__ __launch_bounds__(256) void kda_window_keep_kernel(const WindowArgs a, int row_bytes, int recent, int shift) {
     const int b = blockIdx.y;
-    const int per_row = a.Hkv * D * (int)sizeof(T) / 16, epp = 16 / (int)sizeof(T);
-    const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long c = e / per_row;
-    const int m = (int)(e % per_row);
-    if (c >= a.sinks + recent) return;
+    const uint32_t lane = threadIdx.x & ((1u << shift) - 1);
+    const uint32_t c = blockIdx.x * (256u >> shift) + (threadIdx.x >> shift);
+    if (c >= (uint32_t)(a.sinks + recent)) return;
     int len = a.T;
     if (a.lens) {
         const int l = a.lens[b];
         len = l < 0 ? 0 : (l > a.T ? a.T : l);
     }
-    long long s = a.start ? a.start[b] : 0;
+    int s = a.start ? a.start[b] : 0;
     if (s < 0) s = 0;
-    const long long i = c < a.sinks ? c - s : len - recent + (c - a.sinks);
+    const bool first = c < (uint32_t)a.sinks;
+    const int i = first ? (int)c - s : len - recent + (int)(c - a.sinks);
     if (i < 0 || i >= len) return;
-    const long long p = s + i;
-    if (c >= a.sinks && p < a.sinks) return;   // a first token: written by its own candidate
-    const long long row = ring_row(p, a.sinks, a.window);
-    const long long width = (long long)a.Hkv * D;
-    const long long dst = ((long long)b * (a.sinks + a.window) + row) * width + m * epp;
-    const long long src = (long long)b * a.T + i;
-    *reinterpret_cast<u32x4_t*>(reinterpret_cast<T*>(a.k_cache) + dst) =
-        *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const T*>(a.k) + src * a.k_stride + m * epp);
-    *reinterpret_cast<u32x4_t*>(reinterpret_cast<T*>(a.v_cache) + dst) =
-        *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const T*>(a.v) + src * a.v_stride + m * epp);
+    const uint32_t p = (uint32_t)s + (uint32_t)i;
+    if (!first && p < (uint32_t)a.sinks) return;   // a first token: written by its own candidate
+    const long long slot = (long long)b * (a.sinks + a.window) + ring_row(p, a.sinks, a.window), row = (long long)b * a.T + i;
+    char* kd = reinterpret_cast<char*>(a.k_cache) + slot * row_bytes;
+    char* vd = reinterpret_cast<char*>(a.v_cache) + slot * row_bytes;
+    const char* ks = reinterpret_cast<const char*>(reinterpret_cast<const T*>(a.k) + row * a.k_stride);
+    const char* vs = reinterpret_cast<const char*>(reinterpret_cast<const T*>(a.v) + row * a.v_stride);
+    for (uint32_t o = 16 * lane; o < (uint32_t)row_bytes; o += 16u << shift) {
+        *reinterpret_cast<u32x4_t*>(kd + o) = *reinterpret_cast<const u32x4_t*>(ks + o);
+        *reinterpret_cast<u32x4_t*>(vd + o) = *reinterpret_cast<const u32x4_t*>(vs + o);
+    }
 }
 
 // One token.  A workgroup of four waves runs up to 16 query heads of one (sequence, kv head) over one
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
     long long pos = a.start[b];
     if (pos < 0) pos = 0;
     const int slots = a.sinks + a.window;
-    const int fresh = (int)ring_row(pos, a.sinks, a.window);   // the new token's row
+    const int fresh = ring_row((uint32_t)pos, a.sinks, a.window);   // the new token's row
     const int filled = pos + 1 < slots ? (int)pos + 1 : slots;
     const int k0 = split * a.split_len;
     const int k1 = k0 + a.split_len < filled ? k0 + a.split_len : filled;
@@ -435,10 +435,21 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
     float m = -INFINITY, l = 0.0f;
     const float sc = a.scale * kLog2e;
 
-    for (int t0 = k0 + TK * wave; t0 < k1; t0 += 4 * TK) {
-        // rows past the filled ones stand for the new token and are masked: never read memory that no
-        // token has written
-        u32x4_t gv[Steps::N];
+    // Rows past the filled ones stand for the new token and are masked: memory that no token has written
+    // is never read.  A tile's keys are requested as soon as the products with the last one's are issued,
+    // its values as soon as the last one's are in LDS.
+    u32x4_t gv[Steps::N];
+    Frag<T> fk[2][D / 32];
+    auto request_k = [&](int t0) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            const int row = t0 + 16 * kt + r;
+            const T* kp = (row >= k1 || row == fresh ? kn : kc + row * crow) + 8 * g;
+#pragma unroll
+            for (int kb = 0; kb < D / 32; ++kb) global_frag8(fk[kt][kb], kp + 32 * kb);
+        }
+    };
+    auto request_v = [&](int t0) {
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             const int row = t0 + j * TileStep<T>::ROWS + TileStep<T>::row(lane);
@@ -446,20 +457,25 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
 #pragma unroll
             for (int i = 0; i < Steps::NB; ++i) gv[j * Steps::NB + i] = *reinterpret_cast<const u32x4_t*>(vp + 32 * i);
         }
+    };
+    request_k(k0 + TK * wave);
+    request_v(k0 + TK * wave);
+    for (int t0 = k0 + TK * wave; t0 < k1; t0 += 4 * TK) {
         f32x4_t sT[2];
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
-            const int row = t0 + 16 * kt + r;
-            const T* kp = (row >= k1 || row == fresh ? kn : kc + row * crow) + 8 * g;
-            Frag<T> fk[D / 32];
-#pragma unroll
-            for (int kb = 0; kb < D / 32; ++kb) global_frag8(fk[kb], kp + 32 * kb);
             sT[kt] = zero4();
 #pragma unroll
-            for (int kb = 0; kb < D / 32; ++kb) sT[kt] = mma(fk[kb], fq[kb], sT[kt]);
+            for (int kb = 0; kb < D / 32; ++kb) sT[kt] = mma(fk[kt][kb], fq[kb], sT[kt]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        request_k(t0 + 4 * TK);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < Steps::N; ++i) put.put(Steps::group(i), Steps::block(i), gv[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        request_v(t0 + 4 * TK);
+        __builtin_amdgcn_sched_barrier(0);
         float mx = -INFINITY;
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
@@ -535,45 +551,69 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
     }
 }
 
-// Joins the ranges of a split step.  grid: (sequence, head) rows; D / 4 threads
+// Joins the ranges of a split step.  grid: (sequence, head) rows; one wave: D / 4 lanes own four channels
+// of a range, and 64 / (D / 4) ranges are taken side by side.
 template <int D, typename T>
 __global__ __launch_bounds__(64) void kda_window_join_kernel(const WindowArgs a) {
+    constexpr int NL = D / 4, NS = 64 / NL;
     const long long row = blockIdx.x;
-    const int d = threadIdx.x * 4;
+    const int lane = threadIdx.x, d = (lane % NL) * 4, i0 = lane / NL;
     const float* ml = a.ws_ml + 2 * row * a.n_split;
     const float* o = a.ws_o + row * a.n_split * D + d;
     float M = -INFINITY;
-    for (int i = 0; i < a.n_split; ++i) M = fmaxf(M, ml[2 * i]);
+    for (int i = lane; i < a.n_split; i += 64) M = fmaxf(M, ml[2 * i]);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
     float L = 0.0f;
     f32x4_t v = zero4();
-    for (int i = 0; i < a.n_split; ++i) {
+#pragma unroll 4
+    for (int i = i0; i < a.n_split; i += NS) {
         const float f = fast_exp2(ml[2 * i] - M);
         L = fmaf(f, ml[2 * i + 1], L);
         const f32x4_t x = *reinterpret_cast<const f32x4_t*>(o + (long long)i * D);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = fmaf(f, x[j], v[j]);
     }
+#pragma unroll
+    for (int x = NL; x < 64; x <<= 1) {
+        L += __shfl_xor(L, x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += __shfl_xor(v[j], x);
+    }
     const float inv = 1.0f / L;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= inv;
-    store4<T>(reinterpret_cast<T*>(a.o) + row * D + d, v);
+    if (i0 == 0) store4<T>(reinterpret_cast<T*>(a.o) + row * D + d, v);
 }
 
 namespace {
 
-template <int D, typename T>
-hipError_t window_prefill_t(WindowArgs a, hipStream_t s) {
-    constexpr int NQ = sizeof(T) == 2 ? 2 : 1;   // fp32 operands take twice the registers
+template <int D, typename T, int NQ>
+hipError_t window_attend(WindowArgs a, hipStream_t s) {
     a.q_tiles = (a.T + 64 * NQ - 1) / (64 * NQ);
     a.n_units = (long long)a.B * a.H * a.q_tiles;
     a.per_xcd = (a.n_units + 7) / 8;
     if (a.per_xcd > 0x0fffffff) return hipErrorInvalidValue;
     kda_window_prefill_kernel<D, T, NQ><<<dim3((unsigned)(8 * a.per_xcd)), 256, 0, s>>>(a);
-    hipError_t e = hipGetLastError();
+    return hipGetLastError();
+}
+
+template <int D, typename T>
+hipError_t window_prefill_t(const WindowArgs& a, hipStream_t s) {
+    // 128 queries per workgroup read each key once for twice the products; 64 where there are too few
+    // queries to give every compute unit a workgroup (and for fp32, whose operands take twice the
+    // registers).
+    const bool few = (long long)a.B * a.H * ((a.T + 127) / 128) < a.cus;
+    hipError_t e;
+    if constexpr (sizeof(T) == 2) e = few ? window_attend<D, T, 1>(a, s) : window_attend<D, T, 2>(a, s);
+    else e = window_attend<D, T, 1>(a, s);
     if (e != hipSuccess || !a.k_cache) return e;
     const int recent = a.window < a.T ? a.window : a.T;
-    const long long pieces = ((long long)a.sinks + recent) * (a.Hkv * D * (long long)sizeof(T) / 16);
-    kda_window_keep_kernel<T><<<dim3((unsigned)((pieces + 255) / 256), a.B), 256, 0, s>>>(a, D, recent);
+    const int row_bytes = a.Hkv * D * (int)sizeof(T);
+    int shift = 3;   // threads per row: a power of two of 16-byte pieces, at most the workgroup
+    while (shift < 8 && (16 << shift) < row_bytes) ++shift;
+    const int per = 256 >> shift;
+    kda_window_keep_kernel<T><<<dim3((unsigned)((a.sinks + recent + per - 1) / per), a.B), 256, 0, s>>>(a, row_bytes, recent, shift);
     return hipGetLastError();
 }
 
@@ -585,7 +625,7 @@ hipError_t window_step_t(WindowArgs a, hipStream_t s) {
     kda_window_step_kernel<D, T><<<dim3((unsigned)(8 * a.per_xcd)), 256, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_split == 1) return e;
-    kda_window_join_kernel<D, T><<<dim3((unsigned)((long long)a.B * a.H)), D / 4, 0, s>>>(a);
+    kda_window_join_kernel<D, T><<<dim3((unsigned)((long long)a.B * a.H)), 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
