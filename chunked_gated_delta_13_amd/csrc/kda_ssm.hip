@@ -618,22 +618,36 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
 }
 
 // Entry states from the segments' final states, in place: slot s + 1 holds the final state of segment s
-// from zero (segment 0: from its entry state) and becomes the entry state of segment s + 1.
-// grid: sequences x heads x (state elements / 1024)
+// from zero (segment 0: from its entry state) and becomes the entry state of segment s + 1.  A thread
+// owns two elements and requests kAhead segments at a time: the chain is one multiply-add per segment,
+// the loads do not wait for it.
+// grid: sequences x heads x (state elements / 512)
 __global__ __launch_bounds__(256) void kda_ssm_join_kernel(float* ws, const float* decay, int n_seg, int np) {
-    const int per = np / 1024;
+    constexpr int kAhead = 8;
+    typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+    const int per = np / 512;
     const long long bh = blockIdx.x / per;
-    const int e = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * 4;
+    const int e = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * 2;
     float* p = ws + (bh * n_seg + 1) * (long long)np + e;
     const float* d = decay + bh * n_seg;
-    f32x4_t S = *reinterpret_cast<const f32x4_t*>(p);
-    for (int s = 2; s < n_seg; ++s) {
-        p += np;
-        const f32x4_t hs = *reinterpret_cast<const f32x4_t*>(p);
-        const float f = fast_exp2(d[s]);
+    f32x2_t S = *reinterpret_cast<const f32x2_t*>(p);
+    for (int s = 2; s < n_seg; s += kAhead) {
+        f32x2_t h[kAhead];
+        float f[kAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[i] = fmaf(f, S[i], hs[i]);
-        *reinterpret_cast<f32x4_t*>(p) = S;
+        for (int i = 0; i < kAhead; ++i) {
+            const int t = s + i < n_seg ? s + i : n_seg - 1;
+            h[i] = *reinterpret_cast<const f32x2_t*>(p + (long long)(t - 1) * np);
+            f[i] = d[t];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (s + i >= n_seg) break;
+            const float x = fast_exp2(f[i]);
+            S[0] = fmaf(x, S[0], h[i][0]);
+            S[1] = fmaf(x, S[1], h[i][1]);
+            *reinterpret_cast<f32x2_t*>(p + (long long)(s + i - 1) * np) = S;
+        }
     }
 }
 
@@ -734,7 +748,7 @@ hipError_t launch_ssm(SsmPass pass, int n, int p, bool f32, const SsmArgs& a, hi
 }
 
 hipError_t launch_ssm_join(int n, int p, int bh, int n_seg, float* ws_state, const float* ws_decay, hipStream_t s) {
-    kda_ssm_join_kernel<<<dim3((unsigned)bh * (n * p / 1024)), 256, 0, s>>>(ws_state, ws_decay, n_seg, n * p);
+    kda_ssm_join_kernel<<<dim3((unsigned)bh * (n * p / 512)), 256, 0, s>>>(ws_state, ws_decay, n_seg, n * p);
     return hipGetLastError();
 }
 
