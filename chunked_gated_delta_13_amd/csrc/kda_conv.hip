@@ -26,9 +26,7 @@ template <typename T> struct ConvVec<T, 1> {
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void conv_load(float (&out)[V], const T* p) {
-    typedef typename ConvVec<T, V>::type vec_t;
-    const vec_t x = *reinterpret_cast<const vec_t*>(p);
+__device__ __forceinline__ void conv_widen(float (&out)[V], typename ConvVec<T, V>::type x) {
     if constexpr (V == 1) {
         out[0] = to_f32<T>(x);
     } else {
@@ -36,8 +34,12 @@ __device__ __forceinline__ void conv_load(float (&out)[V], const T* p) {
         for (int i = 0; i < V; ++i) out[i] = to_f32<T>((T)x[i]);
     }
 }
-
 template <typename T, int V>
+__device__ __forceinline__ void conv_load(float (&out)[V], const T* p) {
+    conv_widen<T, V>(out, *reinterpret_cast<const typename ConvVec<T, V>::type*>(p));
+}
+
+template <typename T, int V, bool STREAM = false>
 __device__ __forceinline__ void conv_store(T* p, const float (&in)[V]) {
     typedef typename ConvVec<T, V>::type vec_t;
     if constexpr (V == 1) {
@@ -46,7 +48,8 @@ __device__ __forceinline__ void conv_store(T* p, const float (&in)[V]) {
         vec_t x;
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = from_f32<T>(in[i]);
-        *reinterpret_cast<vec_t*>(p) = x;
+        if constexpr (STREAM) __builtin_nontemporal_store(x, reinterpret_cast<vec_t*>(p));
+        else *reinterpret_cast<vec_t*>(p) = x;
     }
 }
 
@@ -68,8 +71,8 @@ __device__ __forceinline__ void conv_weights(float (&w)[W][V], float (&b)[V], co
 
 }  // namespace
 
-// grid: (channel groups / 256, token tiles, sequences)
-template <typename T, int W, int V>
+// grid: (channel groups / 256, token tiles, sequences).  STREAM: outputs go past the caches.
+template <typename T, int W, int V, bool STREAM>
 __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(const ConvArgs a) {
     const int d = (int)(blockIdx.x * kConvThreads + threadIdx.x) * V;
     const int b = blockIdx.z;
@@ -128,8 +131,9 @@ __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(const Co
     }
     float w[W][V], bias[V];
     conv_weights<T, W, V>(w, bias, a, d);
-    for (long long t = t0; t < t1; ++t) {
-        conv_load<T, V>(h[W - 1], x + t * a.x_stride);
+    // kRows rows are requested together, so that a wave keeps several loads in flight
+    constexpr int kRows = 4;
+    auto token = [&](T* out) {   // h[0 .. W - 1] end at the token
         float acc[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = bias[e];
@@ -141,11 +145,26 @@ __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(const Co
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] = silu_f32(acc[e]);
         }
-        conv_store<T, V>(y + t * a.D, acc);
+        conv_store<T, V, STREAM>(out, acc);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
             for (int e = 0; e < V; ++e) h[j][e] = h[j + 1][e];
+    };
+    long long t = t0;
+    for (; t + kRows <= t1; t += kRows) {
+        typename ConvVec<T, V>::type v[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) v[i] = *reinterpret_cast<const typename ConvVec<T, V>::type*>(x + (t + i) * a.x_stride);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            conv_widen<T, V>(h[W - 1], v[i]);
+            token(y + (t + i) * a.D);
+        }
+    }
+    for (; t < t1; ++t) {
+        conv_load<T, V>(h[W - 1], x + t * a.x_stride);
+        token(y + t * a.D);
     }
 }
 
@@ -182,7 +201,8 @@ hipError_t conv_prefill_wv(const ConvArgs& a, hipStream_t s) {
     const int groups = (a.D + V - 1) / V;
     const int tiles = a.T > 0 ? (int)(((long long)a.T + a.tile - 1) / a.tile) : 1;
     const dim3 grid((groups + kConvThreads - 1) / kConvThreads, tiles, a.B);
-    kda_conv_prefill_kernel<T, W, V><<<grid, kConvThreads, 0, s>>>(a);
+    if (V > 1 && a.streamed) kda_conv_prefill_kernel<T, W, V, (V > 1)><<<grid, kConvThreads, 0, s>>>(a);
+    else kda_conv_prefill_kernel<T, W, V, false><<<grid, kConvThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 

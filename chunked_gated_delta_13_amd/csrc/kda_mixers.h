@@ -20,6 +20,7 @@ struct ConvArgs {
     int B, T, D;
     int silu;
     int tile;                 // tokens per thread (prompt form)
+    int streamed;             // 1: outputs larger than the caches, stored past them
 };
 
 // vec = channels per thread: 16 bytes of them where rows are 16-byte aligned, else 1.
