@@ -130,30 +130,24 @@ __device__ __forceinline__ int pinned_s(int x) {
     return x;
 }
 
-// Numbers of one chunk.  The state is held as 2^scale times the registers' values, so that a chunk whose
-// decay is mild costs no multiplication of the state: it is rescaled only when the exponent leaves
-// +-kScaleMax (values up to 2^(127 - kScaleMax) stay finite).
-constexpr float kScaleMax = 24.0f;
+// Numbers of one chunk.
 struct ChunkDecay {
     float hi[kC];      // sum of the exponents (base 2) up to this token
     float lo[kC];      // fp32: what `hi` leaves of that sum; bf16: hi - log2 dt
     float dt[kC];      // (fp32)
-    float e[kC];       // factor of S^T C: 2^(sum + scale)
+    float e[kC];       // factor of S^T C: 2^sum
     float w[kC];       // weight of the token in the state's update
     float sum;         // of the whole chunk
-    float factor;      // the state's factor before the update, 1 when `rescale` is 0
-    float scale;       // the state's exponent after the chunk
-    int rescale;
+    float factor;      // 2^sum of the whole chunk
 };
 
-// By one wave, lane = token; `scale` is the state's exponent before the chunk and after it.
+// By one wave, lane = token.
 template <typename T>
-__device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bool live, float A2, float& scale, int lane) {
+__device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bool live, float A2, int lane) {
     const float d = live ? softplus_f32(raw) : 0.0f;
     const double s = wave_prefix(live ? (double)fmaxf(d * A2, kDecayMin) : 0.0);
-    const float end = (float)last_lane(s), hi = (float)s;
-    const float next = scale + end;
-    const bool rescale = fabsf(next) > kScaleMax;
+    const double end = last_lane(s);
+    const float hi = (float)s;
     c->hi[lane] = hi;
     if constexpr (sizeof(T) == 4) {
         c->lo[lane] = (float)(s - (double)hi);
@@ -162,16 +156,12 @@ __device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bo
         // 2^(c_i - c_j) dt_j as one exponential; dt = 0 gives +inf here and a factor of 0
         c->lo[lane] = hi - __log2f(d);
     }
-    c->e[lane] = fast_exp2(hi + scale);
-    // 2^(end - s), over 2^next unless the state is brought to the exponent 0
-    c->w[lane] = fast_exp2((float)((rescale ? (double)end : -(double)scale) - s)) * d;
+    c->e[lane] = fast_exp2(hi);
+    c->w[lane] = fast_exp2((float)(end - s)) * d;
     if (lane == 0) {
-        c->sum = end;
-        c->factor = rescale ? fast_exp2(next) : 1.0f;
-        c->scale = rescale ? 0.0f : next;
-        c->rescale = rescale ? 1 : 0;
+        c->sum = (float)end;
+        c->factor = fast_exp2((float)end);
     }
-    scale = rescale ? 0.0f : next;
 }
 
 // A lane's place in the tiles of one workgroup, and the three parts of a chunk's work.  N x P state, NW
@@ -198,39 +188,61 @@ template <int N, int P, typename T, int NW> struct Mixer {
         }
     }
 
-    // M[i][j] = e^{c_i - c_j} dt_j (C_i . B_j) for j <= i, tile pair 0 .. 9 of the ten lower 16 x 16 tiles
-    __device__ __forceinline__ void mix(KDA_LDS T* sM, const KDA_LDS ChunkDecay* cd, int pair, int lane) const {
+    // M[i][j] = e^{c_i - c_j} dt_j (C_i . B_j) for j <= i: K of the ten lower 16 x 16 tiles side by side
+    // (pair 0 .. 9, row by row), each a chain from LDS through the matrix cores and an exponential
+    template <int K>
+    __device__ __forceinline__ void mix(KDA_LDS T* sM, const KDA_LDS ChunkDecay* cd, const int (&pair)[K], int lane) const {
+        constexpr int Q = N / 32;
         const int g = lane >> 4, r = lane & 15;
-        const int ti = pair < 1 ? 0 : (pair < 3 ? 1 : (pair < 6 ? 2 : 3));
-        const int tj = pair - ti * (ti + 1) / 2;
-        Frag<T> fb[N / 32], fc[N / 32];
+        Frag<T> fb[K][Q], fc[K][Q];
+        int ti[K], tj[K];
+        float ci[K];
+        f32x4_t lj[K];
 #pragma unroll
-        for (int q = 0; q < N / 32; ++q) {
-            rb.frag(fb[q], 16 * 32 * tj, 0, q);
-            rc.frag(fc[q], 16 * 32 * ti, 0, q);
+        for (int p = 0; p < K; ++p) {
+            ti[p] = pair[p] < 1 ? 0 : (pair[p] < 3 ? 1 : (pair[p] < 6 ? 2 : 3));
+            tj[p] = pair[p] - ti[p] * (ti[p] + 1) / 2;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                rb.frag(fb[p][q], 16 * 32 * tj[p], 0, q);
+                rc.frag(fc[p][q], 16 * 32 * ti[p], 0, q);
+            }
+            ci[p] = cd->hi[16 * ti[p] + r];
+            lj[p] = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->lo + 16 * tj[p] + 4 * g);
         }
-        const float ci = cd->hi[16 * ti + r];
-        const f32x4_t lj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->lo + 16 * tj + 4 * g);
         __builtin_amdgcn_sched_barrier(0);
-        f32x4_t acc = zero4();   // acc[k]: token j = 16 tj + 4 g + k against i = 16 ti + r
+        f32x4_t acc[K];   // acc[p][k]: token j = 16 tj + 4 g + k against i = 16 ti + r
 #pragma unroll
-        for (int q = 0; q < N / 32; ++q) acc = mma(fb[q], fc[q], acc);
-        float m[4];
-        if constexpr (sizeof(T) == 4) {
-            const float li = cd->lo[16 * ti + r];
-            const f32x4_t cj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->hi + 16 * tj + 4 * g);
-            const f32x4_t dj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->dt + 16 * tj + 4 * g);
+        for (int q = 0; q < Q; ++q)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m[k] = acc[k] * (fast_exp2((ci - cj[k]) + (li - lj[k])) * dj[k]);
-        } else {
+            for (int p = 0; p < K; ++p) acc[p] = mma(fb[p][q], fc[p][q], q == 0 ? zero4() : acc[p]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m[k] = acc[k] * fast_exp2(ci - lj[k]);
+        for (int p = 0; p < K; ++p) {
+            float m[4];
+            if constexpr (sizeof(T) == 4) {
+                const float li = cd->lo[16 * ti[p] + r];
+                const f32x4_t cj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->hi + 16 * tj[p] + 4 * g);
+                const f32x4_t dj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->dt + 16 * tj[p] + 4 * g);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m[k] = acc[p][k] * (fast_exp2((ci[p] - cj[k]) + (li - lj[p][k])) * dj[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m[k] = acc[p][k] * fast_exp2(ci[p] - lj[p][k]);
+            }
+            if (ti[p] == tj[p]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m[k] = 4 * g + k <= r ? m[k] : 0.0f;
+            }
+            lds_store_run<4>(sM + 16 * 32 * ti[p] + tile_at<T, kC>(r, 4 * tj[p] + g), m);
         }
-        if (ti == tj) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m[k] = 4 * g + k <= r ? m[k] : 0.0f;
-        }
-        lds_store_run<4>(sM + 16 * 32 * ti + tile_at<T, kC>(r, 4 * tj + g), m);
+    }
+    // The tiles first, first + step, .., K at a time
+    template <int K>
+    __device__ __forceinline__ void mix_every(KDA_LDS T* sM, const KDA_LDS ChunkDecay* cd, int first, int step, int lane) const {
+        int pair = first;
+        if constexpr (K == 2)
+            for (; pair + step < 10; pair += 2 * step) mix<2>(sM, cd, {pair, pair + step}, lane);
+        for (; pair < 10; pair += step) mix<1>(sM, cd, {pair}, lane);
     }
 
     // x of this wave's columns, transposed: contraction over tokens
@@ -311,46 +323,51 @@ template <int N, int P, typename T, int NW> struct Mixer {
             }
     }
 
-    // S <- e^{c_63} S + B^T (w x)
+    // S <- e^{c_63} S + B^T (w x).  The chunk's sum starts from zero and is added to the decayed state with
+    // one rounding: the matrix cores drop low bits when they add to a large accumulator, always towards
+    // zero, which a state that decays slowly would collect over many chunks.
     __device__ __forceinline__ void update(State& S, const Frag<T> (&xt)[2][NCT], const KDA_LDS ChunkDecay* cd, int lane) const {
-        if (cd->rescale) {
-            const float f = cd->factor;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) S[nt][ct][k] *= f;
-        }
-        // groups of NG row tiles of the state, token tiles (0, 2) then (1, 3); a group's columns of B are
-        // requested while the products of the group before run
-        constexpr int NG = NT < 4 ? NT : 4, NGR = 2 * NT / NG;
-        Frag<T> fb[2][NG], xs[NCT][NP];
+        const float f = cd->factor;
+        // groups of NG row tiles of the state; a group's columns of B are requested while the products of the
+        // group before run
+        constexpr int NG = 2, NGR = NT / NG;
+        Frag<T> fb[2][NG][2], xs[2][NCT][NP];
         float w[2][8];
         load_weights(w[0], cd->w + 4 * (lane >> 4));
         load_weights(w[1], cd->w + 16 + 4 * (lane >> 4));
 #pragma unroll
-        for (int i = 0; i < NG; ++i) cb.frag(fb[0][i], 0, i, 0);
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) cb.frag(fb[0][i][q], 0, i, q);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) weigh(xs[q][ct], xt[q][ct], w[q]);
 #pragma unroll
         for (int j = 0; j < NGR; ++j) {
-            const int q = j / (NGR / 2), n0 = (j % (NGR / 2)) * NG;
             if (j + 1 < NGR) {
 #pragma unroll
                 for (int i = 0; i < NG; ++i)
-                    cb.frag(fb[(j + 1) & 1][i], 0, ((j + 1) % (NGR / 2)) * NG + i, (j + 1) / (NGR / 2));
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) cb.frag(fb[(j + 1) & 1][i][q], 0, (j + 1) * NG + i, q);
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (n0 == 0) {
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) weigh(xs[ct], xt[q][ct], w[q]);
-            }
+            f32x4_t acc[NG][NCT];
 #pragma unroll
             for (int k = NP - 1; k >= 0; --k)
 #pragma unroll
-                for (int i = 0; i < NG; ++i)
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) S[n0 + i][ct] = mma(fb[j & 1][i], xs[ct][k], S[n0 + i][ct]);
-            __builtin_amdgcn_sched_barrier(0);
+                    for (int i = 0; i < NG; ++i)
+#pragma unroll
+                        for (int ct = 0; ct < NCT; ++ct)
+                            acc[i][ct] = mma(fb[j & 1][i][q], xs[q][ct][k], k == NP - 1 && q == 0 ? zero4() : acc[i][ct]);
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) S[j * NG + i][ct][k] = fmaf(f, S[j * NG + i][ct][k], acc[i][ct][k]);
         }
     }
 
@@ -372,13 +389,13 @@ template <int N, int P, typename T, int NW> struct Mixer {
                     for (int k = 0; k < 4; ++k) S[nt][ct][k] = *at_byte(p + (16 * nt + k) * P + 16 * ct, off);
         }
     }
-    __device__ __forceinline__ static void store_state(const State& S, float factor, float* p, uint32_t off) {
+    __device__ __forceinline__ static void store_state(const State& S, float* p, uint32_t off) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) *at_byte(p + (16 * nt + k) * P + 16 * ct, off) = S[nt][ct][k] * factor;
+                for (int k = 0; k < 4; ++k) *at_byte(p + (16 * nt + k) * P + 16 * ct, off) = S[nt][ct][k];
     }
 };
 
@@ -460,10 +477,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
     }
     Mix::load_state(S, sin, s_off);
     // S_T is S0: the other pass's last segment overwrites it
-    if (!OUT && s == 0 && a.keep_S0) Mix::store_state(S, 1.0f, a.ws_state + bh * a.n_seg * (long long)(N * P), s_off);
+    if (!OUT && s == 0 && a.keep_S0) Mix::store_state(S, a.ws_state + bh * a.n_seg * (long long)(N * P), s_off);
 
     float total = 0.0f;   // exponent (base 2) of the segment's decay
-    float final_scale = 0.0f;
     Mix mx;
     // Rows of B, C and x are requested into registers a chunk or more before they are put into their
     // tiles; the raw steps (one wave) a chunk before their sums, a long chain that this wave forms while
@@ -471,7 +487,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
     // lets every wait count the requests behind it.
     Stage<T, P, NW> gx;
     Stage<T, N, NW> gb, gc;
-    float gdt = 0.0f, scale = 0.0f;
+    float gdt = 0.0f;
     int left = (int)(t_end - t_begin);   // tokens left, from the chunk at hand on
     auto rows_at = [&](int ahead) { return left - ahead < kC ? left - ahead : kC; };
     auto request_bc = [&](int ahead) {   // the chunk `ahead` tokens from the one at hand
@@ -486,7 +502,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
     auto request_dt = [&](int ahead) {
         gdt = buffer_load1(dp, make_rows(dp + ahead * a.dt_stride, rows_at(ahead), dt_step, ES), lane * dt_step);
     };
-    auto decay = [&](int ahead, int buf) { chunk_decay<T>(sD + buf, gdt + bias, ahead + lane < left, A2, scale, lane); };
+    auto decay = [&](int ahead, int buf) { chunk_decay<T>(sD + buf, gdt + bias, ahead + lane < left, A2, lane); };
     vec4 zv[4][NCT];
     auto request_z = [&](int ahead) {
         const buffer_t zbuf = make_rows(zp + ahead * a.z_stride, gated ? rows_at(ahead) : 0, z_step, ROW_P);
@@ -508,7 +524,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
     // The wave that forms the decays, and the waves 0 .. MW - 1 that form M.  Of two waves on a SIMD the
     // older one is served first and has time left at the barrier: with all eight sharing this work, waves
     // 0 - 3 waited 3000 of 9300 cycles a chunk for waves 4 - 7.
-    constexpr int DW = AHEAD ? NW / 2 - 1 : NW - 1, MW = AHEAD ? NW / 2 - 1 : NW;
+    constexpr int DW = AHEAD ? NW / 2 - 1 : NW - 1, MW = DW;
 
     if constexpr (!AHEAD) {
         mx.set_bc(sB, sC, lane);
@@ -531,8 +547,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
             __syncthreads();
             if constexpr (OUT) {
                 request_z(0);
-                // (the pair is taken as new in every chunk: its addresses are not worth registers)
-                for (int pair = pinned_s(wave); pair < 10; pair += MW) mx.mix(sM, cd, pair, lane);
+                // (the first tile is taken as new in every chunk: its addresses are not worth registers)
+                if (wave < MW) mx.template mix_every<2>(sM, cd, pinned_s(wave), MW, lane);
             }
             if (wave == DW) {
                 decay(kC, par ^ 1);
@@ -547,7 +563,6 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
             request_x(kC);
             mx.update(S, xt, cd, lane);
             total += cd->sum;
-            final_scale = cd->scale;
             __syncthreads();
             advance();
         }
@@ -569,7 +584,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
         put_bc(1);
         __syncthreads();
         mx.set_bc(sB, sC, lane);
-        for (int pair = wave; pair < 10; pair += NW) mx.mix(sM, sD, pair, lane);
+        mx.template mix_every<1>(sM, sD, wave, NW, lane);
         request_bc(2 * kC);
         request_z(0);
         __syncthreads();
@@ -590,10 +605,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
             request_z(kC);
             mx.update(S, xt, cd, lane);
             total += cd->sum;
-            final_scale = cd->scale;
             mx.set_bc(sB + n3 * kC * N, sC + n3 * kC * N, lane);
-            if (wave < MW)
-                for (int pair = pinned_s(wave); pair < 10; pair += MW) mx.mix(sM + (par ^ 1) * kC * kC, sD + n3, pair, lane);
+            if (wave < MW) mx.template mix_every<1>(sM + (par ^ 1) * kC * kC, sD + n3, pinned_s(wave), MW, lane);
             if (wave == DW) {
                 decay(2 * kC, f3);
                 request_dt(3 * kC);
@@ -614,7 +627,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
         so = a.ws_state + (bh * a.n_seg + s + 1) * (long long)(N * P);
         if (tid == 0) a.ws_decay[bh * a.n_seg + s + 1] = total;
     }
-    if (so) Mix::store_state(S, fast_exp2(final_scale), so, s_off);
+    if (so) Mix::store_state(S, so, s_off);
 }
 
 // Entry states from the segments' final states, in place: slot s + 1 holds the final state of segment s
