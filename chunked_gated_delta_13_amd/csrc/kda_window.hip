@@ -489,14 +489,15 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
                 mx = fmaxf(mx, sT[kt][j]);
             }
         mx = fmaxf(m, max_over_groups(mx) * sc);
-        const float al = fast_exp2(m - mx);   // the tile has a visible row: mx is a number
+        const float base = mx == -INFINITY ? 0.0f : mx;   // every score so far is below fp32's range: no weight
+        const float al = fast_exp2(m - base);
         m = mx;
         float sum = 0.0f;
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                sT[kt][j] = fast_exp2(fmaf(sT[kt][j], sc, -mx));
+                sT[kt][j] = fast_exp2(fmaf(sT[kt][j], sc, -base));
                 sum += sT[kt][j];
             }
         l = l * al + sum;

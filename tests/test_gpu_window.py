@@ -163,6 +163,34 @@ def test_window_step_matches_definition(case):
     assert np.array_equal(ref.f64(kd), kc_ref, equal_nan=True) and np.array_equal(ref.f64(vd), vc_ref, equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("win", [300, 1500])
+def test_window_scores_below_the_range_of_fp32_have_no_weight(dtype, win):
+    """A run of keys whose products with the query are -inf in fp32 (-6e41): their exponentials are 0, also
+    where they fill a whole tile, and the other keys' scores of 0 weigh their values equally.  Weights are 1
+    exactly, so what is off is the sum (a rounding per key and per join) and the output's rounding."""
+    kda = _kda()
+    d, far = 64, 200
+    q = torch.full((1, 1, d), 1e20, dtype=DT[dtype])
+    kc = torch.zeros(1, win, 1, d, dtype=DT[dtype])
+    kc[:, :far] = -1e20
+    vc = _draw(4, dtype, 1, win, 1, d)
+    v = _draw(5, dtype, 1, 1, d)
+    see = torch.cat([vc[:, far:win - 1, 0], v], 1).double()
+    want, mag = see.mean(1, keepdim=True).numpy(), see.abs().mean(1, keepdim=True).numpy()
+    tol = ref.half_step(DT[dtype]) * np.abs(want) + (win + 16) * ref.U32 * mag
+    zero = torch.zeros(1, 1, d, dtype=DT[dtype])
+    o = kda.window_step(q.cuda(), zero.cuda(), v.cuda(), kc.cuda(), vc.cuda(),
+                        torch.tensor([win - 1], dtype=torch.int32, device="cuda"), win)
+    ks = torch.cat([kc[:, :win - 1], zero[:, None]], 1).cuda()
+    vs = torch.cat([vc[:, :win - 1], v[:, None]], 1).cuda()
+    p = kda.window_prefill(q[:, None].expand(1, win, 1, d).contiguous().cuda(), ks, vs, win)
+    torch.cuda.synchronize()
+    for name, got in (("step", o), ("prompt", p[:, -1])):
+        err = np.abs(ref.f64(got) - want)
+        assert (err <= tol).all(), (name, float((err / tol).max()))
+
+
 def test_window_step_splits_where_rows_are_few():
     kda = _kda()
     assert kda.window_step_workspace_bytes(1, 14, 2, 128, 4096, 4) > 0
