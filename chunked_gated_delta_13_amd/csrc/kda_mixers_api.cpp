@@ -20,6 +20,8 @@ using kda::range_of;
 namespace {
 
 constexpr long long kMaxGridYZ = 65535;   // blocks of a launch along y or z
+// Workgroups of a launch along x: up to 512 threads each, and fewer than 2^32 threads in all.
+constexpr long long kMaxUnits = 1LL << 22;
 constexpr size_t kStreamedBytes = (size_t)192 << 20;   // outputs that do not stay in the 256 MB last-level cache
 
 size_t elem_size(kda_dtype_t dt) { return dt == KDA_BF16 ? 2 : 4; }
@@ -92,7 +94,7 @@ kda_status_t check_ssm_shape(int rows_b, int T, int H, int G, int n, int p, kda_
     long long a = 0, b = 0;
     if (!mul_ok((long long)rows_b * T, (long long)H * p, &a) || a >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
     if (!mul_ok((long long)rows_b * H, (long long)n * p, &b) || b >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((long long)rows_b * H > (1LL << 24)) return KDA_ERR_UNSUPPORTED;   // units of a launch fit its grid
+    if ((long long)rows_b * H > kMaxUnits) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -111,7 +113,8 @@ kda_status_t ssm_plan(int B, int T, int H, int p, kda_dtype_t dt, int seg_in, lo
     }
     if (per < 1) per = 1;
     const long long ns = chunks > 0 ? (chunks + per - 1) / per : 1;
-    if (units * ns > (1LL << 28)) return KDA_ERR_UNSUPPORTED;
+    // a split's join runs n p / 512 (at most 32) workgroups of 256 threads per sequence and head
+    if (units * ns > (ns > 1 ? kMaxUnits / 4 : kMaxUnits)) return KDA_ERR_UNSUPPORTED;
     *seg_len = per * kSsmChunk;
     *n_seg = (int)ns;
     return KDA_OK;
@@ -211,7 +214,7 @@ kda_status_t check_window_shape(int rows_b, int T, int H, int Hkv, int d, int wi
     long long a = 0, b = 0;
     if (!mul_ok((long long)rows_b * T, (long long)H * d, &a) || a >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
     if (!mul_ok((long long)rows_b * (window + sinks), (long long)Hkv * d, &b) || b >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((long long)rows_b * H * (T / 64 + 1) > (1LL << 30)) return KDA_ERR_UNSUPPORTED;        // units of a launch
+    if ((long long)rows_b * H * (T / 64 + 1) > 2 * kMaxUnits) return KDA_ERR_UNSUPPORTED;   // workgroups of 256 threads
     return KDA_OK;
 }
 
@@ -449,6 +452,9 @@ kda_status_t kda_window_prefill(const void* q, const void* k, const void* v, voi
     st = check_window_ptrs(q, k, v, k_cache, v_cache, start, lens, o, nullptr, 0, B, T, H, Hkv, d, window, sinks, q_stride,
                            k_stride, v_stride, dt);
     if (st != KDA_OK || T == 0) return st;
+    // the launch that keeps a sequence's rows has a thread for 16 bytes of each, fewer than 2^32 after rounding up
+    const long long kept = (long long)sinks + (window < T ? window : T);
+    if (k_cache && kept * ((long long)Hkv * d * (long long)elem_size(dt) / 16) > (1LL << 31)) return KDA_ERR_UNSUPPORTED;
     kda::WindowArgs a;
     memset(&a, 0, sizeof(a));
     a.q = q;

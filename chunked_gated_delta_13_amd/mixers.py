@@ -65,6 +65,27 @@ def _rows(name, t, dtype, shape, device, lead):
     return step
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _fits(*sizes):
+    """Sizes are 32-bit numbers at the library's entry points."""
+    if max(sizes) > _INT_MAX or min(sizes) < -_INT_MAX:
+        raise ValueError(f"sizes must fit 32 bits, got {max(sizes, key=abs)}")
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace if it is large enough, else a new one; returns it and its bytes."""
+    if workspace is None:
+        return (None, 0) if need == 0 else (torch.empty(need, dtype=torch.uint8, device=dev), need)
+    if workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    size = workspace.numel() * workspace.element_size()
+    return (torch.empty(need, dtype=torch.uint8, device=dev), need) if size < need else (workspace, size)
+
+
 def _hip(t, where):
     dev = t.device
     if dev.type != "cuda":
@@ -109,6 +130,7 @@ def conv_prefill(x, w, bias=None, state=None, *, lens=None, silu=True, y=None, s
     _check("w", w, dt, (D, W), dev)
     if bias is not None:
         _check("bias", bias, dt, (D,), dev)
+    _fits(B, T, D, W)
     keep = (B, W - 1, D)
     if state is not None:
         _check("state", state, dt, keep, dev)
@@ -141,6 +163,7 @@ def conv_step(x, w, state, bias=None, *, silu=True, y=None):
     _check("w", w, dt, (D, W), dev)
     if bias is not None:
         _check("bias", bias, dt, (D,), dev)
+    _fits(N, D, W)
     _check("state", state, dt, (N, W - 1, D), dev)
     if y is None:
         y = x.new_empty((N, D))
@@ -182,6 +205,7 @@ def _ssm_bytes(device, *shape):   # a plan depends on the shape and the device's
 
 def ssm_workspace_bytes(B, T, H, G, n, p, dtype=torch.bfloat16, seg_len=0):
     """Device workspace bytes of ssm_prefill for this shape on the current device."""
+    _fits(B, T, H, G, n, p, seg_len)
     return int(_lib.load().kda_ssm_prefill_workspace_bytes(B, T, H, G, n, p, _code(dtype), seg_len))
 
 
@@ -202,6 +226,7 @@ def ssm_prefill(x, dt, A, Bm, Cm, S0=None, *, D=None, z=None, dt_bias=None, lens
     ty = x.dtype
     code = _code(ty)
     (H, G, n, p), strides = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    _fits(B, T, H, G, n, p, seg_len)
     state = (B, H, n, p)
     if S0 is not None:
         _check("S0", S0, torch.float32, state, dev)
@@ -217,9 +242,7 @@ def ssm_prefill(x, dt, A, Bm, Cm, S0=None, *, D=None, z=None, dt_bias=None, lens
         S_T = torch.empty(state, dtype=torch.float32, device=dev)
     lib = _lib.load()
     need = _ssm_bytes(dev.index, B, T, H, G, n, p, code, seg_len)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _workspace(workspace, need, dev)
     _call(lib.kda_ssm_prefill, dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
           _ptr(S0), _ptr(lens), _ptr(y), _ptr(S_T), B, T, H, G, n, p, *strides, code, seg_len, _ptr(workspace),
           ws_bytes)
@@ -236,6 +259,7 @@ def ssm_step(x, dt, A, Bm, Cm, S, *, D=None, z=None, dt_bias=None, y=None):
     ty = x.dtype
     code = _code(ty)
     (H, G, n, p), strides = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 1)
+    _fits(N, H, G, n, p)
     _check("S", S, torch.float32, (N, H, n, p), dev)
     if y is None:
         y = x.new_empty((N, H, p))
@@ -276,6 +300,7 @@ def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cach
     ty = q.dtype
     code = _code(ty)
     (H, Hkv, d), strides = _window_inputs(q, k, v, 2)
+    _fits(B, T, H, Hkv, d, window, sinks)
     if (k_cache is None) != (v_cache is None):
         raise ValueError("k_cache and v_cache come together")
     if k_cache is not None:
@@ -290,7 +315,7 @@ def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cach
     else:
         _check("o", o, ty, (B, T, H, d), dev)
     _call(_lib.load().kda_window_prefill, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(start),
-          _ptr(lens), _ptr(o), B, T, H, Hkv, d, window, sinks, d ** -0.5 if scale is None else scale, *strides, code)
+          _ptr(lens), _ptr(o), B, T, H, Hkv, d, window, sinks, max(d, 1) ** -0.5 if scale is None else scale, *strides, code)
     return o
 
 
@@ -302,6 +327,7 @@ def _window_bytes(device, *shape):
 
 def window_step_workspace_bytes(N, H, Hkv, d, window, sinks=0, dtype=torch.bfloat16):
     """Device workspace bytes of window_step for this shape on the current device."""
+    _fits(N, H, Hkv, d, window, sinks)
     return int(_lib.load().kda_window_step_workspace_bytes(N, H, Hkv, d, window, sinks, _code(dtype)))
 
 
@@ -315,6 +341,7 @@ def window_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, 
     ty = q.dtype
     code = _code(ty)
     (H, Hkv, d), strides = _window_inputs(q, k, v, 1)
+    _fits(N, H, Hkv, d, window, sinks)
     _check("k_cache", k_cache, ty, (N, sinks + window, Hkv, d), dev)
     _check("v_cache", v_cache, ty, (N, sinks + window, Hkv, d), dev)
     _check("pos", pos, torch.int32, (N,), dev)
@@ -324,9 +351,7 @@ def window_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, 
         _check("o", o, ty, (N, H, d), dev)
     lib = _lib.load()
     need = _window_bytes(dev.index, N, H, Hkv, d, window, sinks, code)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _workspace(workspace, need, dev)
     _call(lib.kda_window_step, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(o), N, H,
-          Hkv, d, window, sinks, d ** -0.5 if scale is None else scale, *strides, code, _ptr(workspace), ws_bytes)
+          Hkv, d, window, sinks, max(d, 1) ** -0.5 if scale is None else scale, *strides, code, _ptr(workspace), ws_bytes)
     return o

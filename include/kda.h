@@ -309,7 +309,10 @@ kda_status_t kda_chunk_prefill_noalloc(const void *q, const void *k, const void 
  * (DEVICE int32 [B], or NULL: every sequence has T tokens) holds the tokens of each sequence of a
  * padded batch; values outside [0, T] are clamped on the device, the rows behind a sequence's end
  * are not read for its results, and the output rows there are left as they were.  Values of live
- * tokens must be finite: a NaN or an infinity may reach the other tokens of its block of 64.
+ * tokens must be finite: in the scan a NaN or an infinity may reach the other tokens of its block of 64
+ * and every token after it, in the attention the tokens up to 127 before it and up to 127 past the end
+ * of its window; other sequences never.  A launch holds fewer than 2^32 threads: calls of more units than
+ * stated below return KDA_ERR_UNSUPPORTED.
  */
 
 /*
@@ -331,7 +334,7 @@ kda_status_t kda_chunk_prefill_noalloc(const void *q, const void *k, const void 
  *   silu       0: act is the identity, else x * sigmoid(x)
  * T == 0 is valid: state_out receives state_in (or zeros).  B == 0 or D == 0 is a no-op.  Pointers
  * need only the alignment of their elements; rows that all start on 16-byte boundaries run faster.
- * B is at most 65535.
+ * B is at most 65535, D at most 2^28.
  */
 kda_status_t kda_conv_prefill(const void *x, const void *w, const void *bias, const void *state_in,
                               const int *lens, void *y, void *state_out, int B, int T, int D, int W,
@@ -368,8 +371,8 @@ kda_status_t kda_conv_step(const void *x, const void *w, const void *bias, void 
  *              (a multiple of 64; >= T = no split).  The result does not depend on it beyond rounding.
  *   workspace  kda_ssm_prefill_workspace_bytes(...) bytes of device memory (may be NULL when that is 0),
  *              written before it is read; calls that overlap in time need one each
- * Rows of x, Bm, Cm and z start on 16-byte boundaries; H * p and the strides of these inputs are at most
- * 2^22 elements.  T == 0 is valid: S_T receives S0 (or zeros).
+ * Rows of x, Bm, Cm and z start on 16-byte boundaries; H * p and the five strides are at most 2^22
+ * elements, B * H at most 2^22, and B * H segments of a split sequence at most 2^20.  T == 0 is valid: S_T receives S0 (or zeros).
  * B == 0 or H == 0 is a no-op.  States and exponents are fp32; with bf16 inputs the state is rounded to
  * bf16 only as the operand of S^T C, never in its update.
  */
@@ -412,7 +415,8 @@ kda_status_t kda_ssm_step(const void *x, const void *dt, const float *A, const v
  *   o          [B, T, H, d]    dtype  (out)
  *   d          64 or 128;  window >= 1;  sinks >= 0;  scale > 0
  * Rows of q, k and v start on 16-byte boundaries.  T == 0, B == 0 or H == 0 is a no-op.  B is at most
- * 65535.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded to bf16 as the
+ * 65535, H at most 65536, T and window + sinks at most 2^29, B H (T / 64 + 1) at most 2^23, and the kept
+ * rows of one sequence (sinks and the smaller of window and T) at most 32 GiB per cache.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded to bf16 as the
  * operand of the product with v.
  */
 kda_status_t kda_window_prefill(const void *q, const void *k, const void *v, void *k_cache,
