@@ -2,7 +2,8 @@
 
 Every .hip translation unit is compiled in parallel with hipcc for gfx950, then
 linked with the host API into ``libkda.so`` next to this file.  Packed fp32
-arithmetic is disabled for all device code (``-packed-fp32-ops`` off).
+arithmetic is disabled for all device code (``-packed-fp32-ops`` off).  The token
+mixers' binding (``_mixers.so``, host code against torch's headers) is built beside it.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -18,6 +20,7 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libkda.so")
 PEAKS_LIB = os.path.join(HERE, "libkda_peaks.so")
+BINDING = os.path.join(HERE, "_mixers.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
@@ -55,21 +58,42 @@ def _link(objs, out):
     os.replace(tmp, out)
 
 
+def build_binding() -> str:
+    """_mixers.so from csrc/binding/: a Python extension that links to torch, which is imported
+    before it, and is handed libkda's entry points at run time."""
+    import torch
+    top = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(top, "include"),
+           "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"), "-isystem", "/opt/rocm/include",
+           os.path.join(CSRC, "binding", "mixers_binding.cpp"), "-o", tmp, "-L" + os.path.join(top, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False) -> str:
-    """libkda.so from csrc/*.hip and csrc/*.cpp, and the benchmark's bandwidth probes
-    (libkda_peaks.so, from csrc/bench/) beside it."""
+    """libkda.so from csrc/*.hip and csrc/*.cpp, the token mixers' binding, and the benchmark's
+    bandwidth probes (libkda_peaks.so, from csrc/bench/) beside it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
                   if f.endswith(".hip") or f.endswith(".cpp"))
     probe_srcs = sorted(os.path.join(CSRC, "bench", f) for f in os.listdir(os.path.join(CSRC, "bench"))
                         if f.endswith(".hip"))
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + len(probe_srcs))) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(_compile, srcs))
         probe_objs = list(ex.map(_compile, probe_srcs))
+        binding.result()
     _link(objs, LIB)
     _link(probe_objs, PEAKS_LIB)
     if verbose:
-        print(f"built {LIB} and {PEAKS_LIB}")
+        print(f"built {LIB}, {BINDING} and {PEAKS_LIB}")
     return LIB
 
 

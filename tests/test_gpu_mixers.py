@@ -290,3 +290,67 @@ def test_window_cache_past_32_bits():
     assert float((o[N - 1].double() - want).abs().max()) <= want * (2.0 ** -8 + 2.0 ** -22)
     assert bool((o[:N - 1] == 2.0).all())
     assert bool((vc[N - 1, 0] == 2.0).all()) and bool((vc[N - 1, 1] == 0.0).all())
+
+
+def test_binding_refuses_rows_it_cannot_describe():
+    """Row strides that the library's one stride cannot say, wrong types, shapes and workspaces: all refused on
+    the host, before any launch, and with the argument's name."""
+    kda = _kda()
+    w = torch.zeros(16, 4, device="cuda")
+    base = torch.zeros(4, 6, 48, device="cuda")
+    for bad in (base[..., :32:2], base[..., 8:24].transpose(-1, -2).contiguous().transpose(-1, -2)):
+        with pytest.raises(ValueError, match="x: the elements of a token must be contiguous"):
+            kda.conv_prefill(bad, w)
+    part = base[..., 8:24]
+    for bad in (part[:, :5], part.transpose(0, 1), part[:, :1].expand(4, 6, 16), part[:1].expand(4, 6, 16)):
+        with pytest.raises(ValueError, match="x: sequence b must start at row b"):
+            kda.conv_prefill(bad, w)
+    for good in (part, part[:1, :5], part[:, :1], part[:, :0], part[:0]):
+        y, state = kda.conv_prefill(good, w)
+        assert y.shape == good.shape and state.shape == (good.shape[0], 3, 16)
+    with pytest.raises(TypeError, match="w must be torch.float32, got torch.bfloat16"):
+        kda.conv_prefill(part, w.bfloat16())
+    with pytest.raises(ValueError, match=r"w must have shape \(16, 4\), got \(8, 4\)"):
+        kda.conv_prefill(part, w[:8])
+    with pytest.raises(ValueError, match="state must be on"):
+        kda.conv_step(part[:, 0], w, torch.zeros(4, 3, 16))
+    with pytest.raises(ValueError, match="y must be contiguous"):
+        kda.conv_step(part[:, 0], w, torch.zeros(4, 3, 16, device="cuda"), y=part[:, 0])
+    with pytest.raises(TypeError, match="inputs must be bfloat16 or float32"):
+        kda.conv_step(part[:, 0].half(), w, torch.zeros(4, 3, 16, device="cuda"))
+    with pytest.raises(TypeError, match="bias must be a tensor"):
+        kda.conv_step(part[:, 0], w, torch.zeros(4, 3, 16, device="cuda"), 1.0)
+
+    x = torch.zeros(2, 70, 4, 64, device="cuda")
+    dt, A, Bm = torch.zeros(2, 70, 4, device="cuda"), torch.zeros(4, device="cuda"), torch.zeros(2, 70, 2, 64, device="cuda")
+    with pytest.raises(ValueError, match=r"Cm must have shape \(2, 70, 2, 64\)"):
+        kda.ssm_prefill(x, dt, A, Bm, Bm[..., :1, :])
+    with pytest.raises(ValueError, match="x: the elements"):
+        kda.ssm_prefill(x.transpose(2, 3).contiguous().transpose(2, 3), dt, A, Bm, Bm)
+    with pytest.raises(ValueError, match="workspace must be on"):
+        kda.ssm_prefill(x, dt, A, Bm, Bm, seg_len=64, workspace=torch.zeros(1 << 20))
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        kda.ssm_prefill(x, dt, A, Bm, Bm, seg_len=64, workspace=torch.zeros(1 << 10, 1 << 10, device="cuda").t())
+    with pytest.raises(ValueError, match="32 bits"):
+        kda.ssm_prefill(x, dt, A, Bm, Bm, seg_len=2 ** 32 + 64)
+    with pytest.raises(TypeError):
+        kda.ssm_prefill(x, dt, A, Bm, Bm, seg_len=64.0)
+    with pytest.raises(RuntimeError, match="ssm_prefill") as e:
+        kda.ssm_prefill(x, dt, A, Bm, Bm, seg_len=100)
+    assert isinstance(e.value, kda.KDAError) and e.value.status == 1
+
+    q = torch.zeros(2, 70, 4, 64, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        kda.window_prefill(q, q, q, 2 ** 32 + 5)
+    with pytest.raises(ValueError, match="come together"):
+        kda.window_prefill(q, q, q, 5, k_cache=torch.zeros(2, 5, 4, 64, device="cuda"))
+    with pytest.raises(ValueError, match=r"k_cache must have shape \(2, 7, 4, 64\)"):
+        c = torch.zeros(2, 5, 4, 64, device="cuda")
+        kda.window_prefill(q, q, q, 5, 2, k_cache=c, v_cache=c)
+    with pytest.raises(TypeError, match="k_cache must be a tensor"):
+        kda.window_step(q[:, 0], q[:, 0], q[:, 0], None, None, _i32(0, 0), 5)
+    with pytest.raises(TypeError, match="pos must be torch.int32"):
+        c = torch.zeros(2, 5, 4, 64, device="cuda")
+        kda.window_step(q[:, 0], q[:, 0], q[:, 0], c, c.clone(), _i32(0, 0).long(), 5)
+    with pytest.raises(kda.KDAError):
+        kda.window_prefill(q, q, q, 5, scale=float("nan"))

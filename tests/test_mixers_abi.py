@@ -254,54 +254,19 @@ def test_window_binding_refuses_what_it_cannot_run():
         kda.window_step(q[:, 0], q[:, 0], q[:, 0], q, q, torch.zeros(2, dtype=torch.int32), 4)
 
 
-def test_binding_refuses_sizes_past_32_bits_and_foreign_workspaces():
-    """What the C integers would cut off is refused before the call, and so is a workspace elsewhere."""
-    import torch
-    from chunked_gated_delta_13_amd import mixers
-    with pytest.raises(ValueError, match="32 bits"):
-        mixers._fits(1, 2 ** 32 + 5)
-    with pytest.raises(ValueError, match="32 bits"):
-        mixers._fits(1, -2 ** 32)
+def test_binding_refuses_sizes_past_32_bits():
+    """What the C integers would cut off is refused before the call."""
     with pytest.raises(ValueError, match="32 bits"):
         kda.window_step_workspace_bytes(1, 8, 2, 128, 2 ** 32 + 20)
     with pytest.raises(ValueError, match="32 bits"):
-        kda.ssm_workspace_bytes(1, 100, 1, 1, 64, 64, seg_len=2 ** 32 + 64)
-    mixers._fits(0, 2 ** 31 - 1)
-    cpu = torch.device("cpu")
-    assert mixers._workspace(None, 0, cpu) == (None, 0)
-    w = torch.empty(64, dtype=torch.float32)
-    assert mixers._workspace(w, 256, cpu) == (w, 256)
-    grown, size = mixers._workspace(w, 257, cpu)
-    assert grown is not w and size == 257 == grown.numel()
-    with pytest.raises(ValueError, match="workspace must be on"):
-        mixers._workspace(torch.empty(64, device="meta"), 16, cpu)
-    with pytest.raises(ValueError, match="workspace must be contiguous"):
-        mixers._workspace(torch.empty(8, 8).t(), 16, cpu)
+        kda.ssm_workspace_bytes(1, 100, 1, 1, 64, 64, seg_len=-2 ** 32 + 64)
+    assert kda.window_step_workspace_bytes(1, 8, 2, 128, 2 ** 31 - 1) == 0
 
 
-@pytest.mark.parametrize("lead", [1, 2])
-def test_binding_rows_of_a_projection(lead):
-    """Row strides that the library's one stride can and cannot say."""
-    import torch
-    from chunked_gated_delta_13_amd.mixers import _rows
-    base = torch.empty(4, 6, 40)
-    rows = base if lead == 2 else base.flatten(0, 1)
-    cpu, f32 = torch.device("cpu"), torch.float32
-    part = rows[..., 8:24]
-    assert _rows("x", part, f32, part.shape, cpu, lead) == 40
-    heads = part.unflatten(-1, (2, 8))
-    assert _rows("x", heads, f32, heads.shape, cpu, lead) == 40
-    for bad in (rows[..., ::2], rows.unflatten(-1, (4, 10)).transpose(-1, -2), rows.unflatten(-1, (4, 10))[..., :8]):
-        with pytest.raises(ValueError, match="contiguous"):
-            _rows("x", bad, f32, bad.shape, cpu, lead)
-    with pytest.raises(TypeError):
-        _rows("x", part, torch.bfloat16, part.shape, cpu, lead)
-    with pytest.raises(ValueError, match="shape"):
-        _rows("x", part, f32, part.shape[:-1] + (15,), cpu, lead)
-    if lead == 2:
-        for bad in (base[:, :5], base.transpose(0, 1), base[:, :1].expand(4, 6, 40), base[:1].expand(4, 6, 40)):
-            with pytest.raises(ValueError, match="sequence b"):
-                _rows("x", bad, f32, bad.shape, cpu, 2)
-        assert _rows("x", base[:1, :5], f32, (1, 5, 40), cpu, 2) == 40
-        assert _rows("x", base[:, :1], f32, (4, 1, 40), cpu, 2) == 240
-        assert _rows("x", base[:, :0], f32, (4, 0, 40), cpu, 2) >= 0
+def test_binding_refuses_what_is_no_tensor():
+    with pytest.raises(TypeError, match="x must be a tensor"):
+        kda.conv_step(None, None, None)
+    with pytest.raises(TypeError, match="x must be a tensor"):
+        kda.ssm_prefill([1.0], None, None, None, None)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        kda.window_prefill(3, None, None, 4)
