@@ -249,12 +249,13 @@ kda_status_t check_window_ptrs(const void* q, const void* k, const void* v, cons
     return KDA_OK;
 }
 
-// Ranges of cache rows of a step: enough workgroups for two per compute unit, at least 256 rows each.
+// Ranges of cache rows of a step: enough workgroups for two per compute unit, each at least one tile for
+// every wave (one sequence of 8 kv heads over 4100 rows: 10.3 us with ranges of 128 rows, 11.3 with 256).
 void window_step_plan(int N, int H, int Hkv, int window, int sinks, int* n_split, int* split_len) {
     const long long slots = (long long)window + sinks;
     const long long units = (long long)N * Hkv * ((H / Hkv + 15) / 16);
     long long want = units > 0 ? 2LL * cu_count() / units : 1;
-    if (want > slots / 256) want = slots / 256;
+    if (want > slots / 128) want = slots / 128;
     if (want < 1) want = 1;
     const long long len = ((slots + want - 1) / want + 127) / 128 * 128;   // whole tiles of the four waves
     *n_split = (int)((slots + len - 1) / len);

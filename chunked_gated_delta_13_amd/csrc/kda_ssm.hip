@@ -141,22 +141,24 @@ struct ChunkDecay {
     float factor;      // 2^sum of the whole chunk
 };
 
-// By one wave, lane = token.
-template <typename T>
+// By one wave, lane = token.  OUT: with the numbers that outputs take.
+template <typename T, bool OUT>
 __device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bool live, float A2, int lane) {
     const float d = live ? softplus_f32(raw) : 0.0f;
     const double s = wave_prefix(live ? (double)fmaxf(d * A2, kDecayMin) : 0.0);
     const double end = last_lane(s);
     const float hi = (float)s;
-    c->hi[lane] = hi;
-    if constexpr (sizeof(T) == 4) {
-        c->lo[lane] = (float)(s - (double)hi);
-        c->dt[lane] = d;
-    } else {
-        // 2^(c_i - c_j) dt_j as one exponential; dt = 0 gives +inf here and a factor of 0
-        c->lo[lane] = hi - __log2f(d);
+    if constexpr (OUT) {
+        c->hi[lane] = hi;
+        if constexpr (sizeof(T) == 4) {
+            c->lo[lane] = (float)(s - (double)hi);
+            c->dt[lane] = d;
+        } else {
+            // 2^(c_i - c_j) dt_j as one exponential; dt = 0 gives +inf here and a factor of 0
+            c->lo[lane] = hi - __log2f(d);
+        }
+        c->e[lane] = fast_exp2(hi);
     }
-    c->e[lane] = fast_exp2(hi);
     c->w[lane] = fast_exp2((float)(end - s)) * d;
     if (lane == 0) {
         c->sum = (float)end;
@@ -412,7 +414,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
     typedef typename Mix::vec4 vec4;
     constexpr int WC = Mix::WC, NCT = Mix::NCT;
     constexpr uint32_t ES = sizeof(T), ROW_P = P * ES;
-    constexpr int NBC = AHEAD ? 3 : 1, NXM = AHEAD ? 2 : 1, ND = AHEAD ? 3 : 2;
+    constexpr int NBC = AHEAD ? 3 : (OUT ? 1 : 2), NXM = AHEAD || !OUT ? 2 : 1, ND = AHEAD ? 3 : 2 * NW;
     // LDS: B, C (with outputs), M (likewise), x tiles (elements), then the numbers of two or three chunks
     constexpr int oC = NBC * kC * N, oM = OUT ? 2 * oC : oC, oX = oM + (OUT ? NXM * kC * kC : 0), oEnd = oX + NXM * kC * P;
     __shared__ __attribute__((aligned(16))) T smem[oEnd];
@@ -502,7 +504,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
     auto request_dt = [&](int ahead) {
         gdt = buffer_load1(dp, make_rows(dp + ahead * a.dt_stride, rows_at(ahead), dt_step, ES), lane * dt_step);
     };
-    auto decay = [&](int ahead, int buf) { chunk_decay<T>(sD + buf, gdt + bias, ahead + lane < left, A2, lane); };
+    auto decay = [&](int ahead, int buf) { chunk_decay<T, OUT>(sD + buf, gdt + bias, ahead + lane < left, A2, lane); };
     vec4 zv[4][NCT];
     auto request_z = [&](int ahead) {
         const buffer_t zbuf = make_rows(zp + ahead * a.z_stride, gated ? rows_at(ahead) : 0, z_step, ROW_P);
@@ -521,52 +523,77 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
         if constexpr (OUT) yp += (long long)kC * a.H * P;
         left -= kC;
     };
-    // The wave that forms the decays, and the waves 0 .. MW - 1 that form M.  Of two waves on a SIMD the
-    // older one is served first and has time left at the barrier: with all eight sharing this work, waves
-    // 0 - 3 waited 3000 of 9300 cycles a chunk for waves 4 - 7.
-    constexpr int DW = AHEAD ? NW / 2 - 1 : NW - 1, MW = DW;
-
     if constexpr (!AHEAD) {
-        mx.set_bc(sB, sC, lane);
-        mx.cb.set(sB, lane);
-        mx.rm.set(sM, lane);
-        mx.set_x(sX, wave, lane);
+        // Decays are a long chain on one wave: NW chunks' at a time, a chunk per wave, NW chunks ahead.  (By one
+        // wave chunk by chunk, while the others wait: 92 us for 20001 tokens of 16 heads.)
+        auto decay_many = [&](int c) {
+            decay((NW + wave) * kC, (c + NW + wave) & (2 * NW - 1));
+            request_dt((2 * NW + wave) * kC);
+        };
         if (left > 0) {
-            if (wave == DW) {
-                request_dt(0);
-                decay(0, 0);
-                request_dt(kC);
-            }
+            request_dt(wave * kC);
+            decay(wave * kC, wave);
+            request_dt((NW + wave) * kC);
             request_bc(0);
             request_x(0);
         }
-        for (int par = 0; left > 0; par ^= 1) {
-            const KDA_LDS ChunkDecay* cd = sD + par;
-            put_bc(0);
-            gx.put(sX, wave, lane);
-            __syncthreads();
-            if constexpr (OUT) {
+        if constexpr (!OUT) {
+            // two sets of tiles: one barrier per chunk
+            if (left > 0) {
+                put_bc(0);
+                gx.put(sX, wave, lane);
+                request_bc(kC);
+                request_x(kC);
+                __syncthreads();
+            }
+            for (int c = 0, par = 0; left > 0; ++c, par ^= 1) {
+                const KDA_LDS ChunkDecay* cd = sD + (c & (2 * NW - 1));
+                put_bc(par ^ 1);
+                gx.put(sX + (par ^ 1) * kC * P, wave, lane);
+                request_bc(2 * kC);
+                request_x(2 * kC);
+                mx.cb.set(sB + par * kC * N, lane);
+                mx.set_x(sX + par * kC * P, wave, lane);
+                Frag<T> xt[2][NCT];
+                mx.load_x(xt);
+                mx.update(S, xt, cd, lane);
+                if ((c & (NW - 1)) == 0) decay_many(c);
+                total += cd->sum;
+                __syncthreads();
+                advance();
+            }
+        } else {
+            mx.set_bc(sB, sC, lane);
+            mx.cb.set(sB, lane);
+            mx.rm.set(sM, lane);
+            mx.set_x(sX, wave, lane);
+            for (int c = 0; left > 0; ++c) {
+                const KDA_LDS ChunkDecay* cd = sD + (c & (2 * NW - 1));
+                put_bc(0);
+                gx.put(sX, wave, lane);
+                __syncthreads();
                 request_z(0);
                 // (the first tile is taken as new in every chunk: its addresses are not worth registers)
-                if (wave < MW) mx.template mix_every<2>(sM, cd, pinned_s(wave), MW, lane);
+                mx.template mix_every<2>(sM, cd, pinned_s(wave), NW, lane);
+                if ((c & (NW - 1)) == 0) decay_many(c);
+                __syncthreads();
+                Frag<T> xt[2][NCT];
+                mx.load_x(xt);
+                mx.outputs(S, xt, zv, gated, Dh, cd, y_buffer(), y_off, y_step, lane);
+                // requested here, where the outputs' registers are free again
+                request_bc(kC);
+                request_x(kC);
+                mx.update(S, xt, cd, lane);
+                total += cd->sum;
+                __syncthreads();
+                advance();
             }
-            if (wave == DW) {
-                decay(kC, par ^ 1);
-                request_dt(2 * kC);
-            }
-            if constexpr (OUT) __syncthreads();
-            Frag<T> xt[2][NCT];
-            mx.load_x(xt);
-            if constexpr (OUT) mx.outputs(S, xt, zv, gated, Dh, cd, y_buffer(), y_off, y_step, lane);
-            // requested here, where the outputs' registers are free again
-            request_bc(kC);
-            request_x(kC);
-            mx.update(S, xt, cd, lane);
-            total += cd->sum;
-            __syncthreads();
-            advance();
         }
     } else if (left > 0) {
+        // The wave that forms the decays, and the waves 0 .. MW - 1 that form M.  Of two waves on a SIMD the
+        // older one is served first and has time left at the barrier: with all eight sharing this work, waves
+        // 0 - 3 waited 3000 of 9300 cycles a chunk for waves 4 - 7.
+        constexpr int DW = NW / 2 - 1, MW = DW;
         // chunks 0 and 1 of B and C, chunk 0 of x, M of chunk 0
         request_bc(0);
         request_x(0);
