@@ -691,7 +691,11 @@ __global__ __launch_bounds__(256) void kda_ssm_join_kernel(float* ws, const floa
     }
 }
 
-// One token: a workgroup owns one (sequence, head) state, P/4 groups of four columns x 16 row groups.
+// One token: a workgroup owns one (sequence, head) state, P/4 groups of four columns x 16 row groups, so that
+// each XCD streams a contiguous range of states, past the caches.  A thread's rows are all requested
+// before the first is used and stored together after the last: 256 sequences of 56 heads, n = p = 128
+// (1.89 GB) take 307 us, 6.2 TB/s; each row stored as soon as it is ready, reads and writes mix in
+// memory and it takes 329.
 template <int N, int P, typename T>
 __global__ __launch_bounds__(4 * P) void kda_ssm_step_kernel(const SsmArgs a) {
     constexpr int NCG = P / 4, NRG = 16, NTH = NCG * NRG, NW = NTH / 64, RPT = N / NRG;
@@ -725,8 +729,12 @@ __global__ __launch_bounds__(4 * P) void kda_ssm_step_kernel(const SsmArgs a) {
             S[m][j] = fmaf(dec, S[m][j], bi * x[j]);
             y[j] = fmaf(ci, S[m][j], y[j]);
         }
-        __builtin_nontemporal_store(S[m], reinterpret_cast<f32x4_t*>(Sb + (long long)i * P));
     }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < RPT; ++m)
+        __builtin_nontemporal_store(S[m], reinterpret_cast<f32x4_t*>(Sb + (long long)(rg + NRG * m) * P));
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int o = NCG; o < 64; o <<= 1)
 #pragma unroll
