@@ -427,14 +427,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefi
 
     // unit = (b, segment, h), heads fastest: the heads of a segment share B and C, and each XCD takes a
     // contiguous range of units
-    const long long unit = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
-    if (unit >= a.n_units) return;
-    const int h = (int)(unit % a.H);
-    const long long bs = unit / a.H;
-    const int s = (int)(bs % a.n_seg_launch);
-    const int b = (int)(bs / a.n_seg_launch);
+    const uint32_t unit = (blockIdx.x & 7) * (uint32_t)a.per_xcd + (blockIdx.x >> 3);
+    if (unit >= (uint32_t)a.n_units) return;
+    const int h = (int)(unit % (uint32_t)a.H);
+    const uint32_t bs = unit / (uint32_t)a.H;
+    const int s = (int)(bs % (uint32_t)a.n_seg_launch);
+    const int b = (int)(bs / (uint32_t)a.n_seg_launch);
     const long long bh = (long long)b * a.H + h;
-    const int grp = h / (a.H / a.G);
+    const int grp = (int)((uint32_t)h / ((uint32_t)a.H / (uint32_t)a.G));
 
     long long len = a.T;
     if (a.lens) {
@@ -699,10 +699,10 @@ __global__ __launch_bounds__(256) void kda_ssm_join_kernel(float* ws, const floa
 template <int N, int P, typename T>
 __global__ __launch_bounds__(4 * P) void kda_ssm_step_kernel(const SsmArgs a) {
     constexpr int NCG = P / 4, NRG = 16, NTH = NCG * NRG, NW = NTH / 64, RPT = N / NRG;
-    const long long nh = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
-    if (nh >= a.n_units) return;
-    const long long n = nh / a.H;
-    const int h = (int)(nh % a.H), grp = h / (a.H / a.G);
+    const uint32_t unit = (blockIdx.x & 7) * (uint32_t)a.per_xcd + (blockIdx.x >> 3);
+    if (unit >= (uint32_t)a.n_units) return;
+    const long long nh = unit, n = unit / (uint32_t)a.H;
+    const int h = (int)(unit % (uint32_t)a.H), grp = (int)((uint32_t)h / ((uint32_t)a.H / (uint32_t)a.G));
     const int tid = threadIdx.x, cg = tid % NCG, rg = tid / NCG, lane = tid & 63, wave = tid >> 6, col = 4 * cg;
     float* Sb = a.S_T + nh * (long long)(N * P) + col;
     f32x4_t S[RPT];

@@ -23,13 +23,27 @@ __device__ __forceinline__ int ring_row(uint32_t p, int sinks, int window) {
     return p < (uint32_t)sinks ? (int)p : sinks + (int)((p - (uint32_t)sinks) % (uint32_t)window);
 }
 
-__device__ __forceinline__ float max_over_groups(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+// Over the four lanes 16 apart that share a query.  SWAP: rows of 16 lanes are swapped pairwise, then halves,
+// on the vector unit; else the values go round through LDS, which takes longer (ragged prompts of the
+// smallest kind 11.8 us instead of 11.4, one token 10.1 instead of 9.8) but leaves the registers of the
+// kernel of 32 queries per wave as they are (the swaps make it spill: 2.55 ms instead of 1.59).
+template <bool SWAP, typename F> __device__ __forceinline__ float over_groups(float v, F f) {
+    if constexpr (SWAP) {
+        const uint32_t u = __float_as_uint(v);
+        const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        const uint32_t w = __float_as_uint(f(__uint_as_float(a[0]), __uint_as_float(a[1])));
+        const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+        return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+    } else {
+        v = f(v, __shfl_xor(v, 16));
+        return f(v, __shfl_xor(v, 32));
+    }
 }
-__device__ __forceinline__ float sum_over_groups(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+template <bool SWAP> __device__ __forceinline__ float max_over_groups(float v) {
+    return over_groups<SWAP>(v, [](float x, float y) { return fmaxf(x, y); });
+}
+template <bool SWAP> __device__ __forceinline__ float sum_over_groups(float v) {
+    return over_groups<SWAP>(v, [](float x, float y) { return x + y; });
 }
 
 // Eight slots of one row in global memory, p at the first one: four at p and four half a row further.
@@ -90,23 +104,21 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
 
     // unit = (b, kv head, query tile, head of the group): consecutive units share keys, and each XCD
     // takes a contiguous range of them
-    long long unit = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
-    if (unit >= a.n_units) return;
-    const int R = a.H / a.Hkv;
+    uint32_t unit = (blockIdx.x & 7) * (uint32_t)a.per_xcd + (blockIdx.x >> 3);
+    if (unit >= (uint32_t)a.n_units) return;
+    const uint32_t R = (uint32_t)a.H / (uint32_t)a.Hkv;
     const int hr = (int)(unit % R);
     unit /= R;
-    const int q0 = (int)(unit % a.q_tiles) * BM;
-    unit /= a.q_tiles;
-    const int hk = (int)(unit % a.Hkv), b = (int)(unit / a.Hkv), h = hk * R + hr;
+    const int q0 = (int)(unit % (uint32_t)a.q_tiles) * BM;
+    unit /= (uint32_t)a.q_tiles;
+    const int hk = (int)(unit % (uint32_t)a.Hkv), b = (int)(unit / (uint32_t)a.Hkv), h = hk * (int)R + hr;
 
-    int len = a.T;
-    if (a.lens) {
-        const int l = a.lens[b];
-        len = l < 0 ? 0 : (l > a.T ? a.T : l);
-    }
-    if (q0 >= len) return;
+    // (both asked for before either is waited for)
+    int len = a.lens ? a.lens[b] : a.T;
     int s = a.start ? a.start[b] : 0;
+    len = len < 0 ? 0 : (len > a.T ? a.T : len);
     if (s < 0) s = 0;
+    if (q0 >= len) return;
     const int window = a.window, sinks = a.sinks;
 
     // Keys in relative positions (0 = the first new token): nsink first tokens, then lo .. hi
@@ -114,7 +126,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
     const int lo = sinks - s > q0 - window + 1 ? sinks - s : q0 - window + 1;
     const int nsink = s >= sinks ? sinks : (sinks < hi + 1 + s ? sinks : hi + 1 + s);
     const int total = nsink + (hi >= lo ? hi - lo + 1 : 0);
-    const int base0 = s > sinks ? (s - sinks) % window : 0;
+    const int base0 = s > sinks ? (int)((uint32_t)(s - sinks) % (uint32_t)window) : 0;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
@@ -252,20 +264,24 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
         }
         if (!done) {
             if (!whole) {
+                // Query i sees the keys from..to of the list, and the first tokens below `first`; all three
+                // from this lane's first key on.
 #pragma unroll
-                for (int kt = 0; kt < 4; ++kt)
+                for (int n = 0; n < NQ; ++n) {
+                    int i = wq + 16 * n + r;
+                    asm volatile("" : "+v"(i));   // (formed here: not worth registers through the loop)
+                    const int at = t0 + 4 * g;
+                    const int out = i - window + 1 - lo, end = nsink + i - lo;
+                    const int from = nsink + (out > 0 ? out : 0) - at, to = (end < total - 1 ? end : total - 1) - at;
+                    const int first = (i + 1 < nsink - s ? i + 1 + s : nsink) - at;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int idx = t0 + 16 * kt + 4 * g + j;
-                        const bool sink = idx < nsink;
-                        const int rel = sink ? idx - s : lo + (idx - nsink);
+                    for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-                        for (int n = 0; n < NQ; ++n) {
-                            const int i = wq + 16 * n + r;
-                            const bool see = idx < total && rel <= i && (sink || i - rel < window);
-                            sT[kt][n][j] = see ? sT[kt][n][j] : -INFINITY;
+                        for (int j = 0; j < 4; ++j) {
+                            const int x = 16 * kt + j;
+                            sT[kt][n][j] = (x >= from && x <= to) || x < first ? sT[kt][n][j] : -INFINITY;
                         }
-                    }
+                }
             }
             bool got = true;
 #pragma unroll
@@ -275,7 +291,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
                 for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) mx = fmaxf(mx, sT[kt][n][j]);
-                mx = fmaxf(m[n], max_over_groups(mx) * sc);
+                mx = fmaxf(m[n], max_over_groups<NQ == 1>(mx) * sc);
                 const float base = mx == -INFINITY ? 0.0f : mx;   // nothing visible yet: all exponentials are 0
                 const float al = fast_exp2(m[n] - base);
                 m[n] = mx;
@@ -322,7 +338,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         const int i = wq + 16 * n + r;
-        const float inv = 1.0f / sum_over_groups(l[n]);
+        const float inv = 1.0f / sum_over_groups<NQ == 1>(l[n]);
         if (i < len) {
             T* op = reinterpret_cast<T*>(a.o) + (((long long)b * a.T + i) * a.H + h) * D + 4 * g;
 #pragma unroll
@@ -383,15 +399,15 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
     __shared__ __attribute__((aligned(16))) char sV_[4][REGION];
     __shared__ float sm[4][16], sl[4][16];
 
-    long long unit = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
-    if (unit >= a.n_units) return;
-    const int split = (int)(unit % a.n_split);
-    unit /= a.n_split;
-    const int R = a.H / a.Hkv, RT = (R + 15) / 16;
-    const int rt = (int)(unit % RT);
-    unit /= RT;
-    const int hk = (int)(unit % a.Hkv);
-    const long long b = unit / a.Hkv;
+    uint32_t unit = (blockIdx.x & 7) * (uint32_t)a.per_xcd + (blockIdx.x >> 3);
+    if (unit >= (uint32_t)a.n_units) return;
+    const int split = (int)(unit % (uint32_t)a.n_split);
+    unit /= (uint32_t)a.n_split;
+    const int R = (int)((uint32_t)a.H / (uint32_t)a.Hkv), RT = (R + 15) / 16;
+    const int rt = (int)(unit % (uint32_t)RT);
+    unit /= (uint32_t)RT;
+    const int hk = (int)(unit % (uint32_t)a.Hkv);
+    const long long b = unit / (uint32_t)a.Hkv;
     const int heads = R - 16 * rt < 16 ? R - 16 * rt : 16;
     const int h0 = hk * R + 16 * rt;
 
@@ -488,7 +504,7 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
                 if (t0 + 16 * kt + 4 * g + j >= k1) sT[kt][j] = -INFINITY;
                 mx = fmaxf(mx, sT[kt][j]);
             }
-        mx = fmaxf(m, max_over_groups(mx) * sc);
+        mx = fmaxf(m, max_over_groups<true>(mx) * sc);
         const float base = mx == -INFINITY ? 0.0f : mx;   // every score so far is below fp32's range: no weight
         const float al = fast_exp2(m - base);
         m = mx;
@@ -514,7 +530,7 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
         }
         wave_order();
     }
-    l = sum_over_groups(l);
+    l = sum_over_groups<true>(l);
 
     // join the waves: every wave's outputs go to its own region as [head][d]
     KDA_LDS float* sO = (KDA_LDS float*)(KDA_LDS char*)sV_[wave];
