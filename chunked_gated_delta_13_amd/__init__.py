@@ -9,6 +9,13 @@ kernels of ``libkda.so``; PyTorch supplies device memory and the current stream.
 Layouts: q, k, log_alpha [B, T, H, dk]; v [B, T, H, dv]; beta [B, T, H];
 S0 / S_T [B, H, dk, dv] (fp32).  q, k, v, o share one dtype (bf16 or fp32);
 log_alpha and beta are fp32.
+
+Beside KDA, the token mixers of mixers.py, each with a prompt and a one-token form:
+
+    y, state = conv_prefill(x, w, bias, state)             # short causal convolution
+    y, S_T   = ssm_prefill(x, dt, A, Bm, Cm, S0, D=D, z=z) # selective state space scan
+    o        = window_prefill(q, k, v, window, sinks, k_cache=kc, v_cache=vc)
+    conv_step, ssm_step, window_step                       # state or cache updated in place
 """
 from __future__ import annotations
 

@@ -9,14 +9,20 @@
 //   S   <- e^{c_63} S + sum_j B_j (e^{c_63 - c_j} dt_j x_j)^T
 // which are products for the matrix cores.  Every exponent is a sum of a's of consecutive tokens,
 // never a quotient of large factors, so nothing overflows that the recurrence itself does not.
-// One workgroup of four waves runs a (sequence, head, segment) with the state in registers: wave w
-// holds p/4 columns of S as accumulator tiles, which are at once the operand of S^T C (with S rounded
-// to bf16 for that product only).  x, B and C are staged once per chunk in LDS and read there both row
-// by row and transposed.  The update must not lose the state's 32 bits: x and B are exact in bf16 and
-// the weighted x is fed as three bf16 parts (24 bits of it), three products instead of one.
-// A long sequence is split into segments: a first pass forms every segment's final state from zero, a
-// small kernel joins them (the transition of a segment is one number per head), and the second pass
-// runs every segment from its entry state.
+// One workgroup of p/16 waves runs a (sequence, head, segment) with the state in registers: a wave holds
+// 16 columns of S as accumulator tiles, which are at once the operand of S^T C (with S rounded to bf16
+// for that product only).  x, B and C are staged once per chunk in LDS and read there both row by row
+// and transposed.  The update must not lose the state's 32 bits: x and B are exact in bf16 and the
+// weighted x is fed as three bf16 parts (24 bits of it), three products instead of one.
+// A long sequence is split into segments where there are fewer (sequence, head) pairs than the GPU holds
+// workgroups: a first pass forms every segment's final state from zero, a small kernel joins them (the
+// transition of a segment is one number per head), and the second pass runs every segment from its entry
+// state.
+// What bounds it: 4 x 16384 tokens of 56 heads, n = p = 128, bf16, take 1.00 ms, 300 TFLOP/s of the
+// formulas' products; the 2.87 GB they cannot do without take 0.58 ms.  A SIMD holds two waves, each a
+// chain LDS - matrix cores - vector unit - LDS, and of 8000 cycles a chunk issues vector instructions in
+// 4300 and products in 2430.  One sequence of 20001 tokens, 16 heads, n = 128, p = 64 takes 90 us, 24 of
+// them the first pass, 9 the join between two launches, 50 the outputs (ten chunks one after the other).
 //
 // Token.  One streaming pass over the state, bound by HBM: 8 bytes of traffic per state element.
 #include "kda_mixers.h"
@@ -403,11 +409,14 @@ template <int N, int P, typename T, int NW> struct Mixer {
 
 }  // namespace
 
-// OUT: with outputs (the pass that runs every segment from its entry state), else final states only.
+// OUT: with outputs (the pass that runs every segment from its entry state), else final states only: two
+// sets of tiles and one barrier per chunk.
 // AHEAD: M of the next chunk is formed beside the outputs of this one, over three sets of B and C tiles,
 // two of x and two of M: one barrier per chunk, and every wave has independent work for the matrix
 // cores, the vector unit and the LDS all through it.  It takes most of the LDS, so one workgroup runs per
-// compute unit; the plain schedule (three barriers) leaves room for two or three.
+// compute unit: taken for p = 128 in bf16, whose eight waves fill it alone (1.00 ms for the long prompts
+// above, 1.22 with the plain schedule of three barriers).  The plain one leaves room for a second
+// workgroup, which p = 64 needs; fp32 tiles leave no room for more sets.
 template <int N, int P, typename T, bool OUT, int NW, bool AHEAD>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void kda_ssm_prefill_kernel(const SsmArgs a) {
     typedef Mixer<N, P, T, NW> Mix;

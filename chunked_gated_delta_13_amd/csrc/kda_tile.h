@@ -52,7 +52,9 @@ template <typename T, int ROWS> __device__ __forceinline__ int tile_at(int r, in
 
 // Row operand of a tile of WIDTH columns (a multiple of 64): a lane's addresses, pinned in registers, so
 // that everything it reads lies at a constant offset from one of them.  `delta` arguments are constant
-// element offsets, by which tiles of one shape share the addresses.
+// element offsets, by which tiles of one shape share the addresses.  The two reads of an operand are
+// volatile: each then stays with its operand.  (The compiler otherwise pairs reads of different operands
+// into one two-address read and sorts their halves with register moves.)
 template <typename T, int ROWS, int WIDTH> struct TileRows {
     typedef typename Vec4<T>::type vec4;
     KDA_LDS T* at[2];   // row r, chunk 4 x + g of a block
