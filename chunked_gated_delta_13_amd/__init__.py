@@ -23,11 +23,11 @@ import ctypes
 
 from . import _lib
 from ._lib import KDAError
-from .mixers import (conv_prefill, conv_step, ssm_prefill, ssm_step, ssm_workspace_bytes, window_prefill, window_step,
-                     window_step_workspace_bytes)
+from .mixers import (conv_prefill, conv_step, ssm_prefill, ssm_step, ssm_workspace_bytes, window_prefill,
+                     window_prefill_workspace_bytes, window_step, window_step_workspace_bytes)
 
 __all__ = ["conv_prefill", "conv_step", "ssm_prefill", "ssm_step", "ssm_workspace_bytes",
-           "window_prefill", "window_step", "window_step_workspace_bytes",
+           "window_prefill", "window_prefill_workspace_bytes", "window_step", "window_step_workspace_bytes",
            "chunk_prefill", "chunk_prefill_ckpt", "chunk_prefill_gate", "chunk_prefill_noalloc",
            "decode_step", "spec_verify", "spec_commit", "prefill_plan", "prefill_workspace_bytes",
            "abi_version", "KDAError", "load_library"]

@@ -61,8 +61,9 @@ SIGNATURES = {
                              _i, _i, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _ll, _i, _i, _vp, _sz, _vp]),
     "kda_ssm_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                           _i, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _ll, _i, _vp]),
+    "kda_window_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "kda_window_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
-                                ctypes.c_float, _ll, _ll, _ll, _i, _vp]),
+                                ctypes.c_float, _ll, _ll, _ll, _i, _vp, _sz, _vp]),
     "kda_window_step_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "kda_window_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                              ctypes.c_float, _ll, _ll, _ll, _i, _vp, _sz, _vp]),

@@ -35,6 +35,7 @@ struct Library {
     decltype(&kda_ssm_prefill_workspace_bytes) ssm_prefill_workspace_bytes;
     decltype(&kda_ssm_prefill) ssm_prefill;
     decltype(&kda_ssm_step) ssm_step;
+    decltype(&kda_window_prefill_workspace_bytes) window_prefill_workspace_bytes;
     decltype(&kda_window_prefill) window_prefill;
     decltype(&kda_window_step_workspace_bytes) window_step_workspace_bytes;
     decltype(&kda_window_step) window_step;
@@ -409,10 +410,10 @@ struct Attention {
     }
 };
 
-// q, k, v, window, sinks, scale, k_cache, v_cache, start, lens, o
+// q, k, v, window, sinks, scale, k_cache, v_cache, start, lens, o, workspace
 PyObject* window_prefill(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     HANDLE_TH_ERRORS
-    if (!arity(nargs, 11)) return nullptr;
+    if (!arity(nargs, 12)) return nullptr;
     const Args a{args};
     const Common c("window_prefill", a.tensor(0, "q"));
     const Attention q(c, a, 3, 6, 2);
@@ -423,11 +424,14 @@ PyObject* window_prefill(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const int b = size(B), t = size(T);
     const float scale = a.scale(5, q.d);
     Pending po(c, a, 10, "o", c.type, q.q.sizes());
+    const Tensor* room = a.optional(11, "workspace");
     const OnDevice on(c.dev);
+    const Workspace ws(c, room, lib.window_prefill_workspace_bytes(b, t, q.H, q.Hkv, q.d, q.window, q.sinks, c.code, start != nullptr));
     const Output& o = po.make(c);
     if (!c.call([&](void* s) {
             return lib.window_prefill(ptr(q.q), ptr(q.k), ptr(q.v), ptr(q.kc), ptr(q.vc), at_type<int>(start), at_type<int>(lens),
-                                      o.ptr(), b, t, q.H, q.Hkv, q.d, q.window, q.sinks, scale, q.qs, q.ks, q.vs, c.code, s);
+                                      o.ptr(), b, t, q.H, q.Hkv, q.d, q.window, q.sinks, scale, q.qs, q.ks, q.vs, c.code, ws.p,
+                                      ws.bytes, s);
         }))
         return nullptr;
     return o.object();

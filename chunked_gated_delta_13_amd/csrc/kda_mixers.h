@@ -69,12 +69,12 @@ struct WindowArgs {
     long long q_stride, k_stride, v_stride;
     int B, T, H, Hkv, window, sinks;
     float scale;
-    int cus;                  // compute units of the device
+    int few;                  // 1: too few queries for 128 of them per workgroup
     int q_tiles;
-    int n_split, split_len;   // ranges of cache rows of the token form
+    int n_split, split_len;   // ranges of keys (token form: of split_len cache rows)
     long long n_units, per_xcd;
-    float* ws_o;              // [N * H, n_split, d] partial outputs of a split step
-    float* ws_ml;             // [N * H, n_split, 2] their maxima (base 2) and sums
+    float* ws_o;              // [rows * H, n_split, d] partial outputs of a split call
+    float* ws_ml;             // [rows * H, n_split, 2] their maxima (base 2) and sums
 };
 
 hipError_t launch_window_prefill(int d, bool f32, const WindowArgs& a, hipStream_t s);

@@ -1,6 +1,7 @@
 // Host side of the token mixers beside KDA: argument validation, launch plans and launches of the
 // short convolution, the state space scan and the window attention.  Nothing here allocates
 // memory or synchronises the host with the device.
+#include <math.h>
 #include <string.h>
 
 #include <atomic>
@@ -262,8 +263,39 @@ void window_step_plan(int N, int H, int Hkv, int window, int sinks, int* n_split
     *split_len = (int)len;
 }
 
-size_t window_step_workspace(int N, int H, int d, int n_split) {
-    return n_split <= 1 ? 0 : (size_t)N * H * n_split * ((size_t)d + 4) * sizeof(float);
+// Partial outputs of `rows` queries' H heads, their maxima and sums, padded to 16 bytes.
+size_t window_workspace(long long rows, int H, int d, int n_split) {
+    return n_split <= 1 ? 0 : (size_t)rows * H * n_split * ((size_t)d + 4) * sizeof(float);
+}
+
+// A prompt's workgroups take 128 queries each where that gives every compute unit one, else 64.  Where these
+// are few too, the keys of a workgroup (at most its window, its queries and the first tokens; without
+// earlier tokens no more than T) are split into ranges of at least two tiles (one in fp32), for at most
+// two workgroups per compute unit (one in fp32), if that shortens the chain: in microseconds, a tile
+// takes 0.65 (d = 64) or 0.9 (d = 128) in bf16 and 2.6 or 4.8 in fp32, the join 3, and a range's outputs
+// are written and read at 3.7 TB/s, so that the best count is the root of tiles / outputs.  Measured with
+// 8 heads on 2, d = 128, bf16: 64 tokens over a window of 4000 65 us in one range, 16 in the 20 taken; 1024 tokens
+// over 1000 26 us in one, 27 in four (stays one); 64 tokens over 200 13.4 us either way.
+void window_prefill_plan(int B, int T, int H, int d, int window, int sinks, kda_dtype_t dt, bool continued, int* few,
+                         int* n_split) {
+    const int cus = cu_count();
+    const bool f32 = dt == KDA_F32;
+    const long long heads = (long long)B * H;
+    *few = heads * ((T + 127LL) / 128) < cus ? 1 : 0;
+    *n_split = 1;
+    const long long units = heads * ((T + 63LL) / 64);
+    if (!*few || units == 0) return;
+    long long keys = (long long)window + sinks + 64;
+    if (!continued && keys > T) keys = T;
+    const long long tiles = (keys + 63) / 64;
+    const double tile_us = f32 ? 0.4 + 0.034 * d : 0.42 + 0.0036 * d, part_us = (double)heads * T * d * 8 / 3.7e6;
+    long long n = (f32 ? 1LL : 2LL) * cus / units;
+    if (n > tiles / (f32 ? 1 : 2)) n = tiles / (f32 ? 1 : 2);
+    const double best = sqrt((double)tiles * tile_us / part_us);
+    if (best < (double)n) n = (long long)best;
+    if (n < 2) return;
+    const double whole = (double)tiles * tile_us, split = (double)((tiles + n - 1) / n) * tile_us + (double)n * part_us + 3.0;
+    if (split < whole) *n_split = (int)n;
 }
 
 bool scale_ok(float scale) { return scale > 0.0f && scale <= 3.0e38f; }
@@ -443,16 +475,29 @@ kda_status_t kda_ssm_step(const void* x, const void* dt, const float* A, const v
     return KDA_OK;
 }
 
+size_t kda_window_prefill_workspace_bytes(int B, int T, int H, int Hkv, int d, int window, int sinks, kda_dtype_t dt,
+                                          int continued) {
+    if (check_window_shape(B, T, H, Hkv, d, window, sinks, dt) != KDA_OK) return 0;
+    int few = 0, ns = 1;
+    window_prefill_plan(B, T, H, d, window, sinks, dt, continued != 0, &few, &ns);
+    return window_workspace((long long)B * T, H, d, ns);
+}
+
 kda_status_t kda_window_prefill(const void* q, const void* k, const void* v, void* k_cache, void* v_cache, const int* start,
                                 const int* lens, void* o, int B, int T, int H, int Hkv, int d, int window, int sinks,
                                 float scale, long long q_stride, long long k_stride, long long v_stride, kda_dtype_t dt,
-                                void* stream) {
+                                void* workspace, size_t workspace_bytes, void* stream) {
     kda_status_t st = check_window_shape(B, T, H, Hkv, d, window, sinks, dt);
     if (st == KDA_OK && !scale_ok(scale)) st = KDA_ERR_INVALID_ARGUMENT;
     if (st != KDA_OK || B == 0 || H == 0) return st;
-    st = check_window_ptrs(q, k, v, k_cache, v_cache, start, lens, o, nullptr, 0, B, T, H, Hkv, d, window, sinks, q_stride,
-                           k_stride, v_stride, dt);
+    int few = 0, n_split = 1;
+    window_prefill_plan(B, T, H, d, window, sinks, dt, start != nullptr, &few, &n_split);
+    if (!workspace) n_split = 1;
+    const size_t need = window_workspace((long long)B * T, H, d, n_split);
+    st = check_window_ptrs(q, k, v, k_cache, v_cache, start, lens, o, need ? workspace : nullptr, need, B, T, H, Hkv, d,
+                           window, sinks, q_stride, k_stride, v_stride, dt);
     if (st != KDA_OK || T == 0) return st;
+    if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
     // the launch that keeps a sequence's rows has a thread for 16 bytes of each, fewer than 2^32 after rounding up
     const long long kept = (long long)sinks + (window < T ? window : T);
     if (k_cache && kept * ((long long)Hkv * d * (long long)elem_size(dt) / 16) > (1LL << 31)) return KDA_ERR_UNSUPPORTED;
@@ -476,7 +521,12 @@ kda_status_t kda_window_prefill(const void* q, const void* k, const void* v, voi
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
-    a.cus = cu_count();
+    a.few = few;
+    a.n_split = n_split;
+    if (need > 0) {
+        a.ws_o = reinterpret_cast<float*>(workspace);
+        a.ws_ml = a.ws_o + (size_t)B * T * H * n_split * d;
+    }
     (void)hipGetLastError();
     if (kda::launch_window_prefill(d, dt == KDA_F32, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
         return KDA_ERR_DEVICE;
@@ -487,7 +537,7 @@ size_t kda_window_step_workspace_bytes(int N, int H, int Hkv, int d, int window,
     if (check_window_shape(N, 1, H, Hkv, d, window, sinks, dt) != KDA_OK || N == 0 || H == 0) return 0;
     int ns = 1, len = 0;
     window_step_plan(N, H, Hkv, window, sinks, &ns, &len);
-    return window_step_workspace(N, H, d, ns);
+    return window_workspace(N, H, d, ns);
 }
 
 kda_status_t kda_window_step(const void* q, const void* k, const void* v, void* k_cache, void* v_cache, const int* pos,
@@ -501,7 +551,7 @@ kda_status_t kda_window_step(const void* q, const void* k, const void* v, void* 
     kda::WindowArgs a;
     memset(&a, 0, sizeof(a));
     window_step_plan(N, H, Hkv, window, sinks, &a.n_split, &a.split_len);
-    const size_t need = window_step_workspace(N, H, d, a.n_split);
+    const size_t need = window_workspace(N, H, d, a.n_split);
     st = check_window_ptrs(q, k, v, k_cache, v_cache, pos, nullptr, o, need ? workspace : nullptr, need, N, 1, H, Hkv, d,
                            window, sinks, q_stride, k_stride, v_stride, dt);
     if (st != KDA_OK) return st;

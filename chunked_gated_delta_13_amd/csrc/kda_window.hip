@@ -99,7 +99,9 @@ template <typename T> __device__ __forceinline__ void store4(T* p, const f32x4_t
 // passes kSumMax (a score far above that maximum) is the maximum brought up to date.
 constexpr float kSumMax = 16384.0f;
 
-template <int D, typename T, int NQ>
+// SPLIT: a workgroup takes one of n_split ranges of its queries' tiles and leaves partial outputs with their
+// maxima and sums, which kda_window_join_kernel joins.
+template <int D, typename T, int NQ, bool SPLIT>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefill_kernel(const WindowArgs a) {
     constexpr int BM = 64 * NQ, TILE = kKeys * D;
     typedef TileSteps<T, kKeys, D, 4> Steps;
@@ -112,6 +114,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
     // takes a contiguous range of them
     uint32_t unit = (blockIdx.x & 7) * (uint32_t)a.per_xcd + (blockIdx.x >> 3);
     if (unit >= (uint32_t)a.n_units) return;
+    int split = 0;
+    if constexpr (SPLIT) {
+        split = (int)(unit % (uint32_t)a.n_split);
+        unit /= (uint32_t)a.n_split;
+    }
     const uint32_t R = (uint32_t)a.H / (uint32_t)a.Hkv;
     const int hr = (int)(unit % R);
     unit /= R;
@@ -132,6 +139,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
     const int lo = sinks - s > q0 - window + 1 ? sinks - s : q0 - window + 1;
     const int nsink = s >= sinks ? sinks : (sinks < hi + 1 + s ? sinks : hi + 1 + s);
     const int total = nsink + (hi >= lo ? hi - lo + 1 : 0);
+    int t_first = 0, t_end = total;   // this workgroup's part of them
+    if constexpr (SPLIT) {
+        const int tiles = (total + kKeys - 1) / kKeys, per = (int)((uint32_t)(tiles + a.n_split - 1) / (uint32_t)a.n_split);
+        t_first = split * per * kKeys < total ? split * per * kKeys : total;
+        t_end = t_first + per * kKeys < total ? t_first + per * kKeys : total;
+    }
     const int base0 = s > sinks ? (int)((uint32_t)(s - sinks) % (uint32_t)window) : 0;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -178,7 +191,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
             }
         }
     };
-    fetch(0, 0);
+    fetch(t_first, 0);
 
     // queries of this wave
     const int wq = q0 + wave * 16 * NQ;
@@ -207,7 +220,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
     bool ready = false;   // every query of the wave has a maximum
     barrier_all();
 
-    for (int t0 = 0, buf = 0; t0 < total; t0 += kKeys, buf ^= 1) {
+    for (int t0 = t_first, buf = 0; t0 < t_end; t0 += kKeys, buf ^= 1) {
         const TileRows<T, kKeys, D> rk = rk0.at_delta(buf * (2 * TILE));
         const TileCols<T, kKeys> cv = cv0.at_delta(buf * (2 * TILE));
 
@@ -236,7 +249,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
 #pragma unroll
         for (int i = 0; i < 4; ++i) cv.frag(fv[0][i], 0, i, 0);
         __builtin_amdgcn_sched_barrier(0);
-        if (t0 + kKeys < total) fetch(t0 + kKeys, buf ^ 1);
+        if (t0 + kKeys < t_end) fetch(t0 + kKeys, buf ^ 1);
         __builtin_amdgcn_sched_barrier(0);
 
         const int w0 = lo + (t0 - nsink);   // relative position of the tile's first window key
@@ -344,8 +357,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_window_prefil
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         const int i = wq + 16 * n + r;
-        const float inv = 1.0f / sum_over_groups<NQ == 1>(l[n]);
-        if (i < len) {
+        const float sum = sum_over_groups<NQ == 1>(l[n]);
+        if (SPLIT && i < len) {
+            const long long part = (((long long)b * a.T + i) * a.H + h) * a.n_split + split;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) *reinterpret_cast<f32x4_t*>(a.ws_o + part * D + 16 * t + 4 * g) = O[t][n];
+            if (g == 0) {
+                a.ws_ml[2 * part] = m[n];
+                a.ws_ml[2 * part + 1] = sum;
+            }
+        }
+        const float inv = 1.0f / sum;
+        if (!SPLIT && i < len) {
             T* op = reinterpret_cast<T*>(a.o) + (((long long)b * a.T + i) * a.H + h) * D + 4 * g;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) {
@@ -581,12 +604,16 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
     }
 }
 
-// Joins the ranges of a split step.  grid: (sequence, head) rows; one wave: D / 4 lanes own four channels
-// of a range, and 64 / (D / 4) ranges are taken side by side.
+// Joins the ranges of a split call.  grid: (sequence, token, head) rows; one wave: D / 4 lanes own four
+// channels of a range, and 64 / (D / 4) ranges are taken side by side.
 template <int D, typename T>
 __global__ __launch_bounds__(64) void kda_window_join_kernel(const WindowArgs a) {
     constexpr int NL = D / 4, NS = 64 / NL;
     const long long row = blockIdx.x;
+    if (a.lens) {   // rows behind a sequence's end have no parts
+        const uint32_t token = blockIdx.x / (uint32_t)a.H, b = token / (uint32_t)a.T;
+        if ((int)(token - b * (uint32_t)a.T) >= a.lens[b]) return;
+    }
     const int lane = threadIdx.x, d = (lane % NL) * 4, i0 = lane / NL;
     const float* ml = a.ws_ml + 2 * row * a.n_split;
     const float* o = a.ws_o + row * a.n_split * D + d;
@@ -618,13 +645,16 @@ __global__ __launch_bounds__(64) void kda_window_join_kernel(const WindowArgs a)
 
 namespace {
 
-template <int D, typename T, int NQ>
+template <int D, typename T, int NQ, bool SPLIT>
 hipError_t window_attend(WindowArgs a, hipStream_t s) {
     a.q_tiles = (a.T + 64 * NQ - 1) / (64 * NQ);
-    a.n_units = (long long)a.B * a.H * a.q_tiles;
+    a.n_units = (long long)a.B * a.H * a.q_tiles * (SPLIT ? a.n_split : 1);
     a.per_xcd = (a.n_units + 7) / 8;
     if (a.per_xcd > 0x0fffffff) return hipErrorInvalidValue;
-    kda_window_prefill_kernel<D, T, NQ><<<dim3((unsigned)(8 * a.per_xcd)), 256, 0, s>>>(a);
+    kda_window_prefill_kernel<D, T, NQ, SPLIT><<<dim3((unsigned)(8 * a.per_xcd)), 256, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (!SPLIT || e != hipSuccess) return e;
+    kda_window_join_kernel<D, T><<<dim3((unsigned)((long long)a.B * a.T * a.H)), 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -633,10 +663,10 @@ hipError_t window_prefill_t(const WindowArgs& a, hipStream_t s) {
     // 128 queries per workgroup read each key once for twice the products; 64 where there are too few
     // queries to give every compute unit a workgroup (and for fp32, whose operands take twice the
     // registers).
-    const bool few = (long long)a.B * a.H * ((a.T + 127) / 128) < a.cus;
     hipError_t e;
-    if constexpr (sizeof(T) == 2) e = few ? window_attend<D, T, 1>(a, s) : window_attend<D, T, 2>(a, s);
-    else e = window_attend<D, T, 1>(a, s);
+    if (a.n_split > 1) e = window_attend<D, T, 1, true>(a, s);
+    else if (sizeof(T) == 2 && !a.few) e = window_attend<D, T, sizeof(T) == 2 ? 2 : 1, false>(a, s);
+    else e = window_attend<D, T, 1, false>(a, s);
     if (e != hipSuccess || !a.k_cache) return e;
     const int recent = a.window < a.T ? a.window : a.T;
     const int row_bytes = a.Hkv * D * (int)sizeof(T);

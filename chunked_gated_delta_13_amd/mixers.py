@@ -19,7 +19,7 @@ _DTYPES = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
 _INT_MAX = 2 ** 31 - 1
 # the library's entry points in the order in which the binding takes them
 _ENTRIES = ("kda_conv_prefill", "kda_conv_step", "kda_ssm_prefill_workspace_bytes", "kda_ssm_prefill", "kda_ssm_step",
-            "kda_window_prefill", "kda_window_step_workspace_bytes", "kda_window_step")
+            "kda_window_prefill_workspace_bytes", "kda_window_prefill", "kda_window_step_workspace_bytes", "kda_window_step")
 _native = None
 
 
@@ -95,8 +95,15 @@ def ssm_step(x, dt, A, Bm, Cm, S, *, D=None, z=None, dt_bias=None, y=None):
     return (_native or _load()).ssm_step(x, dt, A, Bm, Cm, S, D, z, dt_bias, y)
 
 
+def window_prefill_workspace_bytes(B, T, H, Hkv, d, window, sinks=0, dtype=torch.bfloat16, continued=False):
+    """Device workspace bytes of window_prefill for this shape on the current device; ``continued`` where the
+    call is given ``start``."""
+    _fits(B, T, H, Hkv, d, window, sinks)
+    return int(_lib.load().kda_window_prefill_workspace_bytes(B, T, H, Hkv, d, window, sinks, _code(dtype), int(continued)))
+
+
 def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cache=None, start=None, lens=None,
-                   o=None):
+                   o=None, workspace=None):
     """Attention of a prompt batch with a sliding window and ``sinks`` first tokens that stay visible: the
     query at position t sees key j <= t where t - j < window or j < sinks.  Returns o [B, T, H, d].
 
@@ -106,7 +113,8 @@ def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cach
     written to them.  ``lens`` (int32 [B]) gives the new tokens of each sequence of a padded batch; rows
     of o behind them are left as they were.  ``scale`` defaults to d ** -0.5.
     """
-    return (_native or _load()).window_prefill(q, k, v, window, sinks, scale, k_cache, v_cache, start, lens, o)
+    return (_native or _load()).window_prefill(q, k, v, window, sinks, scale, k_cache, v_cache, start, lens, o,
+                                               workspace)
 
 
 def window_step_workspace_bytes(N, H, Hkv, d, window, sinks=0, dtype=torch.bfloat16):

@@ -416,14 +416,20 @@ kda_status_t kda_ssm_step(const void *x, const void *dt, const float *A, const v
  *   d          64 or 128;  window >= 1;  sinks >= 0;  scale > 0
  * Rows of q, k and v start on 16-byte boundaries.  T == 0, B == 0 or H == 0 is a no-op.  B is at most
  * 65535, H at most 65536, T and window + sinks at most 2^29, B H (T / 64 + 1) at most 2^23, and the kept
- * rows of one sequence (sinks and the smaller of window and T) at most 32 GiB per cache.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded to bf16 as the
+ * rows of one sequence (sinks and the smaller of window and T) at most 32 GiB per cache.  A few queries
+ * over a long window are run as ranges of their keys, joined afterwards, when a workspace of
+ * kda_window_prefill_workspace_bytes(...) bytes is given (`continued`: 1 where start is; calls that overlap
+ * in time need one each); with NULL they run as one range.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded to bf16 as the
  * operand of the product with v.
  */
+size_t kda_window_prefill_workspace_bytes(int B, int T, int H, int Hkv, int d, int window, int sinks,
+                                          kda_dtype_t dtype, int continued);
 kda_status_t kda_window_prefill(const void *q, const void *k, const void *v, void *k_cache,
                                 void *v_cache, const int *start, const int *lens, void *o, int B, int T,
                                 int H, int Hkv, int d, int window, int sinks, float scale,
                                 long long q_stride, long long k_stride, long long v_stride,
-                                kda_dtype_t dtype, void *stream);
+                                kda_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                void *stream);
 
 /*
  * One new token of N sequences over their ring caches: q [N, H, d], k, v [N, Hkv, d], o [N, H, d].

@@ -69,6 +69,18 @@ def _window_prefill(kda, dtype):
     return [o, kc, vc], lambda: kda.window_prefill(q, k, v, win, sinks, k_cache=kc, v_cache=vc, start=start, lens=lens, o=o)
 
 
+def _window_split(kda, dtype, workspace):
+    B, T, H, Hkv, d, win, sinks = 2, 20, 4, 2, 128, 900, 4
+    q, k, v, o = _r(1, dtype, B, T, H, d), _r(2, dtype, B, T, Hkv, d), _r(3, dtype, B, T, Hkv, d), _r(4, dtype, B, T, H, d)
+    kc, vc = _r(5, dtype, B, win + sinks, Hkv, d), _r(6, dtype, B, win + sinks, Hkv, d)
+    start, lens = _i32(77, 5000), _i32(20, 13)
+    need = kda.window_prefill_workspace_bytes(B, T, H, Hkv, d, win, sinks, DT[dtype], continued=True)
+    assert need > 0
+    ws = torch.full((need // 4,), float("nan"), device="cuda") if workspace else None
+    return [o, kc, vc], lambda: kda.window_prefill(q, k, v, win, sinks, k_cache=kc, v_cache=vc, start=start, lens=lens, o=o,
+                                                   workspace=ws)
+
+
 def _window_step(kda, dtype, workspace):
     N, H, Hkv, d, win, sinks = 2, 6, 2, 128, 1500, 4
     q, k, v, o = _r(1, dtype, N, H, d), _r(2, dtype, N, Hkv, d), _r(3, dtype, N, Hkv, d), _r(4, dtype, N, H, d)
@@ -91,6 +103,8 @@ CALLS = {
     "ssm_step-bf16": lambda k: _ssm_step(k, "bf16"),
     "window_prefill-bf16": lambda k: _window_prefill(k, "bf16"),
     "window_prefill-f32": lambda k: _window_prefill(k, "f32"),
+    "window_prefill-split": lambda k: _window_split(k, "bf16", True),
+    "window_prefill-split-f32-own_workspace": lambda k: _window_split(k, "f32", False),
     "window_step-bf16": lambda k: _window_step(k, "bf16", True),
     "window_step-f32-own_workspace": lambda k: _window_step(k, "f32", False),
 }

@@ -91,6 +91,56 @@ def test_window_prefill_matches_definition(case):
         assert torch.equal(o, o2)
 
 
+# few queries over long windows: ranges of keys, some of them without any
+SPLITS = [
+    (1, 1, 2, 1, 128, 1000, 4, "bf16", [5000], None),
+    (1, 5, 4, 2, 64, 777, 0, "f32", [2000], None),
+    (3, 40, 4, 2, 128, 600, 5, "bf16", [0, 3, 9000], [40, 33, 17]),      # two rings that have hardly begun
+    (4, 70, 2, 1, 64, 500, 16, "bf16", [10, 700, 100, 2000], [0, 1, 70, 64]),
+    (2, 65, 3, 3, 128, 260, 1, "f32", [400, 0], [65, 2]),
+    (1, 700, 1, 1, 64, 1000, 0, "bf16", None, None),                     # no earlier tokens
+]
+
+
+@pytest.mark.parametrize("case", SPLITS, ids=lambda c: "-".join(map(str, c[:8])))
+def test_window_prefill_split_over_ranges_matches_definition(case):
+    """As above, with the smallest workspace; the same call without the split has the same bounds."""
+    from chunked_gated_delta_13_amd import _lib
+    kda = _kda()
+    B, T, H, Hkv, d, win, sinks, dtype, start, lens = case
+    print("window_prefill split", case, flush=True)
+    q, k, v = _draw(1, dtype, B, T, H, d), _draw(2, dtype, B, T, Hkv, d), _draw(3, dtype, B, T, Hkv, d)
+    st = None if start is None else torch.tensor(start, dtype=torch.int32)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    kc, vc = _caches(B, win, sinks, Hkv, d, dtype, [0] * B if start is None else start, 10)
+    want, mag, a, kc_ref, vc_ref = ref.window(q, k, v, win, sinks, d ** -0.5, kc, vc, st, ln)
+    for b, m in enumerate(ref.lens_of(ln, B, T)):
+        for t in (q, k, v):
+            t[b, m:] = float("nan")
+    need = kda.window_prefill_workspace_bytes(B, T, H, Hkv, d, win, sinks, DT[dtype], continued=start is not None)
+    assert need > 0 and need % 16 == 0
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    qd, kd, vd, sd, ld = dev(q), dev(k), dev(v), dev(st), dev(ln)
+    for split in (True, False):
+        kcd, vcd = kc.cuda(), vc.cuda()
+        o = torch.full((B, T, H, d), 9.0, dtype=DT[dtype], device="cuda")
+        if split:
+            room = torch.full((need // 4 + 64,), float("nan"), device="cuda")
+            kda.window_prefill(qd, kd, vd, win, sinks, k_cache=kcd, v_cache=vcd, start=sd, lens=ld, o=o,
+                               workspace=room[:need // 4])
+        else:
+            ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+            _lib.check(_lib.load().kda_window_prefill(
+                ptr(qd), ptr(kd), ptr(vd), ptr(kcd), ptr(vcd), ptr(sd), ptr(ld), ptr(o), B, T, H, Hkv, d, win, sinks, d ** -0.5,
+                H * d, Hkv * d, Hkv * d, 0 if dtype == "bf16" else 1, None, 0, torch.cuda.current_stream().cuda_stream), "window")
+        torch.cuda.synchronize()
+        _inside(o, want, mag, a, d, win + sinks, dtype)
+        for b, m in enumerate(ref.lens_of(ln, B, T)):
+            assert bool((o[b, m:] == 9.0).all())
+        assert np.array_equal(ref.f64(kcd), kc_ref, equal_nan=True) and np.array_equal(ref.f64(vcd), vc_ref, equal_nan=True)
+    assert bool(torch.isnan(room[need // 4:]).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_window_prefill_slices_scale_and_large_scores(dtype):
     """q, k and v cut from one projection's rows; scores up to several hundred."""

@@ -184,11 +184,13 @@ def test_ssm_binding_refuses_what_it_cannot_run():
         kda.ssm_step(x[:, 0], x[:, 0, :, 0], torch.zeros(2), b[:, 0], b[:, 0], torch.zeros(2, 2, 64, 64))
 
 
-def _window(lib, B=2, T=50, H=4, Hkv=2, d=64, window=20, sinks=4, scale=0.125, dt=BF16, strides=None, **ptr):
+def _window(lib, B=2, T=50, H=4, Hkv=2, d=64, window=20, sinks=4, scale=0.125, dt=BF16, strides=None, ws=None,
+            ws_bytes=0, **ptr):
     q = dict(q=_at(0), k=_at(1), v=_at(2), kc=_at(3), vc=_at(4), start=_at(5), lens=_at(6), o=_at(7))
     q.update(ptr)
     st = strides or (H * d, Hkv * d, Hkv * d)
-    return lib.kda_window_prefill(*[_vp(x) for x in q.values()], B, T, H, Hkv, d, window, sinks, scale, *st, dt, None)
+    return lib.kda_window_prefill(*[_vp(x) for x in q.values()], B, T, H, Hkv, d, window, sinks, scale, *st, dt, _vp(ws), ws_bytes,
+                                  None)
 
 
 @pytest.mark.parametrize("kw,expect", [
@@ -207,6 +209,24 @@ def _window(lib, B=2, T=50, H=4, Hkv=2, d=64, window=20, sinks=4, scale=0.125, d
 ])
 def test_window_prefill_refusals(lib, host_only, kw, expect):
     assert _window(lib, **kw) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(ws=_at(8), ws_bytes=64), WORKSPACE), (dict(ws=_at(8) + 4, ws_bytes=1 << 30), INVALID),
+    (dict(ws=_at(3), ws_bytes=1 << 30), INVALID), (dict(ws=_at(7) + 16, ws_bytes=1 << 30), INVALID),
+])
+def test_window_prefill_workspace_refusals(lib, host_only, kw, expect):
+    assert _window(lib, window=5000, **kw) == expect
+
+
+def test_window_prefill_workspace(lib):
+    need = lib.kda_window_prefill_workspace_bytes
+    per = 2 * 50 * 4 * (64 + 4) * 4
+    assert need(2, 50, 4, 2, 64, 5000, 4, BF16, 1) % per == 0 and need(2, 50, 4, 2, 64, 5000, 4, BF16, 1) >= 2 * per
+    assert need(2, 50, 4, 2, 64, 5000, 4, BF16, 0) == 0           # 50 keys at most
+    assert need(64, 4096, 8, 2, 64, 5000, 4, BF16, 1) == 0        # enough queries
+    assert need(0, 50, 4, 2, 64, 5000, 4, BF16, 1) == 0 and need(2, 0, 4, 2, 64, 5000, 4, BF16, 1) == 0
+    assert need(2, 50, 4, 3, 64, 5000, 4, BF16, 1) == 0           # refused shapes need nothing
 
 
 def test_window_noops(lib):
