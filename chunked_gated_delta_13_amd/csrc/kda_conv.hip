@@ -9,7 +9,7 @@
 // owns one 16-byte group of channels (so that a wave reads and writes 1 KiB runs of a row) and
 // walks a tile of consecutive tokens with the last W - 1 inputs in registers, so each input is
 // read once per tile and W - 1 more times per tile boundary, from cache.  4 x 8192 tokens of 7424
-// channels in bf16 (0.97 GB) take 186 us, 5.2 TB/s, a little above a device copy's rate; one token of 256
+// channels in bf16 (0.97 GB) take 174 us, 5.6 TB/s, above a device copy's 4.9; one token of 256
 // sequences (30 MB) takes 6.1 us, one token of one sequence 4.6 us a call, which is the launch.
 #include "kda_device.h"
 #include "kda_mixers.h"
@@ -73,18 +73,19 @@ __device__ __forceinline__ void conv_weights(float (&w)[W][V], float (&b)[V], co
 
 }  // namespace
 
-// grid: (channel groups / 256, token tiles, sequences).  STREAM: outputs go past the caches.
+// grid: (channel groups x token tiles / 256, sequences), groups fastest, so that every lane has work whatever
+// the width (workgroups of whole tiles, with idle lanes in each tile's last one: 186 us).  STREAM: outputs go past the caches.
 template <typename T, int W, int V, bool STREAM>
 __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(const ConvArgs a) {
-    const int d = (int)(blockIdx.x * kConvThreads + threadIdx.x) * V;
-    const int b = blockIdx.z;
-    if (d >= a.D) return;
+    const uint32_t at = blockIdx.x * kConvThreads + threadIdx.x, groups = (uint32_t)(a.D + V - 1) / V, piece = at / groups;
+    const int d = (int)(at - piece * groups) * V;
+    const int b = blockIdx.y;
     int len = a.T;
     if (a.lens) {
         const int l = a.lens[b];
         len = l < 0 ? 0 : (l > a.T ? a.T : l);
     }
-    const long long t0 = (long long)blockIdx.y * a.tile;
+    const long long t0 = (long long)piece * a.tile;
     if (t0 > 0 && t0 >= len) return;
     const long long t1 = t0 + a.tile < len ? t0 + a.tile : len;
     const T* x = reinterpret_cast<const T*>(a.x) + (long long)b * a.T * a.x_stride + d;
@@ -200,9 +201,9 @@ namespace {
 
 template <typename T, int W, int V>
 hipError_t conv_prefill_wv(const ConvArgs& a, hipStream_t s) {
-    const int groups = (a.D + V - 1) / V;
-    const int tiles = a.T > 0 ? (int)(((long long)a.T + a.tile - 1) / a.tile) : 1;
-    const dim3 grid((groups + kConvThreads - 1) / kConvThreads, tiles, a.B);
+    const long long groups = (a.D + V - 1) / V;
+    const long long tiles = a.T > 0 ? ((long long)a.T + a.tile - 1) / a.tile : 1;
+    const dim3 grid((unsigned)((groups * tiles + kConvThreads - 1) / kConvThreads), a.B, 1);
     if (V > 1 && a.streamed) kda_conv_prefill_kernel<T, W, V, (V > 1)><<<grid, kConvThreads, 0, s>>>(a);
     else kda_conv_prefill_kernel<T, W, V, false><<<grid, kConvThreads, 0, s>>>(a);
     return hipGetLastError();

@@ -338,14 +338,14 @@ kda_status_t kda_conv_prefill(const void* x, const void* w, const void* bias, co
     a.D = D;
     a.silu = silu ? 1 : 0;
     const bool vec = conv_vec(x, bias, state_in, state_out, y, D, x_stride, dt);
-    // Tokens per thread.  Every tile re-reads W - 1 rows, from cache: 16 tokens and streamed stores take
-    // 32768 rows of 7424 channels in bf16 in 186 us, 32 tokens 192, 64 tokens 199; with plain stores 16
-    // take 192.  Short inputs halve the tile until there are about 16 waves per compute unit of 256.
+    // Tokens per thread.  Every tile re-reads W - 1 rows, from cache: 8 or 16 tokens and streamed stores take
+    // 32768 rows of 7424 channels in bf16 in 174 us, 32 tokens 184, 64 tokens 204; with plain stores 16 take
+    // 185.  Short inputs halve the tile until there are about 16 waves per compute unit of 256.
     const long long groups = (D + (vec ? (dt == KDA_BF16 ? 8 : 4) : 1) - 1) / (vec ? (dt == KDA_BF16 ? 8 : 4) : 1);
     int tile = 16;
     while (tile > 4 && groups * B * (((long long)T + tile - 1) / tile) < 64LL * 4096) tile >>= 1;
     a.streamed = (size_t)B * T * D * esz > kStreamedBytes ? 1 : 0;
-    while ((T + (long long)tile - 1) / tile > kMaxGridYZ) tile <<= 1;
+    while (groups * (((long long)T + tile - 1) / tile) > (1LL << 31)) tile <<= 1;   // threads of a launch
     a.tile = tile;
     (void)hipGetLastError();
     if (kda::launch_conv_prefill(W, dt == KDA_F32, vec, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
