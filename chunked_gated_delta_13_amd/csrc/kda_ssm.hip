@@ -337,7 +337,7 @@ template <int N, int P, typename T, int NW> struct Mixer {
     __device__ __forceinline__ void update(State& S, const Frag<T> (&xt)[2][NCT], const KDA_LDS ChunkDecay* cd, int lane) const {
         const float f = cd->factor;
         // groups of NG row tiles of the state; a group's columns of B are requested while the products of the
-        // group before run
+        // group before run, and its sums join the state beside the products of the next one
         constexpr int NG = 2, NGR = NT / NG;
         Frag<T> fb[2][NG][2], xs[2][NCT][NP];
         float w[2][8];
@@ -351,6 +351,15 @@ template <int N, int P, typename T, int NW> struct Mixer {
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) weigh(xs[q][ct], xt[q][ct], w[q]);
+        f32x4_t acc[2][NG][NCT];
+        auto join = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) S[j * NG + i][ct][k] = fmaf(f, S[j * NG + i][ct][k], acc[j & 1][i][ct][k]);
+        };
 #pragma unroll
         for (int j = 0; j < NGR; ++j) {
             if (j + 1 < NGR) {
@@ -360,7 +369,6 @@ template <int N, int P, typename T, int NW> struct Mixer {
                     for (int q = 0; q < 2; ++q) cb.frag(fb[(j + 1) & 1][i][q], 0, (j + 1) * NG + i, q);
             }
             __builtin_amdgcn_sched_barrier(0);
-            f32x4_t acc[NG][NCT];
 #pragma unroll
             for (int k = NP - 1; k >= 0; --k)
 #pragma unroll
@@ -369,14 +377,11 @@ template <int N, int P, typename T, int NW> struct Mixer {
                     for (int i = 0; i < NG; ++i)
 #pragma unroll
                         for (int ct = 0; ct < NCT; ++ct)
-                            acc[i][ct] = mma(fb[j & 1][i][q], xs[q][ct][k], k == NP - 1 && q == 0 ? zero4() : acc[i][ct]);
-#pragma unroll
-            for (int i = 0; i < NG; ++i)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) S[j * NG + i][ct][k] = fmaf(f, S[j * NG + i][ct][k], acc[i][ct][k]);
+                            acc[j & 1][i][ct] =
+                                mma(fb[j & 1][i][q], xs[q][ct][k], k == NP - 1 && q == 0 ? zero4() : acc[j & 1][i][ct]);
+            if (j > 0) join(j - 1);
         }
+        join(NGR - 1);
     }
 
     // A state in memory, p as the lane's element of row tile 0, column tile 0 (byte offset `off`).

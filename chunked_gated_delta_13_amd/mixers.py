@@ -111,7 +111,8 @@ def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cach
     ``k_cache`` / ``v_cache`` [B, sinks + window, Hkv, d] are the sequences' ring caches: earlier tokens
     (``start`` [B] int32 of them, None = 0) are read from them and the new ones that stay visible are
     written to them.  ``lens`` (int32 [B]) gives the new tokens of each sequence of a padded batch; rows
-    of o behind them are left as they were.  ``scale`` defaults to d ** -0.5.
+    of o behind them are left as they were.  ``scale`` defaults to d ** -0.5.  Few queries over a long
+    window are run as ranges of keys, in ``workspace`` if it is large enough, else in a new one.
     """
     return (_native or _load()).window_prefill(q, k, v, window, sinks, scale, k_cache, v_cache, start, lens, o,
                                                workspace)
