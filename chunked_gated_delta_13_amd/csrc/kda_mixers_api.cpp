@@ -99,18 +99,33 @@ kda_status_t check_ssm_shape(int rows_b, int T, int H, int G, int n, int p, kda_
     return KDA_OK;
 }
 
-// Segments of seg_in tokens (whole chunks), or chosen here (seg_in 0): enough of them that every
-// compute unit has two workgroups (one where its tiles fill the LDS: fp32, or p = 128), each at least two
-// chunks.
-kda_status_t ssm_plan(int B, int T, int H, int p, kda_dtype_t dt, int seg_in, long long* seg_len, int* n_seg) {
+// Segments of seg_in tokens (whole chunks), or as many as take the least time (seg_in 0).  Where there are
+// fewer sequences and heads than workgroups at once (two per compute unit; one where the tiles fill the
+// LDS: p = 128, or fp32 with n = 128), a split shortens the chain of chunks.  In microseconds, measured: a chunk of the
+// outputs takes 3.3 (n = 128) or 2.5 (n = 64) in bf16 and 6 to 13 in fp32, half as much again beside a
+// second workgroup; the states of a chunk 0.4 of that; the two further launches 4; and every segment's
+// state is written and read twice, at 6 TB/s together.  8 heads, n = p = 128: 300 tokens 19 us in segments
+// of a chunk, 22 in one piece (fp32 31 and 69); 128 heads, 300 tokens: 30 in two, 25 in one.
+kda_status_t ssm_plan(int B, int T, int H, int n, int p, kda_dtype_t dt, int seg_in, long long* seg_len, int* n_seg) {
     if (seg_in < 0 || seg_in % kSsmChunk != 0) return KDA_ERR_INVALID_ARGUMENT;
     const long long chunks = ((long long)T + kSsmChunk - 1) / kSsmChunk;
     const long long units = (long long)B * H;
     long long per = seg_in > 0 ? seg_in / kSsmChunk : chunks;
-    if (seg_in == 0 && units > 0) {
-        const long long want = (long long)cu_count() * (dt == KDA_F32 || p == 128 ? 1 : 2) / units;
-        if (want >= 2) per = (chunks + want - 1) / want;
-        if (per < 2) per = 2;
+    const bool f32 = dt == KDA_F32;
+    const long long cus = seg_in == 0 && units > 0 ? cu_count() : 0, at_once = p == 128 || (f32 && n == 128) ? cus : 2 * cus;
+    if (cus > 0 && at_once >= 2 * units) {
+        const double chunk = f32 ? 0.05 * n + 0.06 * p - 1.0 : 1.75 + 0.0117 * n;
+        const double segment = (double)units * n * p * 16 / 6e6;
+        double best = (double)chunks * chunk;
+        const long long most = at_once / units < chunks ? at_once / units : chunks;
+        for (long long ns = 2; ns <= most; ++ns) {
+            const long long c = (chunks + ns - 1) / ns;
+            const double us = (double)c * chunk * 1.4 * (units * ns > cus ? 1.45 : 1.0) + (double)ns * segment + 4.0;
+            if (us < best) {
+                best = us;
+                per = c;
+            }
+        }
     }
     if (per < 1) per = 1;
     const long long ns = chunks > 0 ? (chunks + per - 1) / per : 1;
@@ -388,7 +403,7 @@ kda_status_t kda_conv_step(const void* x, const void* w, const void* bias, void*
 size_t kda_ssm_prefill_workspace_bytes(int B, int T, int H, int G, int n, int p, kda_dtype_t dt, int seg_len) {
     long long sl = 0;
     int ns = 1;
-    if (check_ssm_shape(B, T, H, G, n, p, dt) != KDA_OK || ssm_plan(B, T, H, p, dt, seg_len, &sl, &ns) != KDA_OK) return 0;
+    if (check_ssm_shape(B, T, H, G, n, p, dt) != KDA_OK || ssm_plan(B, T, H, n, p, dt, seg_len, &sl, &ns) != KDA_OK) return 0;
     return ssm_workspace(B, H, n, p, ns);
 }
 
@@ -401,7 +416,7 @@ kda_status_t kda_ssm_prefill(const void* x, const void* dt, const float* A, cons
     if (st != KDA_OK) return st;
     long long sl = 0;
     int ns = 1;
-    st = ssm_plan(B, T, H, p, dtype, seg_len, &sl, &ns);
+    st = ssm_plan(B, T, H, n, p, dtype, seg_len, &sl, &ns);
     if (st != KDA_OK || B == 0 || H == 0) return st;
     const SsmPtrs q = {x, dt, A, Bm, Cm, D, z, dt_bias, lens, x_stride, dt_stride, b_stride, c_stride, z_stride};
     st = check_ssm_ptrs(q, S0, y, S_T, B, T, H, G, n, p, dtype);

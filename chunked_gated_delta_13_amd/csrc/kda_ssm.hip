@@ -21,8 +21,8 @@
 // What bounds it: 4 x 16384 tokens of 56 heads, n = p = 128, bf16, take 1.00 ms, 300 TFLOP/s of the
 // formulas' products; the 2.87 GB they cannot do without take 0.58 ms.  A SIMD holds two waves, each a
 // chain LDS - matrix cores - vector unit - LDS, and of 8000 cycles a chunk issues vector instructions in
-// 4300 and products in 2430; the 224 sequences and heads leave 32 of 256 compute units without work.  One sequence of 20001 tokens, 16 heads, n = 128, p = 64 takes 90 us, 24 of
-// them the first pass, 9 the join between two launches, 50 the outputs (ten chunks one after the other).
+// 4300 and products in 2430; the 224 sequences and heads leave 32 of 256 compute units without work.  One sequence of 20001 tokens, 16 heads, n = 128, p = 64 takes 90 us, 26 of
+// them the first pass, 9 the join between two launches, 55 the outputs (ten chunks one after the other).
 //
 // Token.  One streaming pass over the state, bound by HBM: 8 bytes of traffic per state element.
 #include "kda_mixers.h"
