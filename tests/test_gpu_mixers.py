@@ -187,6 +187,36 @@ def test_two_calls_at_once_keep_apart(name):
                 assert torch.equal(t, u)
 
 
+def test_host_threads_call_side_by_side():
+    """Four host threads, a stream and a set of buffers each; every call's results are those of a lone call."""
+    import threading
+    kda = _kda()
+    names = ["conv_prefill-bf16", "ssm_prefill-split-own_workspace", "window_prefill-split-f32-own_workspace",
+             "window_step-f32-own_workspace"]
+    print("threads", names, flush=True)
+    jobs, wrong = [], []
+    for name in names:
+        outs, call = CALLS[name](kda)
+        jobs.append((name, outs, call, *_eager(call, outs)))
+
+    def work(name, outs, call, before, want):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for i in range(20):
+                for t, b in zip(outs, before):
+                    t.copy_(b)
+                call()
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(t, u) for t, u in zip(outs, want)):
+                    wrong.append((name, i))
+
+    threads = [threading.Thread(target=work, args=job) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_a_captured_layer_stack_answers_token_by_token_like_eager_calls():
     """Projection rows -> convolution -> scan, and window attention beside it, for a prompt; then tokens
     from one captured graph that also moves the positions on, against the same tokens made eagerly."""
