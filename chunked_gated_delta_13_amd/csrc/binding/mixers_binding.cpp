@@ -11,6 +11,7 @@
 
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
@@ -115,6 +116,12 @@ struct Common {
         if (t.scalar_type() != ty) throw refusal<WrongType>(name, " must be ", ty, ", got ", t.scalar_type());
         if (t.sizes() != shape) throw refusal<WrongValue>(name, " must have shape ", shape, ", got ", t.sizes());
         if (t.device() != dev) throw refusal<WrongValue>(name, " must be on ", dev, ", got ", t.device());
+        memory(name, t);
+    }
+    // Batches of torch.vmap, wrappers of torch.func and fake tensors have none that a kernel could use.
+    static void memory(const char* name, const Tensor& t) {
+        if (!t.has_storage() || (t.numel() > 0 && t.const_data_ptr() == nullptr))
+            throw refusal<WrongValue>(name, " has no memory of its own (calls inside torch.vmap, torch.func or a fake tensor mode are not supported)");
     }
     void whole(const char* name, const Tensor& t, at::ScalarType ty, c10::IntArrayRef shape) const {
         like(name, t, ty, shape);
@@ -138,12 +145,15 @@ struct Common {
     }
     Tensor fresh(c10::IntArrayRef shape, at::ScalarType ty) const { return at::empty(shape, at::TensorOptions().dtype(ty).device(dev)); }
 
-    // The library call on the current stream of the tensors' device; that device has to be current.
-    template <typename F> bool call(F&& f) const {
+    // The library call on the current stream of the tensors' device; that device has to be current.  The
+    // arguments are plain values, formed before the interpreter lock is released: taking a tensor's pointer
+    // can throw, and an exception must not leave the part that runs without the lock.
+    template <typename F, typename... A> bool call(F* f, A... a) const {
+        static_assert((std::is_scalar_v<A> && ...), "pointers, numbers and enumerators only");
         void* stream = c10::hip::getCurrentHIPStream(dev.index()).stream();
         int st;
         Py_BEGIN_ALLOW_THREADS
-        st = f(stream);
+        st = f(a..., stream);
         Py_END_ALLOW_THREADS
         if (st == KDA_OK) return true;
         PyObject* r = PyObject_CallFunction(on_status, "is", st, where);
@@ -207,6 +217,7 @@ struct Workspace {
         if (t) {
             if (t->device() != c.dev) throw refusal<WrongValue>("workspace must be on ", c.dev, ", got ", t->device());
             if (!t->is_contiguous()) throw refusal<WrongValue>("workspace must be contiguous");
+            Common::memory("workspace", *t);
             bytes = (size_t)t->numel() * t->element_size();
             if (bytes >= need) {
                 p = t->data_ptr();
@@ -255,10 +266,8 @@ PyObject* conv_prefill(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     Pending py(c, a, 6, "y", c.type, {B, T, D}), pso(c, a, 7, "state_out", c.type, {B, W - 1, D}, a.truth(8));
     const OnDevice on(c.dev);
     const Output &y = py.make(c), &so = pso.make(c);
-    if (!c.call([&](void* s) {
-            return lib.conv_prefill(ptr(x), ptr(w), ptr(bias), ptr(state), at_type<int>(lens), y.ptr(), so.ptr(), b, t, d, taps, xs,
-                                    silu, c.code, s);
-        }))
+    if (!c.call(lib.conv_prefill, ptr(x), ptr(w), ptr(bias), ptr(state), at_type<int>(lens), y.ptr(), so.ptr(), b, t, d,
+                taps, xs, silu, c.code))
         return nullptr;
     return pair(y, so);
     END_HANDLE_TH_ERRORS
@@ -283,9 +292,7 @@ PyObject* conv_step(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     Pending py(c, a, 5, "y", c.type, {N, D});
     const OnDevice on(c.dev);
     const Output& y = py.make(c);
-    if (!c.call([&](void* s) {
-            return lib.conv_step(ptr(x), ptr(w), ptr(bias), ptr(state), y.ptr(), n, d, taps, xs, silu, c.code, s);
-        }))
+    if (!c.call(lib.conv_step, ptr(x), ptr(w), ptr(bias), ptr(state), y.ptr(), n, d, taps, xs, silu, c.code))
         return nullptr;
     return y.object();
     END_HANDLE_TH_ERRORS
@@ -340,12 +347,10 @@ PyObject* ssm_prefill(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const OnDevice on(c.dev);
     const Workspace ws(c, room, lib.ssm_prefill_workspace_bytes(b, t, q.H, q.G, q.n, q.p, c.code, seg));
     const Output &y = py.make(c), &S = ps.make(c);
-    if (!c.call([&](void* s) {
-            return lib.ssm_prefill(ptr(q.x), ptr(q.dt), at_type<float>(&q.A), ptr(q.Bm), ptr(q.Cm), at_type<float>(q.D), ptr(q.z),
-                                   at_type<float>(q.dt_bias), at_type<float>(S0), at_type<int>(lens), y.ptr(),
-                                   reinterpret_cast<float*>(S.ptr()), b, t, q.H, q.G, q.n, q.p, q.xs, q.ds, q.bs, q.cs, q.zs,
-                                   c.code, seg, ws.p, ws.bytes, s);
-        }))
+    if (!c.call(lib.ssm_prefill, ptr(q.x), ptr(q.dt), at_type<float>(&q.A), ptr(q.Bm), ptr(q.Cm), at_type<float>(q.D),
+                ptr(q.z), at_type<float>(q.dt_bias), at_type<float>(S0), at_type<int>(lens), y.ptr(),
+                reinterpret_cast<float*>(S.ptr()), b, t, q.H, q.G, q.n, q.p, q.xs, q.ds, q.bs, q.cs, q.zs, c.code, seg,
+                ws.p, ws.bytes))
         return nullptr;
     return pair(y, S);
     END_HANDLE_TH_ERRORS
@@ -365,11 +370,9 @@ PyObject* ssm_step(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     Pending py(c, a, 9, "y", c.type, q.x.sizes());
     const OnDevice on(c.dev);
     const Output& y = py.make(c);
-    if (!c.call([&](void* s) {
-            return lib.ssm_step(ptr(q.x), ptr(q.dt), at_type<float>(&q.A), ptr(q.Bm), ptr(q.Cm), at_type<float>(q.D), ptr(q.z),
-                                at_type<float>(q.dt_bias), at_type<float>(&S), y.ptr(), n, q.H, q.G, q.n, q.p, q.xs, q.ds, q.bs,
-                                q.cs, q.zs, c.code, s);
-        }))
+    if (!c.call(lib.ssm_step, ptr(q.x), ptr(q.dt), at_type<float>(&q.A), ptr(q.Bm), ptr(q.Cm), at_type<float>(q.D),
+                ptr(q.z), at_type<float>(q.dt_bias), at_type<float>(&S), y.ptr(), n, q.H, q.G, q.n, q.p, q.xs, q.ds, q.bs,
+                q.cs, q.zs, c.code))
         return nullptr;
     return y.object();
     END_HANDLE_TH_ERRORS
@@ -424,11 +427,9 @@ PyObject* window_prefill(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const OnDevice on(c.dev);
     const Workspace ws(c, room, lib.window_prefill_workspace_bytes(b, t, q.H, q.Hkv, q.d, q.window, q.sinks, c.code, start != nullptr));
     const Output& o = po.make(c);
-    if (!c.call([&](void* s) {
-            return lib.window_prefill(ptr(q.q), ptr(q.k), ptr(q.v), ptr(q.kc), ptr(q.vc), at_type<int>(start), at_type<int>(lens),
-                                      o.ptr(), b, t, q.H, q.Hkv, q.d, q.window, q.sinks, scale, q.qs, q.ks, q.vs, c.code, ws.p,
-                                      ws.bytes, s);
-        }))
+    if (!c.call(lib.window_prefill, ptr(q.q), ptr(q.k), ptr(q.v), ptr(q.kc), ptr(q.vc), at_type<int>(start),
+                at_type<int>(lens), o.ptr(), b, t, q.H, q.Hkv, q.d, q.window, q.sinks, scale, q.qs, q.ks, q.vs, c.code,
+                ws.p, ws.bytes))
         return nullptr;
     return o.object();
     END_HANDLE_TH_ERRORS
@@ -453,10 +454,8 @@ PyObject* window_step(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const OnDevice on(c.dev);
     const Workspace ws(c, room, lib.window_step_workspace_bytes(n, q.H, q.Hkv, q.d, q.window, q.sinks, c.code));
     const Output& o = po.make(c);
-    if (!c.call([&](void* s) {
-            return lib.window_step(ptr(q.q), ptr(q.k), ptr(q.v), ptr(q.kc), ptr(q.vc), at_type<int>(&pos), o.ptr(), n, q.H, q.Hkv,
-                                   q.d, q.window, q.sinks, scale, q.qs, q.ks, q.vs, c.code, ws.p, ws.bytes, s);
-        }))
+    if (!c.call(lib.window_step, ptr(q.q), ptr(q.k), ptr(q.v), ptr(q.kc), ptr(q.vc), at_type<int>(&pos), o.ptr(), n, q.H,
+                q.Hkv, q.d, q.window, q.sinks, scale, q.qs, q.ks, q.vs, c.code, ws.p, ws.bytes))
         return nullptr;
     return o.object();
     END_HANDLE_TH_ERRORS
