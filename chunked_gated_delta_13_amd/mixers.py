@@ -11,11 +11,8 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch
-
 from . import _lib
 
-_DTYPES = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
 _INT_MAX = 2 ** 31 - 1
 # the library's entry points in the order in which the binding takes them
 _ENTRIES = ("kda_conv_prefill", "kda_conv_step", "kda_ssm_prefill_workspace_bytes", "kda_ssm_prefill", "kda_ssm_step",
@@ -39,10 +36,12 @@ def _load():
 
 
 def _code(dt):
-    code = _DTYPES.get(dt)
-    if code is None:
-        raise TypeError(f"inputs must be bfloat16 or float32, got {dt}")
-    return code
+    import torch
+    if dt is None or dt == torch.bfloat16:
+        return _lib.KDA_BF16
+    if dt == torch.float32:
+        return _lib.KDA_F32
+    raise TypeError(f"inputs must be bfloat16 or float32, got {dt}")
 
 
 def _fits(*sizes):
@@ -69,8 +68,8 @@ def conv_step(x, w, state, bias=None, *, silu=True, y=None):
     return (_native or _load()).conv_step(x, w, state, bias, silu, y)
 
 
-def ssm_workspace_bytes(B, T, H, G, n, p, dtype=torch.bfloat16, seg_len=0):
-    """Device workspace bytes of ssm_prefill for this shape on the current device."""
+def ssm_workspace_bytes(B, T, H, G, n, p, dtype=None, seg_len=0):
+    """Device workspace bytes of ssm_prefill for this shape on the current device (dtype None = bfloat16)."""
     _fits(B, T, H, G, n, p, seg_len)
     return int(_lib.load().kda_ssm_prefill_workspace_bytes(B, T, H, G, n, p, _code(dtype), seg_len))
 
@@ -95,9 +94,9 @@ def ssm_step(x, dt, A, Bm, Cm, S, *, D=None, z=None, dt_bias=None, y=None):
     return (_native or _load()).ssm_step(x, dt, A, Bm, Cm, S, D, z, dt_bias, y)
 
 
-def window_prefill_workspace_bytes(B, T, H, Hkv, d, window, sinks=0, dtype=torch.bfloat16, continued=False):
-    """Device workspace bytes of window_prefill for this shape on the current device; ``continued`` where the
-    call is given ``start``."""
+def window_prefill_workspace_bytes(B, T, H, Hkv, d, window, sinks=0, dtype=None, continued=False):
+    """Device workspace bytes of window_prefill for this shape on the current device (dtype None = bfloat16);
+    ``continued`` where the call is given ``start``."""
     _fits(B, T, H, Hkv, d, window, sinks)
     return int(_lib.load().kda_window_prefill_workspace_bytes(B, T, H, Hkv, d, window, sinks, _code(dtype), int(continued)))
 
@@ -118,8 +117,8 @@ def window_prefill(q, k, v, window, sinks=0, *, scale=None, k_cache=None, v_cach
                                                workspace)
 
 
-def window_step_workspace_bytes(N, H, Hkv, d, window, sinks=0, dtype=torch.bfloat16):
-    """Device workspace bytes of window_step for this shape on the current device."""
+def window_step_workspace_bytes(N, H, Hkv, d, window, sinks=0, dtype=None):
+    """Device workspace bytes of window_step for this shape on the current device (dtype None = bfloat16)."""
     _fits(N, H, Hkv, d, window, sinks)
     return int(_lib.load().kda_window_step_workspace_bytes(N, H, Hkv, d, window, sinks, _code(dtype)))
 

@@ -78,3 +78,25 @@ def test_tensors_without_memory_are_refused(tmp_path, op):
     env = dict(os.environ, LD_PRELOAD=str(lib), PYTHONPATH=ROOT)
     r = subprocess.run([sys.executable, "-c", CHILD, op], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.endswith("done\n"), (r.returncode, r.stdout, r.stderr[-2000:])
+
+
+def test_the_package_is_imported_without_torch():
+    """torch is needed by calls, not by the import (plans of a launcher, the C library's signatures)."""
+    child = ("import sys; sys.modules['torch'] = None\n"
+             "import chunked_gated_delta_13_amd as kda\n"
+             "from chunked_gated_delta_13_amd import _lib\n"
+             "assert 'kda_ssm_prefill' in _lib.SIGNATURES and callable(kda.conv_step)\n"
+             "print('done')")
+    r = subprocess.run([sys.executable, "-c", child], cwd=ROOT, env=dict(os.environ, PYTHONPATH=ROOT), capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout == "done\n", r.stderr[-2000:]
+
+
+def test_sizes_of_workspaces_default_to_bfloat16():
+    import torch
+    import chunked_gated_delta_13_amd as kda
+    for size, args in ((kda.ssm_workspace_bytes, (1, 5000, 2, 1, 64, 64)),
+                       (kda.window_step_workspace_bytes, (1, 8, 2, 128, 5000, 4))):
+        assert size(*args) == size(*args, dtype=torch.bfloat16) > 0
+        with pytest.raises(TypeError, match="bfloat16 or float32"):
+            size(*args, dtype=torch.float16)
