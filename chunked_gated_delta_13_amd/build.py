@@ -58,10 +58,14 @@ def _link(objs, out):
     os.replace(tmp, out)
 
 
-def build_binding() -> str:
+def build_binding() -> str | None:
     """_mixers.so from csrc/binding/: a Python extension that links to torch, which is imported
-    before it, and is handed libkda's entry points at run time."""
-    import torch
+    before it, and is handed libkda's entry points at run time.  Without torch there is nothing to
+    build it against (None): the C library does not need it."""
+    try:
+        import torch
+    except ImportError:
+        return None
     top = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
@@ -89,11 +93,11 @@ def build(verbose: bool = False) -> str:
         binding = ex.submit(build_binding)
         objs = list(ex.map(_compile, srcs))
         probe_objs = list(ex.map(_compile, probe_srcs))
-        binding.result()
+        binding = binding.result()
     _link(objs, LIB)
     _link(probe_objs, PEAKS_LIB)
     if verbose:
-        print(f"built {LIB}, {BINDING} and {PEAKS_LIB}")
+        print(f"built {LIB}, {binding or 'no binding (torch is not installed)'} and {PEAKS_LIB}")
     return LIB
 
 

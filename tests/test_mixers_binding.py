@@ -100,3 +100,13 @@ def test_sizes_of_workspaces_default_to_bfloat16():
         assert size(*args) == size(*args, dtype=torch.bfloat16) > 0
         with pytest.raises(TypeError, match="bfloat16 or float32"):
             size(*args, dtype=torch.float16)
+
+
+def test_the_c_library_is_built_without_torch(monkeypatch):
+    """The binding is left out where torch is missing; libkda is compiled and linked all the same."""
+    from chunked_gated_delta_13_amd import build as kbuild
+    linked = []
+    monkeypatch.setitem(sys.modules, "torch", None)
+    monkeypatch.setattr(kbuild, "_compile", lambda src: src + ".o")
+    monkeypatch.setattr(kbuild, "_link", lambda objs, out: linked.append(out))
+    assert kbuild.build() == kbuild.LIB and linked == [kbuild.LIB, kbuild.PEAKS_LIB]
