@@ -8,7 +8,9 @@
 // Both forms run one pass over the visible keys with the running maximum and sum of the softmax (fp32,
 // exponentials of base 2).  Scores are formed transposed, K Q^T with keys as rows: a lane then holds
 // four keys of one query, the statistics of a query stay in its lanes, and the probabilities are at
-// once the operand of V^T P^T, rounded to the input type for that product only.
+// once the operand of V^T P^T.  For that product only they are rounded to the input type in the prompt
+// form, whose time is its products (P in two parts would add half of them again); the one-token form, bound
+// by HBM, feeds bf16 ones as two parts.
 #include "kda_mixers.h"
 #include "kda_tile.h"
 
@@ -427,6 +429,7 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
     typedef TileSteps<T, TK, D, 1> Steps;
     constexpr int NG = Steps::N / Steps::NB;                   // row groups per tile
     constexpr int OP = D + 4;                                  // pitch of the partial outputs
+    constexpr int PP = sizeof(T) == 2 ? 2 : 1;                 // parts of a probability
     constexpr int REGION = TK * D * (int)sizeof(T) > 16 * OP * 4 ? TK * D * (int)sizeof(T) : 16 * OP * 4;
     __shared__ __attribute__((aligned(16))) char sV_[4][REGION];
     __shared__ float sm[4][16], sl[4][16];
@@ -549,8 +552,17 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
                 sum += sT[kt][j];
             }
         l = l * al + sum;
-        Frag<T> fp;
-        acc_pair_frag<T>(fp, sT[0], sT[1], true);
+        // Probabilities as operands: in bf16 as two parts, which hold 16 bits of them.  The products are a few
+        // percent of the time that the loads take, so rounding them to 8 bits would buy nothing here.
+        Frag<T> fp[PP];
+        acc_pair_frag<T>(fp[0], sT[0], sT[1], true);
+        if constexpr (PP == 2) {
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sT[kt][j] -= fp[0].get(4 * kt + j);
+            acc_pair_frag<T>(fp[1], sT[0], sT[1], true);
+        }
         wave_order();
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) {
@@ -558,7 +570,8 @@ __global__ __launch_bounds__(256) void kda_window_step_kernel(const WindowArgs a
             cv.frag(fv, 0, t, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) O[t][j] *= al;
-            O[t] = mma(fv, fp, O[t]);
+#pragma unroll
+            for (int i = PP - 1; i >= 0; --i) O[t] = mma(fv, fp[i], O[t]);
         }
         wave_order();
     }

@@ -436,7 +436,7 @@ kda_status_t kda_window_prefill(const void *q, const void *k, const void *v, voi
  * pos [N] int32 (DEVICE): tokens of each sequence before this one.  The token's k and v are written to
  * their row of the caches and are visible to its own query.  The workspace holds
  * kda_window_step_workspace_bytes(...) bytes (may be NULL when that is 0); calls that overlap in time
- * need one each.
+ * need one each.  With bf16 inputs a probability enters the product with v as two bf16 parts (16 bits).
  */
 size_t kda_window_step_workspace_bytes(int N, int H, int Hkv, int d, int window, int sinks,
                                        kda_dtype_t dtype);
