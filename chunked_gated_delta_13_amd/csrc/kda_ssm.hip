@@ -139,8 +139,8 @@ __device__ __forceinline__ int pinned_s(int x) {
 // Numbers of one chunk.
 struct ChunkDecay {
     float hi[kC];      // sum of the exponents (base 2) up to this token
-    float lo[kC];      // fp32: what `hi` leaves of that sum; bf16: hi - log2 dt
-    float dt[kC];      // (fp32)
+    float lo[kC];      // what `hi` leaves of that sum
+    float dt[kC];      // fp32: dt; bf16: lo - log2 dt
     float e[kC];       // factor of S^T C: 2^sum
     float w[kC];       // weight of the token in the state's update
     float sum;         // of the whole chunk
@@ -155,14 +155,11 @@ __device__ __forceinline__ void chunk_decay(KDA_LDS ChunkDecay* c, float raw, bo
     const double end = last_lane(s);
     const float hi = (float)s;
     if constexpr (OUT) {
+        const float lo = (float)(s - (double)hi);
         c->hi[lane] = hi;
-        if constexpr (sizeof(T) == 4) {
-            c->lo[lane] = (float)(s - (double)hi);
-            c->dt[lane] = d;
-        } else {
-            // 2^(c_i - c_j) dt_j as one exponential; dt = 0 gives +inf here and a factor of 0
-            c->lo[lane] = hi - __log2f(d);
-        }
+        c->lo[lane] = lo;
+        // bf16: 2^(c_i - c_j) dt_j as one exponential; dt = 0 gives +inf here and a factor of 0
+        c->dt[lane] = sizeof(T) == 4 ? d : lo - __log2f(d);
         c->e[lane] = fast_exp2(hi);
     }
     c->w[lane] = fast_exp2((float)(end - s)) * d;
@@ -204,8 +201,8 @@ template <int N, int P, typename T, int NW> struct Mixer {
         const int g = lane >> 4, r = lane & 15;
         Frag<T> fb[K][Q], fc[K][Q];
         int ti[K], tj[K];
-        float ci[K];
-        f32x4_t lj[K];
+        float ci[K], li[K];
+        f32x4_t cj[K], dj[K];
 #pragma unroll
         for (int p = 0; p < K; ++p) {
             ti[p] = pair[p] < 1 ? 0 : (pair[p] < 3 ? 1 : (pair[p] < 6 ? 2 : 3));
@@ -216,7 +213,9 @@ template <int N, int P, typename T, int NW> struct Mixer {
                 rc.frag(fc[p][q], 16 * 32 * ti[p], 0, q);
             }
             ci[p] = cd->hi[16 * ti[p] + r];
-            lj[p] = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->lo + 16 * tj[p] + 4 * g);
+            li[p] = cd->lo[16 * ti[p] + r];
+            cj[p] = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->hi + 16 * tj[p] + 4 * g);
+            dj[p] = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->dt + 16 * tj[p] + 4 * g);
         }
         __builtin_amdgcn_sched_barrier(0);
         f32x4_t acc[K];   // acc[p][k]: token j = 16 tj + 4 g + k against i = 16 ti + r
@@ -227,15 +226,15 @@ template <int N, int P, typename T, int NW> struct Mixer {
 #pragma unroll
         for (int p = 0; p < K; ++p) {
             float m[4];
+            // sums of a chunk may be large and the decay between two of its tokens small: differences of the
+            // high parts (exact where they are near each other) and of the low parts
             if constexpr (sizeof(T) == 4) {
-                const float li = cd->lo[16 * ti[p] + r];
-                const f32x4_t cj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->hi + 16 * tj[p] + 4 * g);
-                const f32x4_t dj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->dt + 16 * tj[p] + 4 * g);
+                const f32x4_t lj = *reinterpret_cast<const KDA_LDS f32x4_t*>(cd->lo + 16 * tj[p] + 4 * g);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m[k] = acc[p][k] * (fast_exp2((ci[p] - cj[k]) + (li - lj[p][k])) * dj[k]);
+                for (int k = 0; k < 4; ++k) m[k] = acc[p][k] * (fast_exp2((ci[p] - cj[p][k]) + (li[p] - lj[k])) * dj[p][k]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m[k] = acc[p][k] * fast_exp2(ci[p] - lj[p][k]);
+                for (int k = 0; k < 4; ++k) m[k] = acc[p][k] * fast_exp2((ci[p] - cj[p][k]) + (li[p] - dj[p][k]));
             }
             if (ti[p] == tj[p]) {
 #pragma unroll
