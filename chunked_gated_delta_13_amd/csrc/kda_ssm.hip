@@ -11,7 +11,9 @@
 // never a quotient of large factors, so nothing overflows that the recurrence itself does not.
 // One workgroup of p/16 waves runs a (sequence, head, segment) with the state in registers: a wave holds
 // 16 columns of S as accumulator tiles, which are at once the operand of S^T C (with S rounded to bf16
-// for that product only).  x, B and C are staged once per chunk in LDS and read there both row by row
+// for that product only).  The weights M_ij of x_j are rounded to bf16 as the other operand that forms y:
+// in two parts they would need a second set of LDS tiles, for which the wide form has no room (151 of 160 KB),
+// and the product again.  What both roundings leave is 2.2e-3 of y, 1.7e-3 of it the output's own.  x, B and C are staged once per chunk in LDS and read there both row by row
 // and transposed.  The update must not lose the state's 32 bits: x and B are exact in bf16 and the
 // weighted x is fed as three bf16 parts (24 bits of it), three products instead of one.
 // A long sequence is split into segments where there are fewer (sequence, head) pairs than the GPU holds
@@ -193,7 +195,7 @@ template <int N, int P, typename T, int NW> struct Mixer {
         }
     }
 
-    // M[i][j] = e^{c_i - c_j} dt_j (C_i . B_j) for j <= i: K of the ten lower 16 x 16 tiles side by side
+    // M[i][j] = e^{c_i - c_j} dt_j (C_i . B_j) for j <= i, rounded to T: K of the ten lower 16 x 16 tiles side by side
     // (pair 0 .. 9, row by row), each a chain from LDS through the matrix cores and an exponential
     template <int K>
     __device__ __forceinline__ void mix(KDA_LDS T* sM, const KDA_LDS ChunkDecay* cd, const int (&pair)[K], int lane) const {

@@ -373,8 +373,9 @@ kda_status_t kda_conv_step(const void *x, const void *w, const void *bias, void 
  *              written before it is read; calls that overlap in time need one each
  * Rows of x, Bm, Cm and z start on 16-byte boundaries; H * p and the five strides are at most 2^22
  * elements, B * H at most 2^22, and B * H segments of a split sequence at most 2^20.  T == 0 is valid: S_T receives S0 (or zeros).
- * B == 0 or H == 0 is a no-op.  States and exponents are fp32; with bf16 inputs the state is rounded to
- * bf16 only as the operand of S^T C, never in its update.
+ * B == 0 or H == 0 is a no-op.  States and exponents are fp32.  With bf16 inputs two operands of the products
+ * that form y are rounded to bf16: the state in S^T C, and the weights e^(c_i - c_j) dt_j (C_i . B_j) by
+ * which a token takes the inputs of its own block of 64; the state's update rounds neither.
  */
 size_t kda_ssm_prefill_workspace_bytes(int B, int T, int H, int G, int n, int p, kda_dtype_t dtype,
                                        int seg_len);
