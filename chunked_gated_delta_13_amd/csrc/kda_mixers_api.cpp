@@ -313,7 +313,8 @@ void window_prefill_plan(int B, int T, int H, int d, int window, int sinks, kda_
     if (split < whole) *n_split = (int)n;
 }
 
-bool scale_ok(float scale) { return scale > 0.0f && scale <= 3.0e38f; }
+// The kernels take exponentials of base 2: scale log2(e) has to be a finite number too.
+bool scale_ok(float scale) { return scale > 0.0f && scale <= 2.3e38f; }
 
 }  // namespace
 

@@ -414,7 +414,7 @@ kda_status_t kda_ssm_step(const void *x, const void *dt, const float *A, const v
  *                     sinks + (p - sinks) mod window.  Rows no token has reached are never read.
  *   start      [B] int32 DEVICE or NULL (0)   tokens of each sequence before this call (needs the caches)
  *   o          [B, T, H, d]    dtype  (out)
- *   d          64 or 128;  window >= 1;  sinks >= 0;  scale > 0
+ *   d          64 or 128;  window >= 1;  sinks >= 0;  0 < scale <= 2.3e38 (scale log2(e) is finite)
  * Rows of q, k and v start on 16-byte boundaries.  T == 0, B == 0 or H == 0 is a no-op.  B is at most
  * 65535, H at most 65536, T and window + sinks at most 2^29, B H (T / 64 + 1) at most 2^23, and the kept
  * rows of one sequence (sinks and the smaller of window and T) at most 32 GiB per cache.  A few queries

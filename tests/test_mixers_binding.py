@@ -110,3 +110,14 @@ def test_the_c_library_is_built_without_torch(monkeypatch):
     monkeypatch.setattr(kbuild, "_compile", lambda src: src + ".o")
     monkeypatch.setattr(kbuild, "_link", lambda objs, out: linked.append(out))
     assert kbuild.build() == kbuild.LIB and linked == [kbuild.LIB, kbuild.PEAKS_LIB]
+
+
+@pytest.mark.parametrize("scale,status", [(2.2e38, 0), (2.4e38, 1), (3.0e38, 1)])
+def test_a_scale_whose_base_2_form_is_infinite_is_refused(scale, status):
+    """fp32 holds numbers up to 3.40e38; scale log2(e) passes it from 2.36e38 on, and scores of 0 became NaN.
+    Without tokens an accepted call is a no-op."""
+    from chunked_gated_delta_13_amd import _lib
+    lib = _lib.load()
+    none = [None] * 8
+    assert lib.kda_window_prefill(*none, 1, 0, 2, 1, 64, 5, 0, scale, 128, 64, 64, 0, None, 0, None) == status
+    assert lib.kda_window_step(*[None] * 7, 0, 2, 1, 64, 5, 0, scale, 128, 64, 64, 0, None, 0, None) == status
