@@ -128,3 +128,20 @@ def test_running_maximum_is_raised_inside_whole_tiles(dtype, B, T, H, Hkv, d):
     o = kda.window_prefill(q, k, v, win, sinks)
     torch.cuda.synchronize()
     _check(q, k, v, win, sinks, scale, None, None, None, None, o, dtype)
+
+
+def test_negative_counts_of_earlier_tokens_count_as_none():
+    kda = _kda()
+    B, T, H, Hkv, d, win, sinks = 2, 40, 4, 2, 64, 20, 3
+    q, k, v = _r(1, "bf16", B, T, H, d), _r(2, "bf16", B, T, Hkv, d), _r(3, "bf16", B, T, Hkv, d)
+    got = []
+    for n in (0, -1, -2 ** 31):
+        kc, vc = (torch.full((B, sinks + win, Hkv, d), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        before = torch.full((B,), n, dtype=torch.int32, device="cuda")
+        o = kda.window_prefill(q, k, v, win, sinks, k_cache=kc, v_cache=vc, start=before)
+        kc1, vc1 = kc.clone(), vc.clone()
+        s = kda.window_step(q[:, 0], k[:, 0], v[:, 0], kc1, vc1, before, win, sinks)
+        got.append((o, kc, vc, s, kc1, vc1))
+    torch.cuda.synchronize()
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
