@@ -2,8 +2,8 @@
 //
 // A token of these operators keeps the device busy for a few microseconds, so checks and marshalling
 // count: here they take about 1 us of a call (2.5 with two tensors to allocate), written in Python 5.5 to
-// 9.  One token of the convolution, of the scan and of the attention takes 4.6, 4.9 and 9.9 us a call, 3.4,
-// 3.8 and 6.4 of them the library's own launches.  The entry points of libkda are handed over by
+// 9.  One token of the convolution, of the scan and of the attention takes 4.6, 4.9 and 10.2 us a call, 3.4,
+// 3.8 and 6.4 of them the host's part of the library's own launches.  The entry points of libkda are handed over by
 // bind(), so that a process holds one copy of the library; nothing here is linked to it.
 #include <Python.h>
 

@@ -9,8 +9,10 @@
 // owns one 16-byte group of channels (so that a wave reads and writes 1 KiB runs of a row) and
 // walks a tile of consecutive tokens with the last W - 1 inputs in registers, so each input is
 // read once per tile and W - 1 more times per tile boundary, from cache.  4 x 8192 tokens of 7424
-// channels in bf16 (0.97 GB) take 174 us, 5.6 TB/s, above a device copy's 4.9; one token of 256
-// sequences (30 MB) takes 6.1 us, one token of one sequence 4.6 us a call, which is the launch.
+// channels in bf16 (0.97 GB) take 174 us, 5.6 TB/s, above a device copy's 4.9, in fp32 348 us; one token of
+// 256 sequences (30 MB) takes 6.7 us, one token of one sequence 4.6 us a call, 3.4 of them the launch.
+// Rows off 16 bytes (a width that is no multiple of 8 in bf16, of 4 in fp32) are taken one channel per
+// thread: 4095 channels run at 3.7 TB/s in bf16 and 4.6 in fp32, 4096 in bf16 at 6.1.
 #include "kda_device.h"
 #include "kda_mixers.h"
 

@@ -20,11 +20,13 @@
 // workgroups: a first pass forms every segment's final state from zero, a small kernel joins them (the
 // transition of a segment is one number per head), and the second pass runs every segment from its entry
 // state.
-// What bounds it: 4 x 16384 tokens of 56 heads, n = p = 128, bf16, take 1.00 ms, 300 TFLOP/s of the
+// What bounds it: 4 x 16384 tokens of 56 heads, n = p = 128, bf16, take 1.01 ms, 297 TFLOP/s of the
 // formulas' products; the 2.87 GB they cannot do without take 0.58 ms.  A SIMD holds two waves, each a
 // chain LDS - matrix cores - vector unit - LDS, and of 8000 cycles a chunk issues vector instructions in
 // 4300 and products in 2430; the 224 sequences and heads leave 32 of 256 compute units without work.  One sequence of 20001 tokens, 16 heads, n = 128, p = 64 takes 90 us, 26 of
 // them the first pass, 9 the join between two launches, 55 the outputs (ten chunks one after the other).
+// In fp32, 4 x 4096 tokens of 56 heads take 861 us at n = p = 128 (matrix cores busy in 72% of the cycles; the
+// formulas' products at a library product's 154 TFLOP/s would take 488), 616 at p = 64 and 390 at n = p = 64.
 //
 // Token.  One streaming pass over the state, bound by HBM: 8 bytes of traffic per state element.
 #include "kda_mixers.h"
@@ -420,7 +422,7 @@ template <int N, int P, typename T, int NW> struct Mixer {
 // AHEAD: M of the next chunk is formed beside the outputs of this one, over three sets of B and C tiles,
 // two of x and two of M: one barrier per chunk, and every wave has independent work for the matrix
 // cores, the vector unit and the LDS all through it.  It takes most of the LDS, so one workgroup runs per
-// compute unit: taken for p = 128 in bf16, whose eight waves fill it alone (1.00 ms for the long prompts
+// compute unit: taken for p = 128 in bf16, whose eight waves fill it alone (1.01 ms for the long prompts
 // above, 1.22 with the plain schedule of three barriers).  The plain one leaves room for a second
 // workgroup, which p = 64 needs; fp32 tiles leave no room for more sets.
 template <int N, int P, typename T, bool OUT, int NW, bool AHEAD>

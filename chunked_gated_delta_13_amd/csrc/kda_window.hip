@@ -27,7 +27,7 @@ __device__ __forceinline__ int ring_row(uint32_t p, int sinks, int window) {
 
 // Over the four lanes 16 apart that share a query.  SWAP: rows of 16 lanes are swapped pairwise, then halves,
 // on the vector unit; else the values go round through LDS, which takes longer (ragged prompts of the
-// smallest kind 11.8 us instead of 11.4, one token 10.1 instead of 9.8) but leaves the registers of the
+// smallest kind 11.8 us instead of 11.4, one token 0.3 us more) but leaves the registers of the
 // kernel of 32 queries per wave as they are (the swaps make it spill: 2.55 ms instead of 1.59).
 template <bool SWAP, typename F> __device__ __forceinline__ float over_groups(float v, F f) {
     if constexpr (SWAP) {
@@ -90,11 +90,14 @@ template <typename T> __device__ __forceinline__ void store4(T* p, const f32x4_t
 // one of two LDS tiles, one tile ahead, and two workgroups share a compute unit: while one wave of a
 // SIMD forms exponentials, the other feeds the matrix cores.  (Through registers, written to LDS a tile
 // later, the same keys take 1.83 ms instead of 1.68.)
-// What bounds it: 16384 tokens, 56 heads on 8, d = 128, window 4096 in bf16 take 1.59 ms, 1.06 PFLOP/s of
-// the visible products; a large library product reaches 1.30.  Matrix instructions and exponentials of
+// What bounds it: 16384 tokens, 56 heads on 8, d = 128, window 4096 in bf16 take 1.59 to 1.65 ms by card, 1.02
+// to 1.06 PFLOP/s of the visible products; a large library product reaches 1.23 to 1.35.  Matrix instructions and exponentials of
 // the two waves do not overlap without gaps, and tiles at the window's two edges are multiplied whole.
 // Pieces of a few hundred tokens (5 sequences of up to 333, window 200, d = 64) take 11.4 us, bound by
 // the chain of a workgroup: lengths, first keys, five tiles, and the launch that keeps the new rows.
+// In fp32, 8192 tokens, 16 heads on 4, window 1024 take 740 us at d = 128 and 344 at d = 64, 87 and 94 TFLOP/s
+// of the 154 that a library product reaches: the matrix cores are busy in 68 and 73% of the cycles, and at d =
+// 128 two pairs of tiles (128 KB) leave room for one wave a SIMD, with nothing beside its exponentials.
 //
 // The running maximum only has to keep exponentials in range.  A tile that every query of the wave sees
 // whole is taken with the maximum at hand, without forming its own; only if a sum of its exponentials
@@ -416,8 +419,8 @@ __global__ __launch_bounds__(256) void kda_window_keep_kernel(const WindowArgs a
 }
 
 // One token, bound by HBM: every visible key and value is read once (64 sequences, 8 kv heads, d = 128, 4100
-// rows in bf16: 1.08 GB in 196 us, 5.5 TB/s; a plain read of the same memory reaches 6.9).  One sequence
-// takes 9.8 us, a chain of two launches, positions, keys and values.  A workgroup of four waves runs up to
+// rows in bf16: 1.08 GB in 197 us, 5.5 TB/s; a plain read of the same memory reaches 6.9; in fp32 370 us, 5.8
+// TB/s).  One sequence takes 10.2 us (16.5 in fp32), a chain of two launches, positions, keys and values.  A workgroup of four waves runs up to
 // 16 query heads of one (sequence, kv head) over one
 // range of cache rows; each wave takes every fourth tile of 32 rows with statistics of its own, and the
 // waves (then the ranges) are joined at the end.  Keys go from memory straight into the operand; values

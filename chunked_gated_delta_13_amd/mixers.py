@@ -5,6 +5,8 @@ Signatures and their documentation; checks and marshalling are in csrc/binding (
 token of these operators keeps the device busy for a few microseconds only.  Inputs may be slices of a
 projection's rows: tokens of one tensor lie a fixed stride apart and the elements of a token are
 contiguous.  Outputs and states are contiguous.  Calls run on the current stream of the tensors' device.
+Like KDA's own calls they form no gradients: results are detached, also where an input requires one.
+Tensors without memory of their own (inside torch.vmap, torch.func or a fake tensor mode) are refused.
 """
 from __future__ import annotations
 
@@ -57,7 +59,8 @@ def conv_prefill(x, w, bias=None, state=None, *, lens=None, silu=True, y=None, s
     x [B, T, D] (rows may be strided), w [D, W] with W 2, 3 or 4, bias [D]; ``state`` [B, W-1, D] are
     the inputs before the first token (None = zeros), ``state_out`` the last W-1 inputs of each
     sequence (may be ``state`` itself; None when return_state is False).  ``lens`` (int32 [B]) gives
-    the tokens of each sequence of a padded batch; rows of y behind them are left as they were.
+    the tokens of each sequence of a padded batch; rows of y behind them are left as they were.  Widths
+    of whole 16-byte groups of channels run about half again as fast as others.
     """
     return (_native or _load()).conv_prefill(x, w, bias, state, lens, silu, y, state_out, return_state)
 
@@ -125,5 +128,6 @@ def window_step_workspace_bytes(N, H, Hkv, d, window, sinks=0, dtype=None):
 
 def window_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, o=None, workspace=None):
     """The same attention for one new token of N sequences over their ring caches, which receive the
-    token's k and v: q [N, H, d], k, v [N, Hkv, d], ``pos`` (int32 [N]) the tokens before it.  Returns o."""
+    token's k and v: q [N, H, d], k, v [N, Hkv, d], ``pos`` (int32 [N]) the tokens before it (negative values
+    count as 0).  Returns o."""
     return (_native or _load()).window_step(q, k, v, k_cache, v_cache, pos, window, sinks, scale, o, workspace)

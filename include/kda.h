@@ -333,7 +333,8 @@ kda_status_t kda_chunk_prefill_noalloc(const void *q, const void *k, const void 
  *   W          2, 3 or 4
  *   silu       0: act is the identity, else x * sigmoid(x)
  * T == 0 is valid: state_out receives state_in (or zeros).  B == 0 or D == 0 is a no-op.  Pointers
- * need only the alignment of their elements; rows that all start on 16-byte boundaries run faster.
+ * need only the alignment of their elements; rows that all start on 16-byte boundaries (D and x_stride whole
+ * groups of 16 bytes too) run at 5.6 to 6.1 TB/s of traffic, others at 3.7 in bf16 and 4.6 in fp32.
  * B is at most 65535, D at most 2^28.
  */
 kda_status_t kda_conv_prefill(const void *x, const void *w, const void *bias, const void *state_in,
@@ -412,16 +413,19 @@ kda_status_t kda_ssm_step(const void *x, const void *dt, const float *A, const v
  *   k_cache, v_cache  [B, sinks + window, Hkv, d] dtype, in/out, or both NULL (no earlier tokens, none
  *                     kept): token p lies in row p for p < sinks, else in row
  *                     sinks + (p - sinks) mod window.  Rows no token has reached are never read.
- *   start      [B] int32 DEVICE or NULL (0)   tokens of each sequence before this call (needs the caches)
+ *   start      [B] int32 DEVICE or NULL (0)   tokens of each sequence before this call (needs the caches);
+ *                                             negative values count as 0
  *   o          [B, T, H, d]    dtype  (out)
  *   d          64 or 128;  window >= 1;  sinks >= 0;  0 < scale <= 2.3e38 (scale log2(e) is finite)
  * Rows of q, k and v start on 16-byte boundaries.  T == 0, B == 0 or H == 0 is a no-op.  B is at most
- * 65535, H at most 65536, T and window + sinks at most 2^29, B H (T / 64 + 1) at most 2^23, and the kept
- * rows of one sequence (sinks and the smaller of window and T) at most 32 GiB per cache.  A few queries
- * over a long window are run as ranges of their keys, joined afterwards, when a workspace of
- * kda_window_prefill_workspace_bytes(...) bytes is given (`continued`: 1 where start is; calls that overlap
- * in time need one each); with NULL they run as one range.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded to bf16 as the
- * operand of the product with v.
+ * 65535, H at most 65536, T and window + sinks at most 2^29, B H (T / 64 + 1) at most 2^23, and the
+ * kept rows of one sequence (sinks and the smaller of window and T) at most 32 GiB per cache.  A few
+ * queries over a long window are run as ranges of their keys, joined afterwards, when a workspace of
+ * kda_window_prefill_workspace_bytes(...) bytes is given (`continued`: 1 where start is; calls that
+ * overlap in time need one each); with NULL they run as one range.  Scores have to lie inside fp32's
+ * range: one below it has no weight, a query with none inside it, or with one above it, gets NaN.
+ * Statistics and sums are fp32; with bf16 inputs the probabilities are rounded to bf16 as the operand
+ * of the product with v.
  */
 size_t kda_window_prefill_workspace_bytes(int B, int T, int H, int Hkv, int d, int window, int sinks,
                                           kda_dtype_t dtype, int continued);
@@ -434,10 +438,10 @@ kda_status_t kda_window_prefill(const void *q, const void *k, const void *v, voi
 
 /*
  * One new token of N sequences over their ring caches: q [N, H, d], k, v [N, Hkv, d], o [N, H, d].
- * pos [N] int32 (DEVICE): tokens of each sequence before this one.  The token's k and v are written to
- * their row of the caches and are visible to its own query.  The workspace holds
- * kda_window_step_workspace_bytes(...) bytes (may be NULL when that is 0); calls that overlap in time
- * need one each.  With bf16 inputs a probability enters the product with v as two bf16 parts (16 bits).
+ * pos [N] int32 (DEVICE): tokens of each sequence before this one (negative values count as 0).  N is at
+ * most 65535, N H at most 2^23.  The token's k and v are written to their row of the caches and are visible
+ * to its own query.  The workspace holds kda_window_step_workspace_bytes(...) bytes (may be NULL when that is
+ * 0); calls that overlap in time need one each.  With bf16 inputs a probability enters the product with v as two bf16 parts (16 bits).
  */
 size_t kda_window_step_workspace_bytes(int N, int H, int Hkv, int d, int window, int sinks,
                                        kda_dtype_t dtype);
