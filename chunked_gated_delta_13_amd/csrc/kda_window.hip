@@ -9,8 +9,10 @@
 // exponentials of base 2).  Scores are formed transposed, K Q^T with keys as rows: a lane then holds
 // four keys of one query, the statistics of a query stay in its lanes, and the probabilities are at
 // once the operand of V^T P^T.  For that product only they are rounded to the input type in the prompt
-// form, whose time is its products (P in two parts would add half of them again); the one-token form, bound
-// by HBM, feeds bf16 ones as two parts.
+// form: outputs are 2.0 to 2.3e-3 off in bf16, 1.7e-3 of it their own rounding.  P in two parts leaves only the
+// latter, but adds half the products again: a prompt of model width takes 4050 us instead of 1614 (the operands
+// spill), 2048 tokens of 8 heads 30.5 instead of 26.3, short pieces 12.4 instead of 11.5.  The one-token form,
+// bound by HBM, feeds bf16 ones as two parts.
 #include "kda_mixers.h"
 #include "kda_tile.h"
 
