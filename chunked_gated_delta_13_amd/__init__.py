@@ -16,6 +16,13 @@ Beside KDA, the token mixers of mixers.py, each with a prompt and a one-token fo
     y, S_T   = ssm_prefill(x, dt, A, Bm, Cm, S0, D=D, z=z) # selective state space scan
     o        = window_prefill(q, k, v, window, sinks, k_cache=kc, v_cache=vc)
     conv_step, ssm_step, window_step                       # state or cache updated in place
+
+and a full-attention layer's parts:
+
+    o        = attn_prefill(q, k, v, cu_q, cu_k)           # causal, packed prompts
+    cache_write(k, v, k_cache, v_cache, pages, cu, start)  # 4 bits an element, paged
+    k, v     = cache_read(k_cache, v_cache, pages, cu, tokens, d)
+    o        = attn_step(q, k_cache, v_cache, pages, lens)
 """
 from __future__ import annotations
 
@@ -23,11 +30,14 @@ import ctypes
 
 from . import _lib
 from ._lib import KDAError
-from .mixers import (conv_prefill, conv_step, ssm_prefill, ssm_step, ssm_workspace_bytes, window_prefill,
-                     window_prefill_workspace_bytes, window_step, window_step_workspace_bytes)
+from .mixers import (attn_prefill, attn_prefill_workspace_bytes, attn_step, attn_step_workspace_bytes, cache_page_bytes,
+                     cache_read, cache_write, conv_prefill, conv_step, ssm_prefill, ssm_step, ssm_workspace_bytes,
+                     window_prefill, window_prefill_workspace_bytes, window_step, window_step_workspace_bytes)
 
 __all__ = ["conv_prefill", "conv_step", "ssm_prefill", "ssm_step", "ssm_workspace_bytes",
            "window_prefill", "window_prefill_workspace_bytes", "window_step", "window_step_workspace_bytes",
+           "attn_prefill", "attn_prefill_workspace_bytes", "attn_step", "attn_step_workspace_bytes",
+           "cache_page_bytes", "cache_read", "cache_write",
            "chunk_prefill", "chunk_prefill_ckpt", "chunk_prefill_gate", "chunk_prefill_noalloc",
            "decode_step", "spec_verify", "spec_commit", "prefill_plan", "prefill_workspace_bytes",
            "abi_version", "KDAError", "load_library"]

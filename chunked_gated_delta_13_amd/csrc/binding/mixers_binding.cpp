@@ -40,6 +40,12 @@ struct Library {
     decltype(&kda_window_prefill) window_prefill;
     decltype(&kda_window_step_workspace_bytes) window_step_workspace_bytes;
     decltype(&kda_window_step) window_step;
+    decltype(&kda_attn_prefill_workspace_bytes) attn_prefill_workspace_bytes;
+    decltype(&kda_attn_prefill) attn_prefill;
+    decltype(&kda_cache_write) cache_write;
+    decltype(&kda_cache_read) cache_read;
+    decltype(&kda_attn_step_workspace_bytes) attn_step_workspace_bytes;
+    decltype(&kda_attn_step) attn_step;
 } lib;
 PyObject* on_status = nullptr;   // called with a status and the name of the call that returned it
 
@@ -105,7 +111,9 @@ struct Common {
     c10::Device dev;
     kda_dtype_t code;
 
-    Common(const char* where_, const Tensor& t) : where(where_), type(t.scalar_type()), dev(t.device()) {
+    Common(const char* where_, const Tensor& t) : Common(where_, t, t.scalar_type()) {}
+    // calls whose first tensor is not of the type that they compute in
+    Common(const char* where_, const Tensor& t, at::ScalarType ty) : where(where_), type(ty), dev(t.device()) {
         if (!t.is_cuda()) throw refusal<WrongValue>(where, " runs on a HIP device; got a tensor on ", dev);
         if (type == at::kBFloat16) code = KDA_BF16;
         else if (type == at::kFloat) code = KDA_F32;
@@ -461,6 +469,139 @@ PyObject* window_step(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     END_HANDLE_TH_ERRORS
 }
 
+// q, k, v, cu_q, cu_k, scale, o, workspace
+PyObject* attn_prefill(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    if (!arity(nargs, 8)) return nullptr;
+    const Args a{args};
+    const Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k"), &v = a.tensor(2, "v"), &cu_q = a.tensor(3, "cu_q");
+    const Common c("attn_prefill", q);
+    if (q.dim() != 3 || k.dim() != 3) throw refusal<WrongValue>("q must be [Nq, H, d] and k [Nk, Hkv, d]");
+    const Tensor* cu_k = a.optional(4, "cu_k");
+    const int nq = size(q.size(0)), H = size(q.size(1)), d = size(q.size(2)), nk = size(k.size(0)), Hkv = size(k.size(1));
+    const Shape kv{nk, Hkv, d};
+    const long long qs = c.rows("q", q, q.sizes(), 1), ks = c.rows("k", k, kv, 1), vs = c.rows("v", v, kv, 1);
+    if (cu_q.dim() != 1 || cu_q.size(0) < 1) throw refusal<WrongValue>("cu_q must be [B + 1], got ", cu_q.sizes());
+    c.whole("cu_q", cu_q, at::kInt, cu_q.sizes());
+    if (cu_k) c.whole("cu_k", *cu_k, at::kInt, cu_q.sizes());
+    else if (nk != nq) throw refusal<WrongValue>("without cu_k there are as many keys as queries, got ", (int64_t)nk, " and ", (int64_t)nq);
+    const int b = size(cu_q.size(0) - 1);
+    const float scale = a.scale(5, d);
+    Pending po(c, a, 6, "o", c.type, q.sizes());
+    const Tensor* room = a.optional(7, "workspace");
+    const OnDevice on(c.dev);
+    const Workspace ws(c, room, lib.attn_prefill_workspace_bytes(b, nq, nk, H, Hkv, d, c.code));
+    const Output& o = po.make(c);
+    if (!c.call(lib.attn_prefill, ptr(q), ptr(k), ptr(v), at_type<int>(&cu_q), at_type<int>(cu_k), o.ptr(), b, nq, nk, H, Hkv, d,
+                scale, qs, ks, vs, c.code, ws.p, ws.bytes))
+        return nullptr;
+    return o.object();
+    END_HANDLE_TH_ERRORS
+}
+
+// A paged cache: its two pools from argument `o` on and its table behind them.
+struct Pages {
+    const Tensor &kc, &vc, &table;
+    int n_pages, Hkv, max_pages, page;
+    int64_t B;
+
+    Pages(const Common& c, const Args& a, int o, int64_t d)
+        : kc(a.tensor(o, "k_cache")), vc(a.tensor(o + 1, "v_cache")), table(a.tensor(o + 2, "pages")) {
+        if (kc.dim() != 3 || table.dim() != 2) throw refusal<WrongValue>("k_cache must be [n_pages, Hkv, bytes] and pages [B, max_pages]");
+        c.whole("k_cache", kc, at::kByte, kc.sizes());
+        c.whole("v_cache", vc, at::kByte, kc.sizes());
+        c.whole("pages", table, at::kInt, table.sizes());
+        const int64_t row = d / 2 + d / 32;   // bytes of a token's row
+        if (d < 32 || d % 32 != 0 || kc.size(2) % row != 0 || kc.size(2) == 0)
+            throw refusal<WrongValue>("a page of k_cache must hold whole rows of d / 2 + d / 32 bytes, got ", kc.size(2), " bytes for d = ", d);
+        page = size(kc.size(2) / row);
+        n_pages = size(kc.size(0));
+        Hkv = size(kc.size(1));
+        B = table.size(0);
+        max_pages = size(table.size(1));
+    }
+};
+
+// k, v, k_cache, v_cache, pages, cu, start
+PyObject* cache_write(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    if (!arity(nargs, 7)) return nullptr;
+    const Args a{args};
+    const Tensor &k = a.tensor(0, "k"), &v = a.tensor(1, "v");
+    const Common c("cache_write", k);
+    if (k.dim() != 3) throw refusal<WrongValue>("k must be [N, Hkv, d]");
+    const Pages p(c, a, 2, k.size(2));
+    const Shape kv{k.size(0), p.Hkv, k.size(2)};
+    const long long ks = c.rows("k", k, kv, 1), vs = c.rows("v", v, kv, 1);
+    const Tensor *cu = a.optional(5, "cu"), *start = a.optional(6, "start");
+    if (cu) c.whole("cu", *cu, at::kInt, {p.B + 1});
+    else if (k.size(0) != p.B) throw refusal<WrongValue>("without cu there is one token for each row of pages, got ", k.size(0), " and ", p.B);
+    if (start) c.whole("start", *start, at::kInt, {p.B});
+    const int b = size(p.B), n = size(k.size(0)), d = size(k.size(2));
+    const OnDevice on(c.dev);
+    if (!c.call(lib.cache_write, ptr(k), ptr(v), ptr(p.kc), ptr(p.vc), at_type<int>(&p.table), at_type<int>(cu), at_type<int>(start),
+                b, n, p.Hkv, d, p.n_pages, p.max_pages, p.page, ks, vs, c.code))
+        return nullptr;
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// k_cache, v_cache, pages, cu, tokens, d, start, dtype, k, v
+PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    if (!arity(nargs, 10)) return nullptr;
+    const Args a{args};
+    at::ScalarType type = at::kBFloat16;
+    if (a.a[7] != Py_None) {
+        if (!THPDtype_Check(a.a[7])) throw refusal<WrongType>("dtype must be a torch.dtype, got ", std::string(Py_TYPE(a.a[7])->tp_name));
+        type = reinterpret_cast<THPDtype*>(a.a[7])->scalar_type;
+    }
+    const Common c("cache_read", a.tensor(0, "k_cache"), type);
+    const int n = a.size(4), d = a.size(5);
+    if (n < 0 || d < 0) throw refusal<WrongValue>("tokens and d must not be negative");
+    const Pages p(c, a, 0, d);
+    const Tensor *cu = a.optional(3, "cu"), *start = a.optional(6, "start");
+    if (cu) c.whole("cu", *cu, at::kInt, {p.B + 1});
+    else if (n != p.B) throw refusal<WrongValue>("without cu there is one token for each row of pages, got ", (int64_t)n, " and ", p.B);
+    if (start) c.whole("start", *start, at::kInt, {p.B});
+    const int b = size(p.B);
+    Pending pk(c, a, 8, "k", type, {n, p.Hkv, d}), pv(c, a, 9, "v", type, {n, p.Hkv, d});
+    const OnDevice on(c.dev);
+    const Output &k = pk.make(c), &v = pv.make(c);
+    if (!c.call(lib.cache_read, ptr(p.kc), ptr(p.vc), at_type<int>(&p.table), at_type<int>(cu), at_type<int>(start), k.ptr(), v.ptr(), b,
+                n, p.Hkv, d, p.n_pages, p.max_pages, p.page, c.code))
+        return nullptr;
+    return pair(k, v);
+    END_HANDLE_TH_ERRORS
+}
+
+// q, k_cache, v_cache, pages, lens, scale, o, workspace
+PyObject* attn_step(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    if (!arity(nargs, 8)) return nullptr;
+    const Args a{args};
+    const Tensor &q = a.tensor(0, "q"), &lens = a.tensor(4, "lens");
+    const Common c("attn_step", q);
+    if (q.dim() != 3 && q.dim() != 4) throw refusal<WrongValue>("q must be [N, H, d] or [N, m, H, d]");
+    const int lead = (int)q.dim() - 2;
+    const int m = lead == 2 ? size(q.size(1)) : 1, H = size(q.size(lead)), d = size(q.size(lead + 1)), N = size(q.size(0));
+    const long long qs = c.rows("q", q, q.sizes(), lead);
+    const Pages p(c, a, 1, d);
+    if (p.B != N) throw refusal<WrongValue>("pages must have a row for each of the ", (int64_t)N, " sequences, got ", p.B);
+    c.whole("lens", lens, at::kInt, {N});
+    const float scale = a.scale(5, d);
+    Pending po(c, a, 6, "o", c.type, q.sizes());
+    const Tensor* room = a.optional(7, "workspace");
+    const OnDevice on(c.dev);
+    const Workspace ws(c, room, lib.attn_step_workspace_bytes(N, m, H, p.Hkv, d, p.max_pages, p.page, c.code));
+    const Output& o = po.make(c);
+    if (!c.call(lib.attn_step, ptr(q), ptr(p.kc), ptr(p.vc), at_type<int>(&p.table), at_type<int>(&lens), o.ptr(), N, m, H, p.Hkv, d,
+                p.n_pages, p.max_pages, p.page, scale, qs, c.code, ws.p, ws.bytes))
+        return nullptr;
+    return o.object();
+    END_HANDLE_TH_ERRORS
+}
+
 // addresses of libkda's entry points, in the order of `Library`, and the function that raises for a status
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     constexpr int kEntries = sizeof(Library) / sizeof(void*);
@@ -479,7 +620,8 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 
 #define KDA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {KDA_METHOD(bind),     KDA_METHOD(conv_prefill),   KDA_METHOD(conv_step),   KDA_METHOD(ssm_prefill),
-                         KDA_METHOD(ssm_step), KDA_METHOD(window_prefill), KDA_METHOD(window_step), {nullptr, nullptr, 0, nullptr}};
+                         KDA_METHOD(ssm_step), KDA_METHOD(window_prefill), KDA_METHOD(window_step),
+                         KDA_METHOD(attn_prefill), KDA_METHOD(cache_write), KDA_METHOD(cache_read), KDA_METHOD(attn_step), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mixers", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

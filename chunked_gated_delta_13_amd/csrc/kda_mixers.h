@@ -1,5 +1,4 @@
-// Host <-> kernel interface of the short convolution, the state space scan and the window
-// attention inside libkda (not part of the public C ABI).
+// Host <-> kernel interface of the entry points beside KDA inside libkda (not part of the public C ABI).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -79,5 +78,57 @@ struct WindowArgs {
 
 hipError_t launch_window_prefill(int d, bool f32, const WindowArgs& a, hipStream_t s);
 hipError_t launch_window_step(int d, bool f32, const WindowArgs& a, hipStream_t s);
+
+struct AttnArgs {
+    const void* q;            // [Nq] rows of H * d, stride q_stride elements
+    const void* k;            // [Nk] rows of Hkv * d
+    const void* v;
+    const int* cu_q;          // [B + 1] first rows of the sequences and the last one's end (device)
+    const int* cu_k;          // the same of the keys; may be cu_q
+    void* o;                  // [Nq, H, d]
+    long long q_stride, k_stride, v_stride;
+    int B, Nq, Nk, H, Hkv;
+    float scale;
+    int few;                  // 1: too few rows for 128 of them per workgroup
+    int n_split;              // ranges of keys
+    long long per_xcd;        // eighths of the row tiles
+    float* ws_o;              // [Nq * H, n_split, d] partial outputs of a split call
+    float* ws_ml;             // [Nq * H, n_split, 2] their maxima (base 2) and sums
+};
+
+hipError_t launch_attn_prefill(int d, bool f32, const AttnArgs& a, hipStream_t s);
+
+struct CacheArgs {
+    const void* k;            // [N] rows of Hkv * d, stride k_stride elements (written ones)
+    const void* v;
+    void* k_out;              // [N, Hkv, d] (read ones)
+    void* v_out;
+    uint8_t* k_cache;         // [n_pages, Hkv, page_bytes]
+    uint8_t* v_cache;
+    const int* pages;         // [B, max_pages]
+    const int* cu;            // [B + 1], or nullptr: token i is sequence i's
+    const int* start;         // [B] position of each sequence's first token, or nullptr (0)
+    long long k_stride, v_stride, page_bytes;
+    int B, N, Hkv, n_pages, max_pages, page, page_shift;
+};
+
+hipError_t launch_cache_rows(bool write, int d, bool f32, const CacheArgs& a, hipStream_t s);
+
+struct AttnStepArgs {
+    const void* q;            // [N * m] rows of H * d, stride q_stride elements
+    const uint8_t* k_cache;   // [n_pages, Hkv, page_bytes]
+    const uint8_t* v_cache;
+    const int* pages;         // [N, max_pages]
+    const int* lens;          // [N] tokens in the cache, the m new ones among them
+    void* o;                  // [N, m, H, d]
+    long long q_stride, page_bytes;
+    int N, m, H, Hkv, n_pages, max_pages, page, page_shift;
+    float scale;
+    int want, slots;          // slots that the sequences share, and the most there can be
+    float* ws_o;              // [slots, m * H, d] partial outputs
+    float* ws_ml;             // [slots, m * H, 2] their maxima (base 2) and sums
+};
+
+hipError_t launch_attn_step(int d, bool f32, const AttnStepArgs& a, hipStream_t s);
 
 }  // namespace kda

@@ -12,33 +12,36 @@
 #include "kda_host.h"
 #include "kda_mixers.h"
 
-using kda::Range;
-using kda::aligned;
-using kda::mul_ok;
-using kda::overlap;
-using kda::range_of;
+using namespace kda::host;
+
+namespace kda {
+namespace host {
+
+// Compute units of the current device (256 where the runtime does not say).
+int cu_count() {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) {
+            (void)hipGetLastError();
+            n = 256;
+        }
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+}  // namespace host
+}  // namespace kda
 
 namespace {
 
-constexpr long long kMaxGridYZ = 65535;   // blocks of a launch along y or z
-// Workgroups of a launch along x: up to 512 threads each, and fewer than 2^32 threads in all.
-constexpr long long kMaxUnits = 1LL << 22;
 constexpr size_t kStreamedBytes = (size_t)192 << 20;   // outputs that do not stay in the 256 MB last-level cache
-
-size_t elem_size(kda_dtype_t dt) { return dt == KDA_BF16 ? 2 : 4; }
-
-// The bytes spanned by `rows` rows of `width` elements whose starts lie `stride` elements apart.
-Range rows_range(const void* p, long long rows, long long width, long long stride, size_t esz) {
-    if (rows <= 0 || width <= 0 || !p) return range_of(p, 0);
-    return range_of(p, ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * esz);
-}
-
-// rows * stride elements stay far inside 63 bits, and a stride is at least a row's width.
-bool stride_ok(long long rows, long long width, long long stride) {
-    long long n = 0;
-    if (rows <= 1) return stride >= 0;
-    return stride >= width && mul_ok(rows, stride, &n) && n < (1LL << 58);
-}
 
 kda_status_t check_conv(const void* x, const void* w, const void* bias, int rows_b, int T, int D, int W,
                         long long x_stride, kda_dtype_t dt) {
@@ -66,25 +69,6 @@ bool conv_vec(const void* x, const void* bias, const void* s0, const void* s1, c
 }
 
 constexpr int kSsmChunk = 64;
-
-// Compute units of the current device (256 where the runtime does not say).
-int cu_count() {
-    static std::atomic<int> cached[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) {
-        (void)hipGetLastError();
-        return 256;
-    }
-    int n = cached[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) {
-            (void)hipGetLastError();
-            n = 256;
-        }
-        cached[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
 
 kda_status_t check_ssm_shape(int rows_b, int T, int H, int G, int n, int p, kda_dtype_t dt) {
     if (rows_b < 0 || T < 0 || H < 0 || G < 0) return KDA_ERR_INVALID_ARGUMENT;
@@ -142,12 +126,6 @@ size_t ssm_workspace(int B, int H, int n, int p, int n_seg) {
     if (n_seg <= 1) return 0;
     const size_t slots = (size_t)B * H * (size_t)n_seg;
     return slots * (size_t)n * p * sizeof(float) + (slots * sizeof(float) + 15) / 16 * 16;
-}
-
-// A strided row input that is read in 16-byte pieces.
-bool wide_rows_ok(const void* ptr, long long rows, long long width, long long stride, size_t esz) {
-    if (!stride_ok(rows, width, stride)) return false;
-    return aligned(ptr, 16) && (rows <= 1 || ((size_t)stride * esz) % 16 == 0);
 }
 
 struct SsmPtrs {
@@ -312,9 +290,6 @@ void window_prefill_plan(int B, int T, int H, int d, int window, int sinks, kda_
     const double whole = (double)tiles * tile_us, split = (double)((tiles + n - 1) / n) * tile_us + (double)n * part_us + 3.0;
     if (split < whole) *n_split = (int)n;
 }
-
-// The kernels take exponentials of base 2: scale log2(e) has to be a finite number too.
-bool scale_ok(float scale) { return scale > 0.0f && scale <= 2.3e38f; }
 
 }  // namespace
 

@@ -14,7 +14,7 @@
 // spill), 2048 tokens of 8 heads 30.5 instead of 26.3, short pieces 12.4 instead of 11.5.  The one-token form,
 // bound by HBM, feeds bf16 ones as two parts.
 #include "kda_mixers.h"
-#include "kda_tile.h"
+#include "kda_softmax.h"
 
 namespace kda {
 
@@ -25,64 +25,6 @@ constexpr int kKeys = 64;   // keys per tile of the prompt form
 // Row of the cache for position p (32 bits hold every position: starts are int32, prompts at most 2^29).
 __device__ __forceinline__ int ring_row(uint32_t p, int sinks, int window) {
     return p < (uint32_t)sinks ? (int)p : sinks + (int)((p - (uint32_t)sinks) % (uint32_t)window);
-}
-
-// Over the four lanes 16 apart that share a query.  SWAP: rows of 16 lanes are swapped pairwise, then halves,
-// on the vector unit; else the values go round through LDS, which takes longer (ragged prompts of the
-// smallest kind 11.8 us instead of 11.4, one token 0.3 us more) but leaves the registers of the
-// kernel of 32 queries per wave as they are (the swaps make it spill: 2.55 ms instead of 1.59).
-template <bool SWAP, typename F> __device__ __forceinline__ float over_groups(float v, F f) {
-    if constexpr (SWAP) {
-        const uint32_t u = __float_as_uint(v);
-        const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-        const uint32_t w = __float_as_uint(f(__uint_as_float(a[0]), __uint_as_float(a[1])));
-        const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-        return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
-    } else {
-        v = f(v, __shfl_xor(v, 16));
-        return f(v, __shfl_xor(v, 32));
-    }
-}
-template <bool SWAP> __device__ __forceinline__ float max_over_groups(float v) {
-    return over_groups<SWAP>(v, [](float x, float y) { return fmaxf(x, y); });
-}
-template <bool SWAP> __device__ __forceinline__ float sum_over_groups(float v) {
-    return over_groups<SWAP>(v, [](float x, float y) { return x + y; });
-}
-
-// Eight slots of one row in global memory, p at the first one: four at p and four half a row further.
-template <int D> __device__ __forceinline__ void global_frag(Frag<__bf16>& f, const __bf16* p) {
-    frag_join(f, *reinterpret_cast<const bf16x4_t*>(p), *reinterpret_cast<const bf16x4_t*>(p + D / 2));
-}
-template <int D> __device__ __forceinline__ void global_frag(Frag<float>& f, const float* p) {
-    frag_join(f, *reinterpret_cast<const f32x4_t*>(p), *reinterpret_cast<const f32x4_t*>(p + D / 2));
-}
-// Eight consecutive elements of one row (slot order 8g .. 8g + 7; both operands use it).
-__device__ __forceinline__ void global_frag8(Frag<__bf16>& f, const __bf16* p) {
-    f.v = *reinterpret_cast<const bf16x8_t*>(p);
-}
-__device__ __forceinline__ void global_frag8(Frag<float>& f, const float* p) {
-    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(p);
-    const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f.v[i] = lo[i];
-        f.v[4 + i] = hi[i];
-    }
-}
-
-// LDS accesses of one wave run in program order; this keeps the compiler from reordering them.
-__device__ __forceinline__ void wave_order() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-}
-
-template <typename T> __device__ __forceinline__ void store4(T* p, const f32x4_t& v) {
-    typedef __attribute__((ext_vector_type(4))) T vec4;
-    vec4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(v[i]);
-    *reinterpret_cast<vec4*>(p) = o;
 }
 
 }  // namespace

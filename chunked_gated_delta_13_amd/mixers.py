@@ -1,5 +1,6 @@
-"""Token mixers beside KDA: short causal convolution, selective state space scan, and attention with a
-sliding window and a few first tokens that stay visible.
+"""What stands beside KDA in a hybrid model: short causal convolution, selective state space scan, attention with a
+sliding window and a few first tokens that stay visible, causal attention over packed prompts, and a paged cache of
+4 bits an element with the attention over it.
 
 Signatures and their documentation; checks and marshalling are in csrc/binding (``_mixers.so``), since a
 token of these operators keeps the device busy for a few microseconds only.  Inputs may be slices of a
@@ -18,7 +19,9 @@ from . import _lib
 _INT_MAX = 2 ** 31 - 1
 # the library's entry points in the order in which the binding takes them
 _ENTRIES = ("kda_conv_prefill", "kda_conv_step", "kda_ssm_prefill_workspace_bytes", "kda_ssm_prefill", "kda_ssm_step",
-            "kda_window_prefill_workspace_bytes", "kda_window_prefill", "kda_window_step_workspace_bytes", "kda_window_step")
+            "kda_window_prefill_workspace_bytes", "kda_window_prefill", "kda_window_step_workspace_bytes", "kda_window_step",
+            "kda_attn_prefill_workspace_bytes", "kda_attn_prefill", "kda_cache_write", "kda_cache_read",
+            "kda_attn_step_workspace_bytes", "kda_attn_step")
 _native = None
 
 
@@ -131,3 +134,73 @@ def window_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, 
     token's k and v: q [N, H, d], k, v [N, Hkv, d], ``pos`` (int32 [N]) the tokens before it (negative values
     count as 0).  Returns o."""
     return (_native or _load()).window_step(q, k, v, k_cache, v_cache, pos, window, sinks, scale, o, workspace)
+
+
+def attn_prefill_workspace_bytes(B, Nq, Nk, H, Hkv, d, dtype=None):
+    """Device workspace bytes of attn_prefill for B sequences of Nq queries and Nk keys together on the current
+    device (dtype None = bfloat16)."""
+    _fits(B, Nq, Nk, H, Hkv, d)
+    return int(_lib.load().kda_attn_prefill_workspace_bytes(B, Nq, Nk, H, Hkv, d, _code(dtype)))
+
+
+def attn_prefill(q, k, v, cu_q, cu_k=None, *, scale=None, o=None, workspace=None):
+    """Causal attention over packed prompts of different lengths.  Returns o [Nq, H, d].
+
+    q [Nq, H, d]; k, v [Nk, Hkv, d] with Hkv dividing H (all may be slices of a projection's rows): the tokens
+    of sequence b are the rows from ``cu_q[b]`` up to ``cu_q[b + 1]`` (int32 [B + 1], on the device, not
+    decreasing), its keys those from ``cu_k[b]`` on (None = ``cu_q``).  Its queries are its last tokens: with nq
+    queries and nk keys, query i sees the keys j <= i + nk - nq, and one that sees none gets zeros.  A prompt run
+    in pieces has its earlier keys in front, as cache_read returns them.  Rows of o outside the sequences are left as
+    they were.  ``scale`` defaults to d ** -0.5.  Few queries over many keys are run as ranges of keys, in
+    ``workspace`` if it is large enough, else in a new one.
+    """
+    return (_native or _load()).attn_prefill(q, k, v, cu_q, cu_k, scale, o, workspace)
+
+
+def cache_page_bytes(d, page):
+    """Bytes of one page of ``page`` tokens of one kv head with d channels in the 4-bit cache: 4.25 bits an element.
+    k_cache and v_cache are uint8 tensors [n_pages, Hkv, cache_page_bytes(d, page)]."""
+    return page * (d // 2 + d // 32)
+
+
+def cache_write(k, v, k_cache, v_cache, pages, cu=None, start=None):
+    """Keys and values of packed tokens into a paged cache of 4 bits an element, in place.
+
+    k, v [N, Hkv, d] (may be slices of a projection's rows); ``k_cache`` / ``v_cache`` uint8 [n_pages, Hkv,
+    cache_page_bytes(d, page)], ``page`` a power of two from 16 on; ``pages`` int32 [B, max_pages]: the page of each
+    ``page`` positions of a sequence.  Sequence b's tokens are the rows from ``cu[b]`` up to ``cu[b + 1]`` (int32
+    [B + 1]; None: one token each, N = B), the first one at position ``start[b]`` (int32 [B], None = 0; negative values
+    count as 0).  32 channels share a power of two, an element is one of 0, .5, 1, 1.5, 2, 3, 4, 6 with a sign.
+    Tokens past the table, or on an entry outside the pool, are not written.  No two tokens of a call may share a
+    place.
+    """
+    return (_native or _load()).cache_write(k, v, k_cache, v_cache, pages, cu, start)
+
+
+def cache_read(k_cache, v_cache, pages, cu, tokens, d, start=None, *, dtype=None, k=None, v=None):
+    """Keys and values of the cache as packed rows, for the attention of a prompt's next piece.  Returns (k, v)
+    [tokens, Hkv, d] in ``dtype`` (None = bfloat16, which holds every value).
+
+    Row i of sequence b (the rows from ``cu[b]`` up to ``cu[b + 1]``; cu None: one token each) is position
+    ``start[b]`` + i - cu[b] (start None = 0).  Positions without a page are zeros; rows outside the sequences are left as
+    they were.
+    """
+    return (_native or _load()).cache_read(k_cache, v_cache, pages, cu, tokens, d, start, dtype, k, v)
+
+
+def attn_step_workspace_bytes(N, m, H, Hkv, d, max_pages, page, dtype=None):
+    """Device workspace bytes of attn_step for this shape on the current device (dtype None = bfloat16)."""
+    _fits(N, m, H, Hkv, d, max_pages, page)
+    return int(_lib.load().kda_attn_step_workspace_bytes(N, m, H, Hkv, d, max_pages, page, _code(dtype)))
+
+
+def attn_step(q, k_cache, v_cache, pages, lens, *, scale=None, o=None, workspace=None):
+    """Attention of the newest token of N sequences over the 4-bit cache, or of their m newest ones (drafted
+    tokens to be verified).  Returns o, shaped like q.
+
+    q [N, H, d] or [N, m, H, d] (may be slices of a projection's rows); caches and ``pages`` as for cache_write,
+    which has written the new tokens too; ``lens`` int32 [N]: the tokens of each sequence in the cache, at most
+    what its table holds.  Query t sees the first lens - m + 1 + t of them; one that sees none gets zeros, and tokens on
+    a table's entry outside the pool are not seen.  ``scale`` defaults to d ** -0.5.
+    """
+    return (_native or _load()).attn_step(q, k_cache, v_cache, pages, lens, scale, o, workspace)

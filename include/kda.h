@@ -450,6 +450,101 @@ kda_status_t kda_window_step(const void *q, const void *k, const void *v, void *
                              float scale, long long q_stride, long long k_stride, long long v_stride,
                              kda_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * ---- A full-attention layer: packed prompts, a paged cache in 4 bits, tokens over it ----
+ *
+ * The conventions of the token mixers hold: strided rows, contiguous outputs, no overlaps, device sizes
+ * clamped, and a value that is a NaN or an infinity reaches no other sequence.
+ */
+
+/*
+ * Causal attention over packed prompts of different lengths, H / Hkv query heads to a kv head:
+ *
+ *     o_i = sum_j softmax_j(scale q_i . k_j) v_j        j <= i + nk - nq
+ *
+ * A sequence's nq queries are the last of its nk tokens (a prompt run in pieces has its earlier keys in front, as
+ * kda_cache_read returns them).  A query that sees no key gets zeros.
+ *
+ *   q          [Nq, H, d]    dtype   row stride q_stride
+ *   k, v       [Nk, Hkv, d]  dtype   row strides k_stride, v_stride; Hkv divides H
+ *   cu_q       [B + 1] int32 DEVICE  sequence b has the rows from cu_q[b] up to cu_q[b + 1] of q (not decreasing;
+ *                                    values outside [0, Nq] are clamped)
+ *   cu_k       [B + 1] int32 DEVICE  the same of k and v, or NULL: cu_q (Nk == Nq)
+ *   o          [Nq, H, d]    dtype  (out)  rows outside the sequences are left as they were
+ *   d          64 or 128;  0 < scale <= 2.3e38 (scale log2(e) is finite)
+ * Rows of q, k and v start on 16-byte boundaries.  Nq == 0, B == 0 or H == 0 is a no-op.  H is at most 65536, Nk and
+ * Nq H / Hkv at most 2^30, (Nq H / Hkv / 64 + B) Hkv at most 2^23.  Few queries over many keys are run as ranges of
+ * keys, joined afterwards, when a workspace of kda_attn_prefill_workspace_bytes(...) bytes is given (calls that overlap in
+ * time need one each); with NULL they run as one range.  Scores have to lie inside fp32's range: one below it has no
+ * weight, a query with none inside it gets zeros, one with a score above it NaN.  A NaN or an infinity in k or v may reach the
+ * queries up to 127 before it as well.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded
+ * to bf16 as the operand of the product with v.
+ */
+size_t kda_attn_prefill_workspace_bytes(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dtype);
+kda_status_t kda_attn_prefill(const void *q, const void *k, const void *v, const int *cu_q, const int *cu_k,
+                              void *o, int B, int Nq, int Nk, int H, int Hkv, int d, float scale,
+                              long long q_stride, long long k_stride, long long v_stride,
+                              kda_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A paged cache of keys and values in 4 bits an element (open microscaling form): 32 channels of a row share a power
+ * of two 2^e, kept as the byte e + 127, and an element is a sign, two bits of exponent and one of fraction: 0, .5, 1,
+ * 1.5, 2, 3, 4, 6.  e is the smallest integer from -125 to 95 with max |x| <= 7 2^e (larger elements, from 7 2^95 on, are
+ * kept as 6 2^95); elements are rounded to the nearest value, ties to the even fraction.  A block that holds a NaN or an infinity has the byte 255 and reads as NaN.  The
+ * bytes 0, 1 and 223 to 254, which are never written, have no meaning.
+ *
+ *   k_cache, v_cache  [n_pages, Hkv, page (d / 2 + d / 32)] bytes   a page of one kv head: `page` rows of d / 2 bytes of
+ *                     elements (even channels in the low halves), then `page` rows of d / 32 exponents
+ *   pages      [B, max_pages] int32 DEVICE  the page of each `page` positions of a sequence.  An entry outside
+ *                                           [0, n_pages) is never followed
+ *   page       a power of two, 16 to 65536; max_pages * page at most 2^30;  d 64 or 128
+ */
+
+/*
+ * Writes the keys and values of N packed tokens.
+ *
+ *   k, v       [N, Hkv, d] dtype         row strides k_stride, v_stride
+ *   cu         [B + 1] int32 DEVICE      rows of sequence b, as cu_q above; NULL: one token each (N == B)
+ *   start      [B] int32 DEVICE or NULL (0)  position of each sequence's first token (negative values count as 0)
+ * Tokens past the table, on an entry outside the pool, or outside the sequences are not written.  No two tokens of a
+ * call may share a place: which of them it then holds is open, byte by byte.  N Hkv is at most 2^27, Hkv at most 65535.
+ */
+kda_status_t kda_cache_write(const void *k, const void *v, void *k_cache, void *v_cache, const int *pages,
+                             const int *cu, const int *start, int B, int N, int Hkv, int d, int n_pages,
+                             int max_pages, int page, long long k_stride, long long v_stride,
+                             kda_dtype_t dtype, void *stream);
+
+/*
+ * Reads N packed rows back: k, v [N, Hkv, d] dtype (out), exact in either type.  The other arguments are as for writing;
+ * a position without a page is zeros, a row outside the sequences is left as it was.
+ */
+kda_status_t kda_cache_read(const void *k_cache, const void *v_cache, const int *pages, const int *cu,
+                            const int *start, void *k, void *v, int B, int N, int Hkv, int d, int n_pages,
+                            int max_pages, int page, kda_dtype_t dtype, void *stream);
+
+/*
+ * Attention of the newest m tokens of N sequences over the cache, which holds them already (m is 1 in decoding, a few
+ * for drafted tokens that are verified):
+ *
+ *   q          [N, m, H, d] dtype        row stride q_stride
+ *   lens       [N] int32 DEVICE          tokens of each sequence in the cache (clamped to [0, max_pages * page]);
+ *                                        query t sees the first lens - m + 1 + t of them, none gives zeros
+ *   o          [N, m, H, d] dtype  (out)
+ *   workspace  kda_attn_step_workspace_bytes(...) bytes of device memory (may be NULL when that is 0), written before
+ *              it is read; calls that overlap in time need one each
+ * Rows whose table entry lies outside the pool are not seen; n_pages is at least 1.  N == 0, m == 0 or H == 0 is a no-op.
+ * N m H is at most 2^25, the tokens that all tables hold, N max_pages page / 128 + N, at most 2^30, and N ceil(m H / Hkv / 16) Hkv at most
+ * about 2^23.  Scores have to lie inside fp32's range, as above.  A NaN in a row that a later one of the m queries sees
+ * reaches the earlier ones too.  Statistics and sums are fp32, every cached value is exact, and a probability enters the
+ * product with v as two bf16 parts (16 bits; three, 24 bits, for fp32 outputs).
+ */
+size_t kda_attn_step_workspace_bytes(int N, int m, int H, int Hkv, int d, int max_pages, int page,
+                                     kda_dtype_t dtype);
+kda_status_t kda_attn_step(const void *q, const void *k_cache, const void *v_cache, const int *pages,
+                           const int *lens, void *o, int N, int m, int H, int Hkv, int d, int n_pages,
+                           int max_pages, int page, float scale, long long q_stride, kda_dtype_t dtype,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
