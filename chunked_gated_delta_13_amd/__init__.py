@@ -15,7 +15,8 @@ Beside KDA, the token mixers of mixers.py, each with a prompt and a one-token fo
     y, state = conv_prefill(x, w, bias, state)             # short causal convolution
     y, S_T   = ssm_prefill(x, dt, A, Bm, Cm, S0, D=D, z=z) # selective state space scan
     o        = window_prefill(q, k, v, window, sinks, k_cache=kc, v_cache=vc)
-    conv_step, ssm_step, window_step                       # state or cache updated in place
+    o, S_T   = delta_prefill(q, k, v, g, beta, S0)         # gated delta rule, one decay per head
+    conv_step, ssm_step, window_step, delta_step           # state or cache updated in place
 
 and a full-attention layer's parts:
 
@@ -31,13 +32,13 @@ import ctypes
 from . import _lib
 from ._lib import KDAError
 from .mixers import (attn_prefill, attn_prefill_workspace_bytes, attn_step, attn_step_workspace_bytes, cache_page_bytes,
-                     cache_read, cache_write, conv_prefill, conv_step, ssm_prefill, ssm_step, ssm_workspace_bytes,
-                     window_prefill, window_prefill_workspace_bytes, window_step, window_step_workspace_bytes)
+                     cache_read, cache_write, conv_prefill, conv_step, delta_prefill, delta_step, delta_workspace_bytes,
+                     ssm_prefill, ssm_step, ssm_workspace_bytes, window_prefill, window_prefill_workspace_bytes, window_step, window_step_workspace_bytes)
 
 __all__ = ["conv_prefill", "conv_step", "ssm_prefill", "ssm_step", "ssm_workspace_bytes",
            "window_prefill", "window_prefill_workspace_bytes", "window_step", "window_step_workspace_bytes",
            "attn_prefill", "attn_prefill_workspace_bytes", "attn_step", "attn_step_workspace_bytes",
-           "cache_page_bytes", "cache_read", "cache_write",
+           "cache_page_bytes", "cache_read", "cache_write", "delta_prefill", "delta_step", "delta_workspace_bytes",
            "chunk_prefill", "chunk_prefill_ckpt", "chunk_prefill_gate", "chunk_prefill_noalloc",
            "decode_step", "spec_verify", "spec_commit", "prefill_plan", "prefill_workspace_bytes",
            "abi_version", "KDAError", "load_library"]

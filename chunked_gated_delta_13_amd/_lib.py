@@ -67,6 +67,10 @@ SIGNATURES = {
     "kda_window_step_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "kda_window_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                              ctypes.c_float, _ll, _ll, _ll, _i, _vp, _sz, _vp]),
+    "kda_delta_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "kda_delta_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                               _ll, _ll, _ll, _i, _i, _vp, _sz, _vp]),
+    "kda_delta_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _ll, _ll, _ll, _i, _vp]),
     "kda_attn_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "kda_attn_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                               ctypes.c_float, _ll, _ll, _ll, _i, _vp, _sz, _vp]),

@@ -46,6 +46,9 @@ struct Library {
     decltype(&kda_cache_read) cache_read;
     decltype(&kda_attn_step_workspace_bytes) attn_step_workspace_bytes;
     decltype(&kda_attn_step) attn_step;
+    decltype(&kda_delta_prefill_workspace_bytes) delta_prefill_workspace_bytes;
+    decltype(&kda_delta_prefill) delta_prefill;
+    decltype(&kda_delta_step) delta_step;
 } lib;
 PyObject* on_status = nullptr;   // called with a status and the name of the call that returned it
 
@@ -602,6 +605,78 @@ PyObject* attn_step(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     END_HANDLE_TH_ERRORS
 }
 
+// Arguments 0 .. 4 (q, k, v, g, beta) of both forms of the gated delta rule.
+struct Delta {
+    const Tensor &q, &k, &v, &g, &beta;
+    int H, Hk, dk, dv;
+    long long qs, ks, vs;
+
+    Delta(const Common& c, const Args& a, int lead)
+        : q(a.tensor(0, "q")), k(a.tensor(1, "k")), v(a.tensor(2, "v")), g(a.tensor(3, "g")), beta(a.tensor(4, "beta")) {
+        if (q.dim() != lead + 2) throw refusal<WrongValue>(lead == 2 ? "q must be [B, T, Hk, dk]" : "q must be [N, Hk, dk]");
+        if (v.dim() != lead + 2) throw refusal<WrongValue>("v must have one axis of heads and one of channels after the tokens");
+        Hk = size(q.size(lead));
+        dk = size(q.size(lead + 1));
+        H = size(v.size(lead));
+        dv = size(v.size(lead + 1));
+        Shape per(q.sizes().begin(), q.sizes().begin() + lead), wide = per;
+        per.push_back(H);
+        wide.push_back(H);
+        wide.push_back(dv);
+        qs = c.rows("q", q, q.sizes(), lead);
+        ks = c.rows("k", k, q.sizes(), lead);
+        vs = c.rows("v", v, wide, lead);
+        c.whole("g", g, at::kFloat, per);
+        c.whole("beta", beta, at::kFloat, per);
+    }
+};
+
+// q, k, v, g, beta, S0, lens, seg_len, o, S_T, return_state, workspace
+PyObject* delta_prefill(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    if (!arity(nargs, 12)) return nullptr;
+    const Args a{args};
+    const Common c("delta_prefill", a.tensor(0, "q"));
+    const Delta x(c, a, 2);
+    const int64_t B = x.q.size(0), T = x.q.size(1);
+    const Tensor *S0 = a.optional(5, "S0"), *lens = a.optional(6, "lens");
+    if (S0) c.whole("S0", *S0, at::kFloat, {B, x.H, x.dk, x.dv});
+    if (lens) c.whole("lens", *lens, at::kInt, {B});
+    const int b = size(B), t = size(T), seg = a.size(7);
+    Pending po(c, a, 8, "o", c.type, {B, T, x.H, x.dv}), ps(c, a, 9, "S_T", at::kFloat, {B, x.H, x.dk, x.dv}, a.truth(10));
+    const Tensor* room = a.optional(11, "workspace");
+    const OnDevice on(c.dev);
+    const Workspace ws(c, room, lib.delta_prefill_workspace_bytes(b, t, x.H, x.Hk, x.dk, x.dv, c.code, seg));
+    const Output &o = po.make(c), &S = ps.make(c);
+    if (!c.call(lib.delta_prefill, ptr(x.q), ptr(x.k), ptr(x.v), at_type<float>(&x.g), at_type<float>(&x.beta), at_type<float>(S0),
+                at_type<int>(lens), o.ptr(), reinterpret_cast<float*>(S.ptr()), b, t, x.H, x.Hk, x.dk, x.dv, x.qs, x.ks, x.vs, c.code,
+                seg, ws.p, ws.bytes))
+        return nullptr;
+    return pair(o, S);
+    END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, g, beta, S, o
+PyObject* delta_step(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    if (!arity(nargs, 7)) return nullptr;
+    const Args a{args};
+    const Common c("delta_step", a.tensor(0, "q"));
+    const Delta x(c, a, 1);
+    const Tensor& S = a.tensor(5, "S");
+    const int64_t N = x.q.size(0);
+    c.whole("S", S, at::kFloat, {N, x.H, x.dk, x.dv});
+    const int n = size(N);
+    Pending po(c, a, 6, "o", c.type, {N, x.H, x.dv});
+    const OnDevice on(c.dev);
+    const Output& o = po.make(c);
+    if (!c.call(lib.delta_step, ptr(x.q), ptr(x.k), ptr(x.v), at_type<float>(&x.g), at_type<float>(&x.beta), at_type<float>(&S), o.ptr(), n,
+                x.H, x.Hk, x.dk, x.dv, x.qs, x.ks, x.vs, c.code))
+        return nullptr;
+    return o.object();
+    END_HANDLE_TH_ERRORS
+}
+
 // addresses of libkda's entry points, in the order of `Library`, and the function that raises for a status
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     constexpr int kEntries = sizeof(Library) / sizeof(void*);
@@ -621,7 +696,7 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 #define KDA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {KDA_METHOD(bind),     KDA_METHOD(conv_prefill),   KDA_METHOD(conv_step),   KDA_METHOD(ssm_prefill),
                          KDA_METHOD(ssm_step), KDA_METHOD(window_prefill), KDA_METHOD(window_step),
-                         KDA_METHOD(attn_prefill), KDA_METHOD(cache_write), KDA_METHOD(cache_read), KDA_METHOD(attn_step), {nullptr, nullptr, 0, nullptr}};
+                         KDA_METHOD(attn_prefill), KDA_METHOD(cache_write), KDA_METHOD(cache_read), KDA_METHOD(attn_step), KDA_METHOD(delta_prefill), KDA_METHOD(delta_step), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mixers", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -131,4 +131,30 @@ struct AttnStepArgs {
 
 hipError_t launch_attn_step(int d, bool f32, const AttnStepArgs& a, hipStream_t s);
 
+struct DeltaArgs {
+    const void* q;            // rows of Hk * dk, stride q_stride elements
+    const void* k;
+    const void* v;            // rows of H * dv
+    const float* g;           // [rows, H] natural log of the decay
+    const float* beta;        // [rows, H]
+    const int* lens;          // [B] (device, clamped to [0, T]) or nullptr
+    void* o;                  // [rows, H, dv]
+    const float* S_in;        // entry states: of (b h, segment) at bh * sin_bh + seg * sin_seg, or nullptr (zeros)
+    float* S_out;             // final states: of segment out_seg only (at bh * sout_bh), or with out_seg -1 of all; the
+                              // token form reads and writes it
+    float* M_out;             // [BH, m_bh, dk, dk] transitions of the segments (states' pass)
+    long long q_stride, k_stride, v_stride;
+    long long sin_bh, sin_seg, sout_bh, sout_seg, m_bh;
+    long long T, seg_len;     // tokens, tokens per segment (whole chunks)
+    int BH, H, Hk, dv;
+    int n_seg_launch, out_seg;
+    int slices, id_slices;    // slices of state columns, of the transition's columns
+    long long n_units, per_xcd;
+};
+
+// One pass over the first n_seg_launch segments: outputs, or (out false) final states from zero and transitions.
+hipError_t launch_delta_prefill(bool out, int dk, bool f32, int nct, const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_join(int dk, int dv, int bh, int n_seg, const float* M, const float* S0, float* S_in, hipStream_t s);
+hipError_t launch_delta_step(int dk, bool f32, const DeltaArgs& a, hipStream_t s);
+
 }  // namespace kda

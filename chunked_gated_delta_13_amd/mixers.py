@@ -1,6 +1,6 @@
 """What stands beside KDA in a hybrid model: short causal convolution, selective state space scan, attention with a
-sliding window and a few first tokens that stay visible, causal attention over packed prompts, and a paged cache of
-4 bits an element with the attention over it.
+sliding window and a few first tokens that stay visible, causal attention over packed prompts, a paged cache of 4 bits
+an element with the attention over it, and the gated delta rule with one decay per head.
 
 Signatures and their documentation; checks and marshalling are in csrc/binding (``_mixers.so``), since a
 token of these operators keeps the device busy for a few microseconds only.  Inputs may be slices of a
@@ -21,7 +21,8 @@ _INT_MAX = 2 ** 31 - 1
 _ENTRIES = ("kda_conv_prefill", "kda_conv_step", "kda_ssm_prefill_workspace_bytes", "kda_ssm_prefill", "kda_ssm_step",
             "kda_window_prefill_workspace_bytes", "kda_window_prefill", "kda_window_step_workspace_bytes", "kda_window_step",
             "kda_attn_prefill_workspace_bytes", "kda_attn_prefill", "kda_cache_write", "kda_cache_read",
-            "kda_attn_step_workspace_bytes", "kda_attn_step")
+            "kda_attn_step_workspace_bytes", "kda_attn_step",
+            "kda_delta_prefill_workspace_bytes", "kda_delta_prefill", "kda_delta_step")
 _native = None
 
 
@@ -204,3 +205,30 @@ def attn_step(q, k_cache, v_cache, pages, lens, *, scale=None, o=None, workspace
     a table's entry outside the pool are not seen.  ``scale`` defaults to d ** -0.5.
     """
     return (_native or _load()).attn_step(q, k_cache, v_cache, pages, lens, scale, o, workspace)
+
+
+def delta_workspace_bytes(B, T, H, Hk, dk, dv, dtype=None, seg_len=0):
+    """Device workspace bytes of delta_prefill for this shape on the current device (dtype None = bfloat16)."""
+    _fits(B, T, H, Hk, dk, dv, seg_len)
+    return int(_lib.load().kda_delta_prefill_workspace_bytes(B, T, H, Hk, dk, dv, _code(dtype), seg_len))
+
+
+def delta_prefill(q, k, v, g, beta, S0=None, *, lens=None, seg_len=0, o=None, S_T=None, return_state=True, workspace=None):
+    """The gated delta rule of a prompt batch, one decay per head and token.  Returns (o, S_T).
+
+        S <- e^g S + beta k (v - e^g S^T k)^T,    o = S^T q
+
+    q, k [B, T, Hk, dk]; v [B, T, H, dv] (all may be slices of a projection's rows), key head h Hk // H serves value head h;
+    g, beta [B, T, H] fp32, g the natural log of the decay (at most 0, not bounded below); S0, S_T [B, H, dk, dv] fp32
+    (S_T may be S0; None when return_state is False).  As in chunk_prefill, q and k are taken as they are (callers
+    normalise and scale them), and beta too.  ``lens`` (int32 [B]) gives the tokens of each sequence of a padded batch; rows of o behind
+    them are left as they were.  ``seg_len`` forces the tokens per segment of the sequence split (a multiple of 64; 0 = the
+    library's choice).
+    """
+    return (_native or _load()).delta_prefill(q, k, v, g, beta, S0, lens, seg_len, o, S_T, return_state, workspace)
+
+
+def delta_step(q, k, v, g, beta, S, *, o=None):
+    """One token of the gated delta rule for N sequences: q, k [N, Hk, dk], v [N, H, dv], g, beta [N, H] fp32; ``S``
+    [N, H, dk, dv] is updated in place.  Returns o [N, H, dv]."""
+    return (_native or _load()).delta_step(q, k, v, g, beta, S, o)

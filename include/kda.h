@@ -451,6 +451,48 @@ kda_status_t kda_window_step(const void *q, const void *k, const void *v, void *
                              kda_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Gated delta rule of a prompt: KDA's update with one decay per head and token, and key heads shared by the H / Hk
+ * value heads of a group:
+ *
+ *     S <- e^(g_t) S
+ *     S <- S + beta_t k_t (v_t - S^T k_t)^T
+ *     o_t = S^T q_t                                  read after the write
+ *
+ *   q, k       [B, T, Hk, dk] dtype   row strides q_stride, k_stride; Hk divides H; taken as they are
+ *   v          [B, T, H, dv]  dtype   row stride v_stride
+ *   g          [B, T, H]      fp32    natural log of the decay; at most 0 (-infinity forgets all; values below -110
+ *                                     count as that)
+ *   beta       [B, T, H]      fp32
+ *   S0         [B, H, dk, dv] fp32 or NULL (zeros)
+ *   o          [B, T, H, dv]  dtype  (out)
+ *   S_T        [B, H, dk, dv] fp32 or NULL  (out)  state after each sequence's last token; may be S0
+ *   dk, dv     64 or 128 each
+ *   seg_len    0: the library splits the sequence where that fills the GPU; else tokens per segment (a multiple of 64;
+ *              >= T = no split).  The result does not depend on it beyond rounding
+ *   workspace  kda_delta_prefill_workspace_bytes(...) bytes of device memory (may be NULL when that is 0), written
+ *              before it is read; calls that overlap in time need one each
+ * Rows of q, k and v start on 16-byte boundaries.  B * H, times the segments of a split, is at most 2^20.  T == 0 is valid: S_T receives
+ * S0 (or zeros).  B == 0 or H == 0 is a no-op.  A NaN or an infinity may reach the other tokens of its block of 64 and
+ * every token after it.  States and exponents are fp32, and with bf16 inputs every factor on the state's path keeps 24
+ * bits; the products that form o take the state and the weights 2^(c_i - c_j) (q_i . k_j) rounded to bf16.
+ */
+size_t kda_delta_prefill_workspace_bytes(int B, int T, int H, int Hk, int dk, int dv, kda_dtype_t dtype,
+                                         int seg_len);
+kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                               const float *S0, const int *lens, void *o, float *S_T, int B, int T, int H,
+                               int Hk, int dk, int dv, long long q_stride, long long k_stride,
+                               long long v_stride, kda_dtype_t dtype, int seg_len, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the gated delta rule for N sequences, S [N, H, dk, dv] updated in place: the same arguments without the
+ * time axis (q, k [N, Hk, dk], v, o [N, H, dv], g, beta [N, H]).
+ */
+kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                            float *S, void *o, int N, int H, int Hk, int dk, int dv, long long q_stride,
+                            long long k_stride, long long v_stride, kda_dtype_t dtype, void *stream);
+
+/*
  * ---- A full-attention layer: packed prompts, a paged cache in 4 bits, tokens over it ----
  *
  * The conventions of the token mixers hold: strided rows, contiguous outputs, no overlaps, device sizes
