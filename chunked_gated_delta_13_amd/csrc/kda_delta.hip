@@ -29,45 +29,56 @@ template <> struct DeltaTraits<float> { static constexpr int C = 32, NP = 1; };
 
 constexpr float kLeastExponent = -160.0f;   // 2^-160 of any state is below fp32's range: the same as nothing
 
-// Straight from memory to LDS, 16 bytes a lane, without the compiler's waits (see barrier_all): it would wait for
-// every such request before the next read of LDS.  `lds` is uniform.
-__device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory");
+// Straight from memory (a uniform base and a lane's offset in bytes) to LDS, 16 bytes a lane, without the compiler's
+// waits (see barrier_all): it would wait for every such request before the next read of LDS.  `lds` is uniform.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void KDA_LDS* p) { return (uint32_t)(size_t)p; }
 
 // An operand kept as the wave holds it: 8 elements a lane, lane after lane.
-template <typename T> __device__ __forceinline__ void frag_get(Frag<T>& f, const KDA_LDS T* p) {
-    typedef typename Vec4<T>::type vec4;
-    frag_join(f, *reinterpret_cast<const KDA_LDS vec4*>(p), *reinterpret_cast<const KDA_LDS vec4*>(p + 4));
+__device__ __forceinline__ void frag_get(Frag<float>& f, const KDA_LDS float* p) {
+    frag_join(f, *reinterpret_cast<const KDA_LDS f32x4_t*>(p), *reinterpret_cast<const KDA_LDS f32x4_t*>(p + 4));
 }
-template <> __device__ __forceinline__ void frag_get(Frag<__bf16>& f, const KDA_LDS __bf16* p) {
+__device__ __forceinline__ void frag_get(Frag<__bf16>& f, const KDA_LDS __bf16* p) {
     f.v = *reinterpret_cast<const KDA_LDS bf16x8_t*>(p);
 }
 
-// Two stacked accumulator tiles as an operand in NP parts, the first one largest.
-template <typename T, int NP> __device__ __forceinline__ void parts_of(Frag<T> (&f)[NP], f32x4_t lo, f32x4_t hi) {
+// Two stacked accumulator tiles as an operand in NP parts, the first one largest.  (bf16: a pair of elements is rounded by
+// one instruction and widened again by one each.)
+template <int NP> __device__ __forceinline__ void parts_of(Frag<__bf16> (&f)[NP], f32x4_t lo, f32x4_t hi) {
+    float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        acc_pair_frag<T>(f[p], lo, hi, true);
-        if (p + 1 < NP) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                lo[j] -= f[p].get(j);
-                hi[j] -= f[p].get(4 + j);
+        for (int j = 0; j < 4; ++j) {
+            const bf16x2_t u = {(__bf16)x[2 * j], (__bf16)x[2 * j + 1]};
+            f[p].v[2 * j] = u[0];
+            f[p].v[2 * j + 1] = u[1];
+            if (p + 1 < NP) {
+                uint32_t w = __builtin_bit_cast(uint32_t, u);
+                asm("" : "+v"(w));   // (else either element is rounded once more on its own)
+                x[2 * j] -= __uint_as_float(w << 16);
+                x[2 * j + 1] -= __uint_as_float(w & 0xffff0000u);
             }
         }
     }
 }
+template <int NP> __device__ __forceinline__ void parts_of(Frag<float> (&f)[NP], f32x4_t lo, f32x4_t hi) {
+    static_assert(NP == 1, "fp32 operands are whole");
+    acc_pair_frag<float>(f[0], lo, hi, true);
+}
 
-// acc + a b for factors in parts: the products above 2^-24, the smallest first.
+// c += a b of two rows of tiles for factors in parts: the products above 2^-24, the smallest first.
 template <typename T, int NP>
-__device__ __forceinline__ f32x4_t mma_parts(const Frag<T> (&a)[NP], const Frag<T> (&b)[NP], f32x4_t c) {
+__device__ __forceinline__ void mma_parts(const Frag<T> (&a)[2][NP], const Frag<T> (&b)[NP], f32x4_t& c0, f32x4_t& c1) {
 #pragma unroll
     for (int s = NP - 1; s >= 0; --s)
 #pragma unroll
-        for (int p = 0; p <= s; ++p) c = mma(a[p], b[s - p], c);
-    return c;
+        for (int p = 0; p <= s; ++p) {
+            c0 = mma(a[0][p], b[s - p], c0);
+            c1 = mma(a[1][p], b[s - p], c1);
+        }
 }
 
 // A 16 x 16 by 16 x 16 product in fp32: slots 4 g + j of either operand.
@@ -88,6 +99,20 @@ __device__ __forceinline__ double lane_f64(double x, int lane) {
     return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
 }
 
+// LDS accesses of one wave run in program order; this keeps the compiler from reordering them.
+__device__ __forceinline__ void wave_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Values of lane I of each quad.
+template <int I> __device__ __forceinline__ f32x4_t quad_lane(const f32x4_t& v) {
+    f32x4_t o;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v[x]), I * 0x55, 0xF, 0xF, true));
+    return o;
+}
+
 template <typename T> __device__ __forceinline__ void store4_t(T* p, const f32x4_t& v) {
     typename Vec4<T>::type o;
 #pragma unroll
@@ -97,22 +122,22 @@ template <typename T> __device__ __forceinline__ void store4_t(T* p, const f32x4
 
 }  // namespace
 
-// Prompt.  A workgroup runs one (sequence, head, segment, slice of 64 NCT state columns) with two roles: four state
-// waves hold the slice (16 NCT columns each, fp32, in the accumulators' layout) and run chunk c; four chunk waves
-// prepare what chunk c + 1 needs and does not depend on the state.  A SIMD hosts one of each.  Three workgroup barriers a
-// chunk:
+// Prompt.  A workgroup runs one (sequence, head, segment, slice of 16 NSW state columns) with two roles: NSW state
+// waves hold the slice (16 columns each, fp32, in the accumulators' layout) and run chunk c; four chunk waves
+// prepare what chunk c + 1 needs and does not depend on the state.  With eight state waves a SIMD hosts two of them and a
+// chunk wave.  Three workgroup barriers a chunk:
 //     interval   state waves, chunk c             chunk waves, chunk n = c + 1
-//     1          X = K S0, Q S0                   A (fp32), B
-//     2          R, U = T R                       inverses of A's diagonal blocks; K and Q of n + 1 requested
-//     3          V of c + 1 requested; O, S       T by blocks, row by row; exponents of n + 1
+//     1          X = K S0, Q S0                   A (fp32) and the inverses of its diagonal blocks
+//     2          R, U = T R                       K and Q of n + 1 requested; the first products of T's other blocks
+//     3          O, S; V of c + 1 requested       T's other blocks, T's parts to LDS; B; exponents of n + 1
 // K has three buffers (chunks c, n and the one in flight), Q, B and the exponents' tables two or three, T and V one: each is
 // overwritten only in an interval after its last reader's.
 //
 // OUT: outputs are formed (else only states).
-template <typename T, int DK, int NCT, bool OUT>
-__global__ __launch_bounds__(512) void kda_delta_prefill_kernel(const DeltaArgs a) {
+template <typename T, int DK, int NSW, bool OUT>
+__global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const DeltaArgs a) {
     constexpr int C = DeltaTraits<T>::C, NP = DeltaTraits<T>::NP, NA = C / 16, NQ = C / 32;   // token tiles, pairs of them
-    constexpr int NT = DK / 16, NKB = DK / 32, DVS = 64 * NCT;
+    constexpr int NT = DK / 16, NKB = DK / 32, DVS = 16 * NSW;
     constexpr int KT = C * DK, VT = C * DVS;                     // elements of a tile
     constexpr int NF = NQ * (NQ + 1);                            // operands of a lower triangle
     constexpr int FR = 64 * 8;                                   // elements of an operand
@@ -121,7 +146,8 @@ __global__ __launch_bounds__(512) void kda_delta_prefill_kernel(const DeltaArgs 
     struct Shared {
         T k[3][KT], q[OUT ? 2 : 1][KT], v[VT];
         T t[NP][NF * FR], b[2][OUT ? NF * FR : 8];
-        float low[NLOW * 256], diag[NA * 256], rows[NA * 256];   // A below the diagonal; its diagonal blocks, then T's by columns; T's by rows
+        float low[NLOW * 256], diag[NA * 256], rows[NA * 256], pair[512];   // A's blocks below the diagonal, transposed; T's on it, as they
+                                                                            // are and transposed; two of T's below it
         float arr[3][ARR];
     };
     static_assert(sizeof(Shared) <= 160 * 1024, "LDS of a compute unit");
@@ -148,57 +174,68 @@ __global__ __launch_bounds__(512) void kda_delta_prefill_kernel(const DeltaArgs 
         len = l < 0 ? 0 : (l > a.T ? a.T : l);
     }
     const long long begin = seg * a.seg_len;
-    long long todo = len - begin;           // tokens of this unit
-    todo = todo < 0 ? 0 : (todo < a.seg_len ? todo : a.seg_len);
-    const int nc = (int)((todo + C - 1) / C);
+    long long todo_ = len - begin;          // tokens of this unit (a segment has fewer than 2^31)
+    todo_ = todo_ < 0 ? 0 : (todo_ < a.seg_len ? todo_ : a.seg_len);
+    const int todo = (int)todo_, nc = (todo + C - 1) / C;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
 
-    // Rows of one tile from memory: step i of `steps` covers 1 KB; rows past the unit's take its last one (finite, and of
-    // no weight: their beta is 0).
-    auto fetch = [&](const T* base, long long stride, int chunk, KDA_LDS T* tile, int i, int nb) {
-        const int group = i / nb, block = i % nb;
-        const int row16 = group * TileStep<T>::ROWS + TileStep<T>::row(lane);
-        const long long at = (long long)chunk * C + row16, row = at < todo ? at : todo - 1;
-        const T* p = base + row * stride + tile_dma_piece<T>(row16, lane) * TileStep<T>::ELEMS + 32 * block;
-        dma16(p, lds_address(tile + block * C * 32 + group * TileStep<T>::ROWS * 32));
+    // Rows of one tile from memory: step i covers 1 KB, rows of a group and a block of 32 columns; nb blocks.  `off` is the
+    // lane's offset in a whole chunk.  Rows past the unit's take its last one (finite, and of no weight: their beta is 0).
+    constexpr int GROUPS = C / TileStep<T>::ROWS, ES = (int)sizeof(T);
+    auto lane_off = [&](long long stride, int group, int last) {
+        int row = group * TileStep<T>::ROWS + TileStep<T>::row(lane);
+        const int piece = tile_dma_piece<T>(row, lane);
+        row = row < last ? row : last;
+        return (uint32_t)row * (uint32_t)(stride * ES) + (uint32_t)(piece * 16);
     };
-    constexpr int GROUPS = C / TileStep<T>::ROWS;
+    auto fetch = [&](const T* base, uint32_t off, KDA_LDS T* tile, int group, int block) {
+        dma16(base + 32 * block, off, lds_address(tile + block * C * 32 + group * TileStep<T>::ROWS * 32));
+    };
     const long long tok0 = (long long)b * a.T + begin;
 
-    if (wave < 4) {
+    if (wave < NSW) {
         // ------------------------------------------------------------------------------------------ state waves
         const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * a.v_stride + (long long)h * a.dv + slice * DVS;
-        constexpr int VSTEPS = GROUPS * (DVS / 32) / 4;
+        constexpr int NB = DVS / 32, VG = NSW / GROUPS;   // blocks of a row; waves that share a group of rows
+        const int v_group = wave / VG;
+        const uint32_t v_off = lane_off(a.v_stride, v_group, C);
         auto fetch_v = [&](int chunk) {
             if (ident) return;
+            const int left = todo - chunk * C;
+            const uint32_t off = left >= C ? v_off : lane_off(a.v_stride, v_group, left - 1);
+            const T* base = vp + (long long)chunk * C * a.v_stride;
 #pragma unroll
-            for (int i = 0; i < VSTEPS; ++i) fetch(vp, a.v_stride, chunk, sh->v, wave * VSTEPS + i, DVS / 32);
+            for (int i = 0; i < NB / VG; ++i) fetch(base, off, sh->v, v_group, (wave % VG) * (NB / VG) + i);
         };
         if (nc > 0) fetch_v(0);
 
-        const int col = slice * DVS + wave * 16 * NCT + r;   // this lane's column of tile 0
+        const int col = slice * DVS + wave * 16 + r;   // this lane's column
         const int width = ident ? DK : a.dv;
-        f32x4_t S[NT][NCT];
-        const float* s_in = ident ? nullptr : (a.S_in ? a.S_in + bh * a.sin_bh + seg * a.sin_seg : nullptr);
+        f32x4_t S[NT];
+        if (!ident && a.S_in) {
+            const float* s_in = a.S_in + bh * a.sin_bh + seg * a.sin_seg + (long long)(4 * g) * width + col;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int c = 0; c < NCT; ++c)
+                for (int j = 0; j < 4; ++j) S[t][j] = s_in[(16 * t + j) * width];
+        } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = 16 * t + 4 * g + j;
-                    S[t][c][j] = s_in ? s_in[(long long)row * width + col + 16 * c] : (ident && row == col + 16 * c ? 1.0f : 0.0f);
-                }
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[t][j] = ident && 16 * t + 4 * g + j == col ? 1.0f : 0.0f;
+        }
         TileRows<T, C, DK> rk, rq;
-        TileCols<T, C> ck, cvt[NCT];
+        TileCols<T, C> ck, cvt;
         rk.set(sh->k[0], lane);
         rq.set(sh->q[0], lane);
         ck.set(sh->k[0], lane);
-#pragma unroll
-        for (int c = 0; c < NCT; ++c) cvt[c].set_tile(sh->v, lane, wave * NCT + c);
+        cvt.set_tile(sh->v, lane, wave);
         const KDA_LDS T* tf = lds_pin(&sh->t[0][0] + lane * 8);
+        const int o_step = a.H * a.dv;   // (at most 2^22)
+        T* op = OUT ? reinterpret_cast<T*>(a.o) + (tok0 * a.H + h) * a.dv + slice * DVS + wave * 16 : nullptr;
+        const uint32_t o_off = (uint32_t)((r * o_step + 4 * g) * ES);
 
         barrier_all();
         if (nc > 0) {
@@ -206,36 +243,41 @@ __global__ __launch_bounds__(512) void kda_delta_prefill_kernel(const DeltaArgs 
             barrier_lds();
             barrier_lds();
         }
-        T* op = OUT ? reinterpret_cast<T*>(a.o) + (tok0 * a.H + h) * a.dv + slice * DVS + wave * 16 * NCT + 4 * g : nullptr;
         for (int n = 0; n < nc; ++n) {
             const int kb3 = n % 3;
             const TileRows<T, C, DK> k_rows = rk.at_delta(kb3 * KT);
             const TileRows<T, C, DK> q_rows = rq.at_delta((OUT ? n & 1 : 0) * KT);
             const KDA_LDS float* arr = &sh->arr[kb3][0];
 
-            // 1: X = K S0 and (transposed) S0^T Q^T, contraction block by contraction block
-            f32x4_t X[NA][NCT], O[NA][NCT];
+            // 1: X = K S0 and (transposed) S0^T Q^T, contraction block by contraction block; the parts of the next
+            // block's state are formed between the products of this one
+            f32x4_t X[NA], O[NA];
 #pragma unroll
-            for (int i = 0; i < NA; ++i)
+            for (int i = 0; i < NA; ++i) X[i] = O[i] = zero4();
+            {
+                Frag<T> kf[2][NA], qf[NA], s[2][NP];
 #pragma unroll
-                for (int c = 0; c < NCT; ++c) X[i][c] = O[i][c] = zero4();
+                for (int i = 0; i < NA; ++i) k_rows.frag(kf[0][i], 0, i, 0);
+                parts_of<NP>(s[0], S[0], S[NKB]);
 #pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) {
-                Frag<T> s[NCT][NP];
+                for (int kb = 0; kb < NKB; ++kb) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (OUT) {
 #pragma unroll
-                for (int c = 0; c < NCT; ++c) parts_of<T, NP>(s[c], S[kb][c], S[kb + NKB][c]);
+                        for (int i = 0; i < NA; ++i) q_rows.frag(qf[i], 0, i, kb);
+                    }
+                    if (kb + 1 < NKB) {
 #pragma unroll
-                for (int i = 0; i < NA; ++i) {
-                    Frag<T> f;
-                    k_rows.frag(f, 0, i, kb);
+                        for (int i = 0; i < NA; ++i) k_rows.frag(kf[(kb + 1) & 1][i], 0, i, kb + 1);
+                        parts_of<NP>(s[(kb + 1) & 1], S[kb + 1], S[kb + 1 + NKB]);
+                    }
 #pragma unroll
                     for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c) X[i][c] = mma(f, s[c][p], X[i][c]);
+                        for (int i = 0; i < NA; ++i) X[i] = mma(kf[kb & 1][i], s[kb & 1][p], X[i]);
                     if constexpr (OUT) {
-                        q_rows.frag(f, 0, i, kb);
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c) O[i][c] = mma(s[c][0], f, O[i][c]);
+                        for (int i = 0; i < NA; ++i) O[i] = mma(s[kb & 1][0], qf[i], O[i]);
                     }
                 }
             }
@@ -243,146 +285,140 @@ __global__ __launch_bounds__(512) void kda_delta_prefill_kernel(const DeltaArgs 
 
             // 2: R = beta (V - 2^c X) in X's place, then U = T R
 #pragma unroll
-            for (int q = 0; q < NQ; ++q)
+            for (int q = 0; q < NQ; ++q) {
+                Frag<T> v;
+                if (!ident) cvt.frag(v, 0, 0, q);
+                else v.zero();
 #pragma unroll
-                for (int c = 0; c < NCT; ++c) {
-                    Frag<T> v;
-                    if (!ident) cvt[c].frag(v, 0, 0, q);
-                    else v.zero();
+                for (int x = 0; x < 2; ++x) {
+                    const int i = q + x * NQ;
+                    const f32x4_t grow = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 2 * C + 16 * i + 4 * g);
+                    const f32x4_t beta = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 4 * C + 16 * i + 4 * g);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int i = q + x * NQ;
-                        const f32x4_t grow = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 2 * C + 16 * i + 4 * g);
-                        const f32x4_t beta = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 4 * C + 16 * i + 4 * g);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) X[i][c][j] = beta[j] * fmaf(-grow[j], X[i][c][j], v.get(4 * x + j));
-                    }
+                    for (int j = 0; j < 4; ++j) X[i][j] = beta[j] * fmaf(-grow[j], X[i][j], v.get(4 * x + j));
                 }
-            f32x4_t U[NA][NCT];
+            }
+            f32x4_t U[NA];
 #pragma unroll
-            for (int i = 0; i < NA; ++i)
-#pragma unroll
-                for (int c = 0; c < NCT; ++c) U[i][c] = zero4();
+            for (int i = 0; i < NA; ++i) U[i] = zero4();
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
-                Frag<T> rr[NCT][NP];
+                Frag<T> rr[NP];
+                parts_of<NP>(rr, X[2 * q], X[2 * q + 1]);
 #pragma unroll
-                for (int c = 0; c < NCT; ++c) parts_of<T, NP>(rr[c], X[2 * q][c], X[2 * q + 1][c]);
+                for (int i = 2 * q; i < NA; i += 2) {
+                    Frag<T> tt[2][NP];
 #pragma unroll
-                for (int i = 2 * q; i < NA; ++i) {
-                    Frag<T> tt[NP];
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) frag_get<T>(tt[p], tf + (p * NF + frag_at(i, q)) * FR);
-#pragma unroll
-                    for (int c = 0; c < NCT; ++c) U[i][c] = mma_parts<T, NP>(tt, rr[c], U[i][c]);
+                        for (int p = 0; p < NP; ++p) frag_get(tt[y][p], tf + (p * NF + frag_at(i + y, q)) * FR);
+                    mma_parts<T, NP>(tt, rr, U[i], U[i + 1]);
                 }
             }
             barrier_lds();
 
             // 3: outputs, then the state
-            if (n + 1 < nc) fetch_v(n + 1);
             if constexpr (OUT) {
                 const KDA_LDS T* bf = lds_pin(&sh->b[n & 1][0] + lane * 8);
+                constexpr int UP = NP > 1 ? 2 : 1;
+                Frag<T> f[NF];
+#pragma unroll
+                for (int i = 0; i < NF; ++i) frag_get(f[i], bf + i * FR);
 #pragma unroll
                 for (int i = 0; i < NA; ++i) {
                     const float grow = arr[2 * C + 16 * i + r];
 #pragma unroll
-                    for (int c = 0; c < NCT; ++c)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) O[i][c][j] *= grow;
+                    for (int j = 0; j < 4; ++j) O[i][j] *= grow;
                 }
-                constexpr int UP = NP > 1 ? 2 : 1;
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
-                    Frag<T> uu[NCT][UP];
+                    Frag<T> uu[UP];
+                    parts_of<UP>(uu, U[2 * q], U[2 * q + 1]);
 #pragma unroll
-                    for (int c = 0; c < NCT; ++c) parts_of<T, UP>(uu[c], U[2 * q][c], U[2 * q + 1][c]);
+                    for (int p = UP - 1; p >= 0; --p)
 #pragma unroll
-                    for (int i = 2 * q; i < NA; ++i) {
-                        Frag<T> f;
-                        frag_get<T>(f, bf + frag_at(i, q) * FR);
-#pragma unroll
-                        for (int p = UP - 1; p >= 0; --p)
-#pragma unroll
-                            for (int c = 0; c < NCT; ++c) O[i][c] = mma(uu[c][p], f, O[i][c]);
-                    }
+                        for (int i = 2 * q; i < NA; ++i) O[i] = mma(uu[p], f[frag_at(i, q)], O[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < NA; ++i) {
-                    const long long at = (long long)n * C + 16 * i + r;
-                    if (at < todo) {
-#pragma unroll
-                        for (int c = 0; c < NCT; ++c) store4_t<T>(op + at * a.H * a.dv + 16 * c, O[i][c]);
-                    }
-                }
+                for (int i = 0; i < NA; ++i)
+                    if (n * C + 16 * i + r < todo) store4_t<T>(at_byte(op + (long long)(n * C + 16 * i) * o_step, pinned_u(o_off)), O[i]);
             }
             const float dec = arr[5 * C];
 #pragma unroll
             for (int i = 0; i < NA; ++i) {
                 const f32x4_t late = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 3 * C + 16 * i + 4 * g);
 #pragma unroll
-                for (int c = 0; c < NCT; ++c)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) U[i][c][j] *= late[j];
+                for (int j = 0; j < 4; ++j) U[i][j] *= late[j];
             }
             const TileCols<T, C> k_cols = ck.at_delta(kb3 * KT);
-            Frag<T> uu[NQ][NCT][NP];
+            Frag<T> uu[NQ][NP];
 #pragma unroll
-            for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                for (int c = 0; c < NCT; ++c) parts_of<T, NP>(uu[q][c], U[q][c], U[q + NQ][c]);
+            for (int q = 0; q < NQ; ++q) parts_of<NP>(uu[q], U[q], U[q + NQ]);
             // (a chunk's sum starts from zero and joins the decayed state with one rounding)
+            Frag<T> kc[2][2][NQ];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x4_t add[NCT];
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-                for (int c = 0; c < NCT; ++c) add[c] = zero4();
+                for (int q = 0; q < NQ; ++q) k_cols.frag(kc[0][y][q], 0, y, q);
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    Frag<T> f;
-                    k_cols.frag(f, 0, t, q);
+            for (int t = 0; t < NT; t += 2) {
+                if (t + 2 < NT) {
 #pragma unroll
-                    for (int p = NP - 1; p >= 0; --p)
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c) add[c] = mma(f, uu[q][c][p], add[c]);
+                        for (int q = 0; q < NQ; ++q) k_cols.frag(kc[(t / 2 + 1) & 1][y][q], 0, t + 2 + y, q);
                 }
+                f32x4_t add[2] = {zero4(), zero4()};
 #pragma unroll
-                for (int c = 0; c < NCT; ++c)
+                for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) S[t][c][j] = fmaf(S[t][c][j], dec, add[c][j]);
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) add[y] = mma(kc[(t / 2) & 1][y][q], uu[q][p], add[y]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[t + y][j] = fmaf(S[t + y][j], dec, add[y][j]);
             }
+            if (n + 1 < nc) fetch_v(n + 1);
             barrier_lds();
         }
         float* s_out = ident ? a.M_out + (bh * a.m_bh + seg) * (long long)(DK * DK)
                              : (a.S_out && (a.out_seg < 0 || a.out_seg == seg) ? a.S_out + bh * a.sout_bh + (a.out_seg < 0 ? seg : 0) * a.sout_seg : nullptr);
         if (s_out) {
+            s_out += (long long)(4 * g) * width + col;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int c = 0; c < NCT; ++c)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s_out[(long long)(16 * t + 4 * g + j) * width + col + 16 * c] = S[t][c][j];
+                for (int j = 0; j < 4; ++j) s_out[(16 * t + j) * width] = S[t][j];
         }
         return;
     }
 
     // ---------------------------------------------------------------------------------------------- chunk waves
-    const int cw = wave - 4;
+    const int cw = wave - NSW;
+    __builtin_amdgcn_s_setprio(3);   // (the state waves wait for these at every barrier otherwise: 5% slower)
     const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * a.k_stride + (long long)hk * DK;
     const T* qp = reinterpret_cast<const T*>(a.q) + tok0 * a.q_stride + (long long)hk * DK;
-    constexpr int KSTEPS = GROUPS * NKB / 4;
+    static_assert(GROUPS == 4, "a chunk wave has a group of rows");
+    const uint32_t k_off = lane_off(a.k_stride, cw, C), q_off = lane_off(a.q_stride, cw, C);
     auto fetch_kq = [&](int chunk) {
+        const int left = todo - chunk * C;
+        const uint32_t ko = left >= C ? k_off : lane_off(a.k_stride, cw, left - 1);
+        const T* base = kp + (long long)chunk * C * a.k_stride;
 #pragma unroll
-        for (int i = 0; i < KSTEPS; ++i) fetch(kp, a.k_stride, chunk, sh->k[chunk % 3], cw * KSTEPS + i, NKB);
+        for (int i = 0; i < NKB; ++i) fetch(base, ko, sh->k[chunk % 3], cw, i);
         if constexpr (OUT) {
+            const uint32_t qo = left >= C ? q_off : lane_off(a.q_stride, cw, left - 1);
+            base = qp + (long long)chunk * C * a.q_stride;
 #pragma unroll
-            for (int i = 0; i < KSTEPS; ++i) fetch(qp, a.q_stride, chunk, sh->q[chunk & 1], cw * KSTEPS + i, NKB);
+            for (int i = 0; i < NKB; ++i) fetch(base, qo, sh->q[chunk & 1], cw, i);
         }
     };
-    // exponents and beta of a chunk's tokens, one a lane (wave 0)
+    // exponents and beta of a chunk's tokens, one a lane (the last wave)
     float g_next = 0.0f, beta_next = 0.0f;
     auto request_arr = [&](int chunk) {
-        const long long at = (long long)chunk * C + lane;
+        const int at = chunk * C + lane;
         const bool there = lane < C && at < todo;
         g_next = there ? a.g[(tok0 + at) * a.H + h] : 0.0f;
         beta_next = there ? a.beta[(tok0 + at) * a.H + h] : 0.0f;
@@ -414,130 +450,198 @@ __global__ __launch_bounds__(512) void kda_delta_prefill_kernel(const DeltaArgs 
 
     if (nc > 0) {
         fetch_kq(0);
-        if (cw == 0) {
+        if (cw == 3) {
             request_arr(0);
             put_arr(0);
         }
         // the halves of operands that lie above the diagonal stay zero
-        for (int i = tid - 256; i < NP * NF * FR; i += 256) (&sh->t[0][0])[i] = (T)0.0f;
+        for (int i = tid - 64 * NSW; i < NP * NF * FR; i += 256) (&sh->t[0][0])[i] = (T)0.0f;
         if constexpr (OUT)
-            for (int i = tid - 256; i < 2 * NF * FR; i += 256) (&sh->b[0][0])[i] = (T)0.0f;
+            for (int i = tid - 64 * NSW; i < 2 * NF * FR; i += 256) (&sh->b[0][0])[i] = (T)0.0f;
     }
     barrier_all();
     for (int n = 0; n < nc; ++n) {
         const bool more = n + 1 < nc;
-        if (cw == 0 && more) request_arr(n + 1);
+        if (cw == 3 && more) request_arr(n + 1);
         const KDA_LDS float* arr = &sh->arr[n % 3][0];
-        // 1: tiles of K K^T (rows by block of rows i, columns by j) and of K Q^T (the transposed ones)
         const TileRows<T, C, DK> k_rows = rk.at_delta((n % 3) * KT);
         const TileRows<T, C, DK> q_rows = rq.at_delta((OUT ? n & 1 : 0) * KT);
-        static_for<0, (NA * (NA + 1) / 2 + 3) / 4>([&](auto step) {
-            const int idx = decltype(step)::value * 4 + cw;
-            int i = 0, j = idx;   // (wave-uniform)
-            while (j > i) j -= ++i;
-            if (i >= NA) return;
-            const KDA_LDS float* ai = arr + 16 * i;
-            const KDA_LDS float* aj = arr + 16 * j;
-            const TileRows<T, C, DK> ki = k_rows.at_delta(16 * 32 * i), kj = k_rows.at_delta(16 * 32 * j), qi = q_rows.at_delta(16 * 32 * i);
-            f32x4_t G = zero4(), P = zero4();
+        // 2^(c_i - c_j) of row r of block i, columns 4 g .. of block j
+        auto decays = [&](int i, int j) {
+            const KDA_LDS float *ai = arr + 16 * i + r, *aj = arr + 16 * j + 4 * g;
+            const f32x4_t hj = *reinterpret_cast<const KDA_LDS f32x4_t*>(aj), lj = *reinterpret_cast<const KDA_LDS f32x4_t*>(aj + C);
+            const float hi = ai[0], lo = ai[C];
+            f32x4_t w;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = fast_exp2((hi - hj[x]) + (lo - lj[x]));
+            return w;
+        };
+        // rows j of K by rows i of `rows`, for one tile
+        auto product = [&](const TileRows<T, C, DK>& rows, int i, int j) {
+            const TileRows<T, C, DK> x = k_rows.at_delta(16 * 32 * j), y = rows.at_delta(16 * 32 * i);
+            Frag<T> fx[NKB], fy[NKB];
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb) {
-                Frag<T> x, y;
-                ki.frag(x, 0, 0, kb);
-                kj.frag(y, 0, 0, kb);
-                G = mma(x, y, G);
-                if constexpr (OUT) {
-                    qi.frag(x, 0, 0, kb);
-                    P = mma(y, x, P);
-                }
+                x.frag(fx[kb], 0, 0, kb);
+                y.frag(fy[kb], 0, 0, kb);
             }
-            {   // rows 4 g .. of block i, column r of block j
-                const f32x4_t hi = *reinterpret_cast<const KDA_LDS f32x4_t*>(ai + 4 * g), lo = *reinterpret_cast<const KDA_LDS f32x4_t*>(ai + C + 4 * g);
-                const f32x4_t beta = *reinterpret_cast<const KDA_LDS f32x4_t*>(ai + 4 * C + 4 * g);
-                const float hj = aj[r], lj = aj[C + r];
+            f32x4_t p = zero4();
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float w = fast_exp2((hi[x] - hj) + (lo[x] - lj));
-                    G[x] = i == j && r >= 4 * g + x ? 0.0f : beta[x] * w * G[x];
-                }
-                KDA_LDS float* to = (i == j ? &sh->diag[i * 256] : &sh->low[(i * (i - 1) / 2 + j) * 256]) + lane * 4;
-                *reinterpret_cast<KDA_LDS f32x4_t*>(to) = G;
-            }
-            if constexpr (OUT) {   // row r of block i, columns 4 g .. of block j
-                const f32x4_t hi = *reinterpret_cast<const KDA_LDS f32x4_t*>(aj + 4 * g), lo = *reinterpret_cast<const KDA_LDS f32x4_t*>(aj + C + 4 * g);
-                const float hj = ai[r], lj = ai[C + r];
-                typename Vec4<T>::type o;
+            for (int kb = 0; kb < NKB; ++kb) p = mma(fx[kb], fy[kb], p);
+            return p;
+        };
+        auto dumped = [&](const KDA_LDS float* p) { return *reinterpret_cast<const KDA_LDS f32x4_t*>(p + lane * 4); };
+        auto dump = [&](KDA_LDS float* p, const f32x4_t& v) { *reinterpret_cast<KDA_LDS f32x4_t*>(p + lane * 4) = v; };
+        auto low = [&](int i, int j) { return &sh->low[(i * (i - 1) / 2 + j) * 256]; };
+        auto below = [&](int i, int j) {   // A_ij, i > j, transposed
+            f32x4_t G = product(k_rows, i, j);
+            const f32x4_t w = decays(i, j);
+            const float beta = arr[4 * C + 16 * i + r];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float w = fast_exp2((hj - hi[x]) + (lj - lo[x]));
-                    o[x] = from_f32<T>(i == j && 4 * g + x > r ? 0.0f : w * P[x]);
-                }
-                *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->b[n & 1][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o;
-            }
-        });
-        barrier_lds();
+            for (int x = 0; x < 4; ++x) G[x] *= beta * w[x];
+            dump(low(i, j), G);
+        };
 
-        // 2: (I + A_ii)^-1 of all diagonal blocks at once, a block per 16 lanes, a column per lane
-        if (more) fetch_kq(n + 1);
-        if (cw == 0) {
-            const int blk = g < NA ? g : 0;
-            const KDA_LDS float* L = &sh->diag[blk * 256];
-            f32x4_t x[4];
+        // 1: A by tiles of K K^T.  Wave i forms the inverse of the diagonal one of row i.
+        f32x4_t Dt = zero4();   // T_ii transposed
+        if (cw < NA) {
+            const f32x4_t G = product(k_rows, cw, cw), up = decays(cw, cw);
+            const float br = arr[4 * C + 16 * cw + r], hj = arr[16 * cw + r], lj = arr[C + 16 * cw + r];
+            const f32x4_t hi = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 16 * cw + 4 * g), lo = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + C + 16 * cw + 4 * g);
+            const f32x4_t beta = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 4 * C + 16 * cw + 4 * g);
+            // L = A_ii and its transpose, both in the accumulators' layout.  (K K^T is symmetric.)
+            f32x4_t L, Lt, D;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i >> 2][i & 3] = i == r ? 1.0f : 0.0f;
-#pragma unroll
-            for (int j = 0; j < 15; ++j) {
-                const float xj = x[j >> 2][j & 3];
-#pragma unroll
-                for (int y = (j + 1) >> 2; y < 4; ++y) {
-                    const f32x4_t l = *reinterpret_cast<const KDA_LDS f32x4_t*>(L + (16 * y + j) * 4);   // rows 4 y .. of column j
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        if (4 * y + z > j) x[y][z] = fmaf(-l[z], xj, x[y][z]);
-                }
+            for (int x = 0; x < 4; ++x) {
+                L[x] = 4 * g + x > r ? G[x] * beta[x] * fast_exp2((hi[x] - hj) + (lo[x] - lj)) : 0.0f;
+                Lt[x] = 4 * g + x < r ? G[x] * br * up[x] : 0.0f;
+                D[x] = Dt[x] = 4 * g + x == r ? 1.0f : 0.0f;
             }
-            if (g < NA) {
+            // The 4 x 4 blocks on its diagonal, whose columns are the lanes of a quad: column r of the inverse by
+            // substitution from above, and its row r (the transpose's column) from the right.
+            const f32x4_t l0 = quad_lane<0>(L), l1 = quad_lane<1>(L), l2 = quad_lane<2>(L);
+            if ((r >> 2) == g) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    *reinterpret_cast<KDA_LDS f32x4_t*>(&sh->diag[g * 256 + (16 * y + r) * 4]) = x[y];   // rows 4 y .. of column r
+                for (int x = 1; x < 4; ++x) D[x] = fmaf(-l0[x], D[0], D[x]);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) sh->rows[g * 256 + (16 * (r >> 2) + 4 * y + z) * 4 + (r & 3)] = x[y][z];
-                }
+                for (int x = 2; x < 4; ++x) D[x] = fmaf(-l1[x], D[1], D[x]);
+                D[3] = fmaf(-l2[3], D[2], D[3]);
+                Dt[2] = fmaf(-l2[3], Dt[3], Dt[2]);
+                Dt[1] = fmaf(-l1[2], Dt[2], fmaf(-l1[3], Dt[3], Dt[1]));
+                Dt[0] = fmaf(-l0[1], Dt[1], fmaf(-l0[2], Dt[2], fmaf(-l0[3], Dt[3], Dt[0])));
             }
+            // Blocks of 8 and of 16 rows from halves: D - D M D, M the part of L between the halves.  An accumulator is
+            // the operand of its own matrix from the right, and of its transpose from the left.
+            KDA_LDS float* turn = &sh->rows[cw * 256];
+#pragma unroll
+            for (int w = 4; w <= 8; w *= 2) {
+                f32x4_t Mt;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = r, col = 4 * g + x;   // of M; Mt holds it transposed
+                    Mt[x] = row / (2 * w) == col / (2 * w) && row / w != col / w ? -Lt[x] : 0.0f;
+                }
+                D = mma16(Dt, mma16(Mt, D, zero4()), D);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) turn[(16 * (r >> 2) + 4 * g + x) * 4 + (r & 3)] = D[x];   // row 4 g + x, column r
+                wave_order();
+                Dt = dumped(turn);
+                wave_order();
+            }
+            dump(&sh->diag[cw * 256], D);
+        }
+        if constexpr (NA == 4) {
+            below(cw < 2 ? 3 : (cw == 2 ? 2 : 1), cw == 2 ? 1 : (cw == 1 ? 2 : 0));   // (3,0) (3,2) (2,1) (1,0)
+            if (cw == 0) below(2, 0);
+            if (cw == 3) below(3, 1);
+        } else {
+            if (cw == 2) below(1, 0);
         }
         barrier_lds();
 
-        // 3: T_ij = -(sum_{j < m <= i} T_im A_mj) T_jj, transposed, from the diagonal outwards; wave i has row i
-        static_for<0, NA>([&](auto row) {
-            constexpr int I = decltype(row)::value;
-            if (cw != I) return;
-            f32x4_t t[I + 1];
-            t[I] = *reinterpret_cast<const KDA_LDS f32x4_t*>(&sh->rows[I * 256 + lane * 4]);
-#pragma unroll
-            for (int j = I - 1; j >= 0; --j) {
-                f32x4_t s = zero4();
-#pragma unroll
-                for (int m = I; m > j; --m) s = mma16(*reinterpret_cast<const KDA_LDS f32x4_t*>(&sh->low[(m * (m - 1) / 2 + j) * 256 + lane * 4]), t[m], s);
-                s = mma16(*reinterpret_cast<const KDA_LDS f32x4_t*>(&sh->diag[j * 256 + lane * 4]), s, zero4());
-#pragma unroll
-                for (int x = 0; x < 4; ++x) t[j][x] = -s[x];
+        // 2: T below the diagonal.  Of a 2 x 2 block matrix that is T_ij = -T_ii A_ij T_jj: first inside the pairs of rows
+        // (0, 1) and (2, 3), then between the pairs (columns 0 and 1, a wave each).
+        if (more) fetch_kq(n + 1);
+        f32x4_t x0 = zero4(), x1 = zero4();
+        auto negated = [](f32x4_t v) { return f32x4_t{-v[0], -v[1], -v[2], -v[3]}; };
+        if (cw == 1 || (NA == 4 && cw == 3)) {
+            const f32x4_t Q = mma16(dumped(low(cw, cw - 1)), dumped(&sh->diag[(cw - 1) * 256]), zero4());
+            x0 = negated(mma16(Q, Dt, zero4()));                           // T_10 or T_32, transposed
+            if constexpr (NA == 4) {
+                if (cw == 1) dump(&sh->pair[0], negated(mma16(Dt, Q, zero4())));   // T_10
+                else dump(&sh->pair[256], x0);
             }
+        } else if (NA == 4) {   // A_2x T_xx, A_3x T_xx for x = cw / 2
+            const f32x4_t D = dumped(&sh->diag[(cw >> 1) * 256]);
+            x0 = mma16(dumped(low(2, cw >> 1)), D, zero4());
+            x1 = mma16(dumped(low(3, cw >> 1)), D, zero4());
+        }
+        barrier_lds();
+
+        // 3: the rest of T, and all of it to the state waves, which have read the last one; B
+        auto put = [&](int i, int j, f32x4_t v) {
 #pragma unroll
-            for (int j = 0; j <= I; ++j) {
-                f32x4_t v = t[j];
+            for (int p = 0; p < NP; ++p) {
+                typename Vec4<T>::type o;
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    typename Vec4<T>::type o;
+                for (int x = 0; x < 4; ++x) {
+                    o[x] = from_f32<T>(v[x]);
+                    v[x] -= to_f32<T>(o[x]);
+                }
+                *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->t[p][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o;
+            }
+        };
+        auto weights = [&](int i, int j) {   // B_ij
+            const f32x4_t P = product(q_rows, i, j), w = decays(i, j);
+            typename Vec4<T>::type o;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        o[x] = from_f32<T>(v[x]);
-                        v[x] -= to_f32<T>(o[x]);
+            for (int x = 0; x < 4; ++x) o[x] = from_f32<T>(i == j && 4 * g + x > r ? 0.0f : w[x] * P[x]);
+            *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->b[n & 1][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o;
+        };
+        if (cw < NA) put(cw, cw, Dt);
+        if (cw == 1 || (NA == 4 && cw == 3)) {
+            put(cw, cw - 1, x0);
+            if constexpr (OUT) {
+                if constexpr (NA == 4) {
+                    if (cw == 1) {
+                        weights(0, 0);
+                        weights(1, 0);
+                        weights(1, 1);
+                        weights(2, 0);
+                    } else {
+                        weights(2, 1);
+                        weights(2, 2);
+                        weights(3, 3);
                     }
-                    *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->t[p][frag_at(I, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o;
+                } else {
+                    weights(1, 0);
                 }
             }
-        });
-        if (cw == 0 && more) put_arr(n + 1);
+            if (cw == 3 && more) put_arr(n + 1);
+        } else if constexpr (NA == 4) {
+            if (cw == 0) {
+                const f32x4_t T10 = dumped(&sh->pair[0]);
+                x0 = mma16(dumped(low(2, 1)), T10, x0);
+                x1 = mma16(dumped(low(3, 1)), T10, x1);
+            }
+            const f32x4_t D2 = dumped(&sh->rows[2 * 256]), D3 = dumped(&sh->rows[3 * 256]), T32 = dumped(&sh->pair[256]);
+            put(2, cw >> 1, negated(mma16(x0, D2, zero4())));
+            put(3, cw >> 1, negated(mma16(x1, D3, mma16(x0, T32, zero4()))));
+            if constexpr (OUT) {
+                if (cw == 0) {
+                    weights(3, 0);
+                } else {
+                    weights(3, 1);
+                    weights(3, 2);
+                }
+            }
+        } else {
+            if constexpr (OUT) {
+                if (cw == 0) weights(0, 0);
+                if (cw == 2) weights(1, 1);
+            }
+            if (cw == 3 && more) put_arr(n + 1);
+        }
         barrier_all();   // (K and Q of n + 1 have arrived)
     }
     if (nc > 0) {
@@ -682,18 +786,18 @@ __global__ __launch_bounds__(4 * DV) void kda_delta_step_kernel(const DeltaArgs 
 
 namespace {
 
-template <typename T, int DK, int NCT, bool OUT> hipError_t run_chunks(DeltaArgs a, hipStream_t s) {
-    a.slices = a.dv / (64 * NCT);
-    a.id_slices = OUT ? 0 : DK / (64 * NCT);
+template <typename T, int DK, int NSW, bool OUT> hipError_t run_chunks(DeltaArgs a, hipStream_t s) {
+    a.slices = a.dv / (16 * NSW);
+    a.id_slices = OUT ? 0 : DK / (16 * NSW);
     a.n_units = (long long)a.BH * a.n_seg_launch * (a.slices + a.id_slices);
     a.per_xcd = (a.n_units + 7) / 8;
     if (a.n_units > (1LL << 22)) return hipErrorInvalidValue;
-    kda_delta_prefill_kernel<T, DK, NCT, OUT><<<dim3((unsigned)(8 * a.per_xcd)), 512, 0, s>>>(a);
+    kda_delta_prefill_kernel<T, DK, NSW, OUT><<<dim3((unsigned)(8 * a.per_xcd)), 64 * NSW + 256, 0, s>>>(a);
     return hipGetLastError();
 }
-template <typename T, int DK> hipError_t prefill_t(bool out, int nct, const DeltaArgs& a, hipStream_t s) {
-    if (out) return nct == 2 ? run_chunks<T, DK, 2, true>(a, s) : run_chunks<T, DK, 1, true>(a, s);
-    return run_chunks<T, DK, 1, false>(a, s);
+template <typename T, int DK> hipError_t prefill_t(bool out, int width, const DeltaArgs& a, hipStream_t s) {
+    if (out) return width == 128 ? run_chunks<T, DK, 8, true>(a, s) : run_chunks<T, DK, 4, true>(a, s);
+    return run_chunks<T, DK, 4, false>(a, s);
 }
 template <int DK, int DV, typename T> hipError_t step_t(DeltaArgs a, hipStream_t s) {
     a.per_xcd = (a.n_units + 7) / 8;
@@ -707,9 +811,9 @@ template <typename T> hipError_t step_of(int dk, const DeltaArgs& a, hipStream_t
 
 }  // namespace
 
-hipError_t launch_delta_prefill(bool out, int dk, bool f32, int nct, const DeltaArgs& a, hipStream_t s) {
-    if (dk == 64) return f32 ? prefill_t<float, 64>(out, nct, a, s) : prefill_t<__bf16, 64>(out, nct, a, s);
-    return f32 ? prefill_t<float, 128>(out, nct, a, s) : prefill_t<__bf16, 128>(out, nct, a, s);
+hipError_t launch_delta_prefill(bool out, int dk, bool f32, int width, const DeltaArgs& a, hipStream_t s) {
+    if (dk == 64) return f32 ? prefill_t<float, 64>(out, width, a, s) : prefill_t<__bf16, 64>(out, width, a, s);
+    return f32 ? prefill_t<float, 128>(out, width, a, s) : prefill_t<__bf16, 128>(out, width, a, s);
 }
 hipError_t launch_delta_join(int dk, int dv, int bh, int n_seg, const float* M, const float* S0, float* S_in, hipStream_t s) {
     const dim3 grid((unsigned)bh, (unsigned)(dv / 16));

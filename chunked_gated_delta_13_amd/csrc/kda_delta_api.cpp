@@ -21,12 +21,12 @@ kda_status_t check_shape(int B, int T, int H, int Hk, int dk, int dv, kda_dtype_
     if (H > 0 && (Hk == 0 || H % Hk != 0)) return KDA_ERR_INVALID_ARGUMENT;
     long long a = 0;
     if (!mul_ok((long long)B * T, (long long)H * dv, &a) || a >= (1LL << 58)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((long long)B * H > kMaxUnits / 4) return KDA_ERR_UNSUPPORTED;
+    if ((long long)B * H > kMaxUnits / 4 || T > (1 << 30)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
-// State columns per workgroup are 64 nct: 128 where the sequences and heads alone fill the compute units, else 64.
-int delta_nct(long long units, int dv) { return dv == 128 && 2 * units > cu_count() ? 2 : 1; }
+// State columns per workgroup: 128 where the sequences and heads alone fill the compute units, else 64.
+int delta_width(long long units, int dv) { return dv == 128 && 2 * units > cu_count() ? 128 : 64; }
 
 // Segments of seg_in tokens, or (seg_in 0) as many as take the least time: with fewer sequences and heads than
 // compute units a split shortens the chain of chunks.  Its first pass runs all segments but the last from zero, and their
@@ -83,6 +83,10 @@ kda_status_t check_ptrs(const Inputs& x, const float* S_in, const void* o, const
     if (!wide_rows_ok(x.q, rows, (long long)Hk * dk, x.q_stride, esz) || !wide_rows_ok(x.k, rows, (long long)Hk * dk, x.k_stride, esz) ||
         !wide_rows_ok(x.v, rows, (long long)H * dv, x.v_stride, esz))
         return KDA_ERR_INVALID_ARGUMENT;
+    // offsets inside a chunk are 32-bit: 64 rows of at most 2^22 elements
+    const long long widest = 1LL << 22;
+    if ((long long)H * dv > widest || (rows > 1 && (x.q_stride > widest || x.k_stride > widest || x.v_stride > widest)))
+        return KDA_ERR_UNSUPPORTED;
     if (!aligned(x.g, 4) || !aligned(x.beta, 4) || !aligned(x.lens, 4) || !aligned(o, 16) || !aligned(S_in, 16) || !aligned(S_out, 16) ||
         !aligned(ws, 16))
         return KDA_ERR_INVALID_ARGUMENT;
@@ -170,7 +174,7 @@ kda_status_t kda_delta_prefill(const void* q, const void* k, const void* v, cons
         p.M_out = M;
         p.m_bh = ns - 1;
         p.n_seg_launch = ns - 1;
-        if (kda::launch_delta_prefill(false, dk, f32, 1, p, s) != hipSuccess) return KDA_ERR_DEVICE;
+        if (kda::launch_delta_prefill(false, dk, f32, 64, p, s) != hipSuccess) return KDA_ERR_DEVICE;
         if (kda::launch_delta_join(dk, dv, B * H, ns, M, S0, entry, s) != hipSuccess) return KDA_ERR_DEVICE;
         a.S_in = entry;
         a.sin_bh = ns * state;
@@ -180,7 +184,7 @@ kda_status_t kda_delta_prefill(const void* q, const void* k, const void* v, cons
     a.sout_bh = state;
     a.out_seg = ns - 1;
     a.n_seg_launch = ns;
-    if (kda::launch_delta_prefill(true, dk, f32, delta_nct((long long)B * H * ns, dv), a, s) != hipSuccess) return KDA_ERR_DEVICE;
+    if (kda::launch_delta_prefill(true, dk, f32, delta_width((long long)B * H * ns, dv), a, s) != hipSuccess) return KDA_ERR_DEVICE;
     return KDA_OK;
 }
 

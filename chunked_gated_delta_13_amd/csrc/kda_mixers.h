@@ -152,8 +152,9 @@ struct DeltaArgs {
     long long n_units, per_xcd;
 };
 
-// One pass over the first n_seg_launch segments: outputs, or (out false) final states from zero and transitions.
-hipError_t launch_delta_prefill(bool out, int dk, bool f32, int nct, const DeltaArgs& a, hipStream_t s);
+// One pass over the first n_seg_launch segments, `width` (64 or 128) state columns a workgroup: outputs, or (out false, 64
+// columns) final states from zero and transitions.
+hipError_t launch_delta_prefill(bool out, int dk, bool f32, int width, const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_join(int dk, int dv, int bh, int n_seg, const float* M, const float* S0, float* S_in, hipStream_t s);
 hipError_t launch_delta_step(int dk, bool f32, const DeltaArgs& a, hipStream_t s);
 
