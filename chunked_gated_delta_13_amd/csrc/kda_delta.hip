@@ -27,6 +27,7 @@ template <typename T> struct DeltaTraits;
 template <> struct DeltaTraits<__bf16> { static constexpr int C = 64, NP = 3; };
 template <> struct DeltaTraits<float> { static constexpr int C = 32, NP = 1; };
 
+constexpr float kDeadExponent = -126.0f;    // a segment's decay that leaves nothing of its entry state
 constexpr float kLeastExponent = -160.0f;   // 2^-160 of any state is below fp32's range: the same as nothing
 
 // Straight from memory (a uniform base and a lane's offset in bytes) to LDS, 16 bytes a lane, without the compiler's
@@ -177,6 +178,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
     long long todo_ = len - begin;          // tokens of this unit (a segment has fewer than 2^31)
     todo_ = todo_ < 0 ? 0 : (todo_ < a.seg_len ? todo_ : a.seg_len);
     const int todo = (int)todo_, nc = (todo + C - 1) / C;
+    int first = 0;                          // chunk to start from
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
@@ -195,6 +197,47 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
     };
     const long long tok0 = (long long)b * a.T + begin;
 
+    if constexpr (!OUT) {
+        // Where the decays from some chunk to the segment's end together leave less than 2^-126 of a state, nothing before
+        // that chunk matters (as long as no token's transition expands: beta |k|^2 at most 2): the state from zero is run from there, and the transition is dead (marked, not formed).  Sums of
+        // 64 chunks at a time from the end backwards, 8 or 16 of them a wave.
+        constexpr int NW = NSW + 4;
+        KDA_LDS float* sums = &sh->low[0];
+        bool dead = false;
+        float total = 0.0f;
+        for (int last = nc; last > 0 && !dead; last -= 64) {
+            for (int i = wave; i < 64; i += NW) {
+                const int c = last - 1 - i, at = c * C + lane;
+                float e = 0.0f;
+                if (c >= 0 && lane < C && at < todo) e = a.g[(tok0 + at) * a.H + h] * kLog2e;
+                if (e < kLeastExponent) e = kLeastExponent;   // (a NaN stays one, and kills nothing)
+#pragma unroll
+                for (int x = 1; x < 64; x <<= 1) e += __shfl_xor(e, x);
+                if (lane == 0) sums[i] = e;
+            }
+            barrier_lds();
+            float e = sums[lane];
+#pragma unroll
+            for (int x = 1; x < 64; x <<= 1) {
+                const float y = __shfl_up(e, x);
+                if (lane >= x) e += y;
+            }
+            e += total;
+            const unsigned long long past = __ballot(e <= kDeadExponent);
+            if (past) {
+                dead = true;
+                first = last - 1 - __builtin_ctzll(past);
+            }
+            total = __shfl(e, 63);
+            barrier_lds();
+        }
+        if (ident) {
+            if (slice == 0 && tid == 0) a.dead[bh * a.m_bh + seg] = dead ? 1 : 0;
+            if (dead) return;
+            first = 0;
+        }
+    }
+
     if (wave < NSW) {
         // ------------------------------------------------------------------------------------------ state waves
         const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * a.v_stride + (long long)h * a.dv + slice * DVS;
@@ -209,7 +252,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
 #pragma unroll
             for (int i = 0; i < NB / VG; ++i) fetch(base, off, sh->v, v_group, (wave % VG) * (NB / VG) + i);
         };
-        if (nc > 0) fetch_v(0);
+        if (nc > 0) fetch_v(first);
 
         const int col = slice * DVS + wave * 16 + r;   // this lane's column
         const int width = ident ? DK : a.dv;
@@ -243,7 +286,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             barrier_lds();
             barrier_lds();
         }
-        for (int n = 0; n < nc; ++n) {
+        for (int n = first; n < nc; ++n) {
             const int kb3 = n % 3;
             const TileRows<T, C, DK> k_rows = rk.at_delta(kb3 * KT);
             const TileRows<T, C, DK> q_rows = rq.at_delta((OUT ? n & 1 : 0) * KT);
@@ -449,10 +492,10 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
     rq.set(sh->q[0], lane);
 
     if (nc > 0) {
-        fetch_kq(0);
+        fetch_kq(first);
         if (cw == 3) {
-            request_arr(0);
-            put_arr(0);
+            request_arr(first);
+            put_arr(first);
         }
         // the halves of operands that lie above the diagonal stay zero
         for (int i = tid - 64 * NSW; i < NP * NF * FR; i += 256) (&sh->t[0][0])[i] = (T)0.0f;
@@ -460,7 +503,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             for (int i = tid - 64 * NSW; i < 2 * NF * FR; i += 256) (&sh->b[0][0])[i] = (T)0.0f;
     }
     barrier_all();
-    for (int n = 0; n < nc; ++n) {
+    for (int n = first; n < nc; ++n) {
         const bool more = n + 1 < nc;
         if (cw == 3 && more) request_arr(n + 1);
         const KDA_LDS float* arr = &sh->arr[n % 3][0];
@@ -652,47 +695,64 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
 }
 
 // Entry states of a split's segments: S_in(s + 1) = M_s S_in(s) + H_s in fp32.  H lies in the place of S_in(s + 1); M_s
-// is dk x dk.  A workgroup owns 16 columns of one (sequence, head), in LDS; a thread sums a row's part of them.
+// is dk x dk, and a dead one leaves nothing to do.  A workgroup owns 16 columns of one (sequence, head), a wave one tile of
+// rows, which it forms from the tiles of the state in LDS (as the accumulators hold them, which is how an operand does); what
+// the next step reads is requested a step ahead.
 template <int DK>
-__global__ __launch_bounds__(256) void kda_delta_join_kernel(const float* M, const float* S0, float* S_in, int n_seg, int dv) {
-    constexpr int TPR = 256 / DK, CPT = 16 / TPR;   // threads of a row, columns of a thread
+__global__ __launch_bounds__(4 * DK) void kda_delta_join_kernel(const float* M, const int* dead, const float* S0, float* S_in, int n_seg, int dv) {
+    constexpr int NT = DK / 16;   // row tiles, a wave each
     const long long bh = blockIdx.x;
-    const int row = threadIdx.x / TPR, c0 = (threadIdx.x % TPR) * CPT, col = blockIdx.y * 16 + c0;
-    __shared__ __attribute__((aligned(16))) float cur[DK][16];
-    float* at = S_in + bh * n_seg * (long long)(DK * dv) + (long long)row * dv + col;
-    const float* m = M + bh * (n_seg - 1) * (long long)(DK * DK) + (long long)row * DK;
-    f32x4_t s[CPT / 4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, r = lane & 15;
+    __shared__ __attribute__((aligned(16))) float cur[2][NT * 256];
+    float* at = S_in + bh * n_seg * (long long)(DK * dv) + (long long)(16 * wave + 4 * g) * dv + blockIdx.y * 16 + r;
+    const float* s0 = S0 ? S0 + bh * (long long)(DK * dv) + (at - (S_in + bh * n_seg * (long long)(DK * dv))) : nullptr;
+    const float* m = M + (bh * (n_seg - 1) * DK + 16 * wave + r) * (long long)DK + 4 * g;
+    dead += bh * (n_seg - 1);
+    const long long step = (long long)DK * dv;
+    f32x4_t s, next[2] = {zero4(), zero4()}, w[2][NT];
+    auto request = [&](int seg, bool alive, f32x4_t& n, f32x4_t (&t)[NT]) {   // the step after segment `seg`: its H, its transition
 #pragma unroll
-    for (int x = 0; x < CPT / 4; ++x)
-        s[x] = S0 ? *reinterpret_cast<const f32x4_t*>(S0 + (bh * DK + row) * dv + col + 4 * x) : zero4();
-    for (int seg = 0; seg < n_seg; ++seg) {
+        for (int j = 0; j < 4; ++j) n[j] = at[(seg + 1) * step + j * dv];
+        if (alive) {
 #pragma unroll
-        for (int x = 0; x < CPT / 4; ++x) {
-            if (seg == 0) *reinterpret_cast<f32x4_t*>(at + 4 * x) = s[x];
-            *reinterpret_cast<f32x4_t*>(&cur[row][c0 + 4 * x]) = s[x];
+            for (int k = 0; k < NT; ++k) t[k] = *reinterpret_cast<const f32x4_t*>(m + (long long)seg * (DK * DK) + 16 * k);
         }
-        __syncthreads();
-        if (seg + 1 < n_seg) {
-            at += (long long)DK * dv;
+    };
 #pragma unroll
-            for (int x = 0; x < CPT / 4; ++x) s[x] = *reinterpret_cast<const f32x4_t*>(at + 4 * x);
-#pragma unroll 4
-            for (int k = 0; k < DK; k += 4) {
-                const f32x4_t w = *reinterpret_cast<const f32x4_t*>(m + k);
+    for (int j = 0; j < 4; ++j) {
+        s[j] = s0 ? s0[j * dv] : 0.0f;
+        at[j * dv] = s[j];
+    }
+    int turn = 0;
+    for (int from = 0; from + 1 < n_seg; from += 64) {   // 64 segments' marks at a time
+        const int end = from + 64 < n_seg - 1 ? from + 64 : n_seg - 1;
+        const unsigned long long live = __ballot(from + lane < end && dead[from + lane < end ? from + lane : from] == 0);
+        request(from, live & 1, next[0], w[0]);
+        for (int seg0 = from; seg0 < end; seg0 += 2)
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
+            for (int y = 0; y < 2; ++y) {
+                const int seg = seg0 + y;
+                if (seg >= end) break;
+                const bool alive = live >> (seg - from) & 1;   // (uniform over the workgroup)
+                if (seg + 1 < end) request(seg + 1, live >> (seg + 1 - from) & 1, next[y ^ 1], w[y ^ 1]);
+                if (alive) {
+                    // (two buffers in turn: a wave reaches the barrier before it overwrites one with its last reads of it done)
+                    KDA_LDS float* c = (KDA_LDS float*)cur[turn];
+                    turn ^= 1;
+                    *reinterpret_cast<KDA_LDS f32x4_t*>(c + wave * 256 + lane * 4) = s;
+                    barrier_lds();
+                    f32x4_t p[2] = {zero4(), zero4()};
 #pragma unroll
-                    for (int x = 0; x < CPT / 4; ++x) {
-                        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&cur[k + y][c0 + 4 * x]);
+                    for (int k = 0; k < NT; ++k) p[k & 1] = mma16(w[y][k], *reinterpret_cast<const KDA_LDS f32x4_t*>(c + k * 256 + lane * 4), p[k & 1]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) s[x][j] = fmaf(w[y], v[j], s[x][j]);
+                    for (int j = 0; j < 4; ++j) {
+                        s[j] = next[y][j] + (p[0][j] + p[1][j]);
+                        at[(seg + 1) * step + j * dv] = s[j];
                     }
+                } else {
+                    s = next[y];
+                }
             }
-#pragma unroll
-            for (int x = 0; x < CPT / 4; ++x) *reinterpret_cast<f32x4_t*>(at + 4 * x) = s[x];
-            m += DK * DK;
-        }
-        __syncthreads();
     }
 }
 
@@ -797,6 +857,8 @@ template <typename T, int DK, int NSW, bool OUT> hipError_t run_chunks(DeltaArgs
 }
 template <typename T, int DK> hipError_t prefill_t(bool out, int width, const DeltaArgs& a, hipStream_t s) {
     if (out) return width == 128 ? run_chunks<T, DK, 8, true>(a, s) : run_chunks<T, DK, 4, true>(a, s);
+    if constexpr (DK == 128)
+        if (width == 128) return run_chunks<T, DK, 8, false>(a, s);
     return run_chunks<T, DK, 4, false>(a, s);
 }
 template <int DK, int DV, typename T> hipError_t step_t(DeltaArgs a, hipStream_t s) {
@@ -815,10 +877,10 @@ hipError_t launch_delta_prefill(bool out, int dk, bool f32, int width, const Del
     if (dk == 64) return f32 ? prefill_t<float, 64>(out, width, a, s) : prefill_t<__bf16, 64>(out, width, a, s);
     return f32 ? prefill_t<float, 128>(out, width, a, s) : prefill_t<__bf16, 128>(out, width, a, s);
 }
-hipError_t launch_delta_join(int dk, int dv, int bh, int n_seg, const float* M, const float* S0, float* S_in, hipStream_t s) {
+hipError_t launch_delta_join(int dk, int dv, int bh, int n_seg, const float* M, const int* dead, const float* S0, float* S_in, hipStream_t s) {
     const dim3 grid((unsigned)bh, (unsigned)(dv / 16));
-    if (dk == 64) kda_delta_join_kernel<64><<<grid, 256, 0, s>>>(M, S0, S_in, n_seg, dv);
-    else kda_delta_join_kernel<128><<<grid, 256, 0, s>>>(M, S0, S_in, n_seg, dv);
+    if (dk == 64) kda_delta_join_kernel<64><<<grid, 256, 0, s>>>(M, dead, S0, S_in, n_seg, dv);
+    else kda_delta_join_kernel<128><<<grid, 512, 0, s>>>(M, dead, S0, S_in, n_seg, dv);
     return hipGetLastError();
 }
 hipError_t launch_delta_step(int dk, bool f32, const DeltaArgs& a, hipStream_t s) {

@@ -28,23 +28,39 @@ kda_status_t check_shape(int B, int T, int H, int Hk, int dk, int dv, kda_dtype_
 // State columns per workgroup: 128 where the sequences and heads alone fill the compute units, else 64.
 int delta_width(long long units, int dv) { return dv == 128 && 2 * units > cu_count() ? 128 : 64; }
 
+// The split's first pass takes 128 columns too where both the state's and the transition's allow it.
+int first_width(long long units, int dk, int dv) { return dk == 128 && dv == 128 && 4 * units > cu_count() ? 128 : 64; }
+
+// Microseconds of a chunk: outputs and states of bf16, by columns of a workgroup.
+double chunk_us(int dk, int width, kda_dtype_t dt, bool out) {
+    const double us = (width == 128 ? 6.2 : 5.0) * (out ? 1.0 : 0.84) * (dk == 128 ? 1.0 : 0.8);
+    return dt == KDA_F32 ? 2.2 * us : us;
+}
+
 // Segments of seg_in tokens, or (seg_in 0) as many as take the least time: with fewer sequences and heads than
 // compute units a split shortens the chain of chunks.  Its first pass runs all segments but the last from zero, and their
-// transitions (dk columns more), the second all of them with outputs; a chunk of the first takes 0.7 of one of the second.
+// transitions (dk columns more), the second all of them with outputs.  (Where decays leave nothing of a state over a
+// segment, the first pass runs its end alone; the plan, which does not know them, counts whole segments.)
 kda_status_t delta_plan(int B, int T, int H, int dk, int dv, kda_dtype_t dt, int seg_in, long long* seg_len, int* n_seg) {
     if (seg_in < 0 || seg_in % kSegment != 0) return KDA_ERR_INVALID_ARGUMENT;
     const long long chunks = ((long long)T + kSegment - 1) / kSegment, units = (long long)B * H;
     long long per = seg_in > 0 ? seg_in / kSegment : chunks;
     if (seg_in == 0 && units > 0) {
         const long long cus = cu_count();
-        const int slices = dv / 64, all = slices + dk / 64;
-        const double chunk = dt == KDA_F32 ? 8.0 : 2.5;
-        double best = (double)chunks * chunk * ((double)((units * slices + cus - 1) / cus));
+        const auto rounds = [&](long long n) { return (double)((n + cus - 1) / cus); };
+        const auto second = [&](long long ns) {
+            const int w = delta_width(units * ns, dv);
+            return rounds(units * ns * (dv / w)) * chunk_us(dk, w, dt, true);
+        };
+        const auto first = [&](long long ns) {
+            const int w = first_width(units * (ns - 1), dk, dv);
+            return rounds(units * (ns - 1) * ((dv + dk) / w)) * chunk_us(dk, w, dt, false);
+        };
+        double best = (double)chunks * second(1);
         if (2 * units <= cus) {
             for (long long ns = 2; ns <= cus / units && ns <= chunks; ++ns) {
                 const long long c = (chunks + ns - 1) / ns;
-                const double first = (double)((units * (ns - 1) * all + cus - 1) / cus), second = (double)((units * ns * slices + cus - 1) / cus);
-                const double us = (double)c * chunk * (0.7 * first + second) + 2.0 * (double)ns + 12.0;
+                const double us = (double)c * (first(ns) + second(ns)) + 1.5 * (double)ns + 12.0;
                 if (us < best) {
                     best = us;
                     per = c;
@@ -60,10 +76,12 @@ kda_status_t delta_plan(int B, int T, int H, int dk, int dv, kda_dtype_t dt, int
     return KDA_OK;
 }
 
-// Workspace of a split, fp32: the segments' entry states [B * H, n_seg, dk, dv], their transitions [B * H, n_seg - 1, dk, dk].
+// Workspace of a split: the segments' entry states [B * H, n_seg, dk, dv] and transitions [B * H, n_seg - 1, dk, dk], fp32, and
+// which of the latter are dead, int32 [B * H, n_seg - 1], padded to 16 bytes.
 size_t delta_workspace(int B, int H, int dk, int dv, int ns) {
     if (ns <= 1) return 0;
-    return (size_t)B * H * sizeof(float) * ((size_t)ns * dk * dv + (size_t)(ns - 1) * dk * dk);
+    const size_t bh = (size_t)B * H;
+    return bh * sizeof(float) * ((size_t)ns * dk * dv + (size_t)(ns - 1) * dk * dk) + (bh * (ns - 1) * sizeof(int) + 15) / 16 * 16;
 }
 
 struct Inputs {
@@ -172,10 +190,11 @@ kda_status_t kda_delta_prefill(const void* q, const void* k, const void* v, cons
         p.sout_seg = state;
         p.out_seg = -1;
         p.M_out = M;
+        p.dead = reinterpret_cast<int*>(M + (size_t)B * H * (ns - 1) * dk * dk);
         p.m_bh = ns - 1;
         p.n_seg_launch = ns - 1;
-        if (kda::launch_delta_prefill(false, dk, f32, 64, p, s) != hipSuccess) return KDA_ERR_DEVICE;
-        if (kda::launch_delta_join(dk, dv, B * H, ns, M, S0, entry, s) != hipSuccess) return KDA_ERR_DEVICE;
+        if (kda::launch_delta_prefill(false, dk, f32, first_width((long long)B * H * (ns - 1), dk, dv), p, s) != hipSuccess) return KDA_ERR_DEVICE;
+        if (kda::launch_delta_join(dk, dv, B * H, ns, M, p.dead, S0, entry, s) != hipSuccess) return KDA_ERR_DEVICE;
         a.S_in = entry;
         a.sin_bh = ns * state;
         a.sin_seg = state;

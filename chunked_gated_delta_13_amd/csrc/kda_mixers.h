@@ -143,6 +143,7 @@ struct DeltaArgs {
     float* S_out;             // final states: of segment out_seg only (at bh * sout_bh), or with out_seg -1 of all; the
                               // token form reads and writes it
     float* M_out;             // [BH, m_bh, dk, dk] transitions of the segments (states' pass)
+    int* dead;                // [BH, m_bh] 1: nothing is left of a state over the segment, whose transition is not formed
     long long q_stride, k_stride, v_stride;
     long long sin_bh, sin_seg, sout_bh, sout_seg, m_bh;
     long long T, seg_len;     // tokens, tokens per segment (whole chunks)
@@ -152,10 +153,10 @@ struct DeltaArgs {
     long long n_units, per_xcd;
 };
 
-// One pass over the first n_seg_launch segments, `width` (64 or 128) state columns a workgroup: outputs, or (out false, 64
-// columns) final states from zero and transitions.
+// One pass over the first n_seg_launch segments, `width` (64 or 128) state columns a workgroup: outputs, or (out false; 128
+// columns with dk = dv = 128 only) final states from zero and transitions.
 hipError_t launch_delta_prefill(bool out, int dk, bool f32, int width, const DeltaArgs& a, hipStream_t s);
-hipError_t launch_delta_join(int dk, int dv, int bh, int n_seg, const float* M, const float* S0, float* S_in, hipStream_t s);
+hipError_t launch_delta_join(int dk, int dv, int bh, int n_seg, const float* M, const int* dead, const float* S0, float* S_in, hipStream_t s);
 hipError_t launch_delta_step(int dk, bool f32, const DeltaArgs& a, hipStream_t s);
 
 }  // namespace kda

@@ -135,6 +135,23 @@ def test_delta_prefill_matches_definition(case):
         assert bool((o[b, n:] == 9.0).all())
 
 
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("f32", 64, 128), ("bf16", 64, 64)])
+def test_delta_prefill_split_with_dead_and_living_segments(dtype, dk, dv):
+    """Segments over which decays leave nothing of a state (their transitions are not formed, and their own states are run
+    from where it matters), others that keep it, in any order, and more of them than a wave has lanes."""
+    kda = _kda()
+    B, T, H, Hk, seg = 2, 70 * 64 + 5, 2, 1, 64
+    rows, g, beta, S0 = _inputs(8, dtype, B, T, H, Hk, dk, dv)
+    g = g * 0.1                                              # about 2^-1 a segment
+    for b, h, s in ((0, 0, 3), (0, 0, 4), (0, 0, 6), (0, 1, 0), (1, 0, 68), (1, 1, 1), (1, 1, 3), (1, 1, 5)):
+        g[b, s * seg + 20:s * seg + 40, h] = -6.0            # 2^-173
+    g[1, 64 * 64:64 * 64 + 64, 1] = -1.4                     # 2^-129 over a whole segment
+    dr = rows.cuda()
+    o, S_T = kda.delta_prefill(*_split(dr, H, Hk, dk, dv), g.cuda(), beta.cuda(), S0.cuda(), seg_len=seg)
+    torch.cuda.synchronize()
+    _check(o, S_T, *_split(rows, H, Hk, dk, dv), g, beta, S0, None, dtype)
+
+
 @pytest.mark.parametrize("dtype,seg", [("bf16", 0), ("bf16", 64), ("f32", 0)])
 def test_delta_prefill_of_near_parallel_keys(dtype, seg):
     """Keys in groups of near-parallel vectors, beta up to 1 and hardly any decay: A's entries lie near beta, the inverse

@@ -195,7 +195,7 @@ def test_delta_noops_and_sizes(lib):
     assert _dstep(lib, N=0, q=None, k=None, v=None, g=None, b=None, S=None, o=None) == OK
     assert _dstep(lib, H=0, Hk=0, q=None, k=None, v=None, g=None, b=None, S=None, o=None) == OK
     size = lib.kda_delta_prefill_workspace_bytes
-    assert size(2, 300, 4, 2, 64, 128, BF16, 64) == 8 * 4 * (5 * 64 * 128 + 4 * 64 * 64)
+    assert size(2, 300, 4, 2, 64, 128, BF16, 64) == 8 * 4 * (5 * 64 * 128 + 4 * 64 * 64) + 8 * 4 * 4
     assert size(2, 300, 4, 2, 64, 128, BF16, 320) == 0 and size(2, 300, 4, 3, 64, 128, BF16, 64) == 0
 
 
