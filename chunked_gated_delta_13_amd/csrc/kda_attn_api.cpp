@@ -13,6 +13,7 @@ using namespace kda::host;
 
 namespace {
 
+constexpr size_t kStreamedBytes = (size_t)192 << 20;   // results that do not stay in the 256 MB last-level cache
 constexpr long long kMaxRows = 1LL << 30;   // rows and keys that 32 bits count, with room for a tile more
 
 kda_status_t check_heads(int H, int Hkv, int d, kda_dtype_t dt) {
@@ -130,7 +131,7 @@ kda_status_t check_step_shape(int N, int m, int H, int Hkv, int d, int n_pages, 
     if (st != KDA_OK || H == 0 || N == 0 || m == 0) return st;
     const long long tiles = ((long long)max_pages * page + 127) / 128;
     long long rows = 0;
-    if (!mul_ok((long long)N * m, H, &rows) || rows > 8 * kMaxUnits) return KDA_ERR_UNSUPPORTED;   // the join's workgroups of 64
+    if (!mul_ok((long long)N * m, H, &rows) || rows > 2 * kMaxUnits) return KDA_ERR_UNSUPPORTED;   // the join's workgroups of 256
     if ((long long)N * (tiles + 1) > kMaxRows) return KDA_ERR_UNSUPPORTED;
     int want = 0, slots = 0;
     step_plan(N, m, H, Hkv, max_pages, page, &want, &slots);
@@ -246,6 +247,7 @@ kda_status_t kda_cache_read(const void* k_cache, const void* v_cache, const int*
     a.v_cache = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(v_cache));
     a.k_out = k;
     a.v_out = v;
+    a.streamed = 2 * out > kStreamedBytes ? 1 : 0;
     (void)hipGetLastError();
     if (kda::launch_cache_rows(false, d, dt == KDA_F32, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess) return KDA_ERR_DEVICE;
     return KDA_OK;

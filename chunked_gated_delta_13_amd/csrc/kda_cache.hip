@@ -46,10 +46,21 @@ __device__ __forceinline__ void load8(float (&x)[8], const float* p) {
         x[4 + i] = b[i];
     }
 }
-__device__ __forceinline__ void store8(__bf16* p, const bf16x8_t& v) { *reinterpret_cast<bf16x8_t*>(p) = v; }
-__device__ __forceinline__ void store8(float* p, const bf16x8_t& v) {
-    *reinterpret_cast<f32x4_t*>(p) = f32x4_t{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
-    *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{(float)v[4], (float)v[5], (float)v[6], (float)v[7]};
+template <bool STREAMED> __device__ __forceinline__ void store8(__bf16* p, const bf16x8_t& v) {
+    bf16x8_t* to = reinterpret_cast<bf16x8_t*>(p);
+    if constexpr (STREAMED) __builtin_nontemporal_store(v, to);
+    else *to = v;
+}
+template <bool STREAMED> __device__ __forceinline__ void store8(float* p, const bf16x8_t& v) {
+    f32x4_t* to = reinterpret_cast<f32x4_t*>(p);
+    const f32x4_t lo = {(float)v[0], (float)v[1], (float)v[2], (float)v[3]}, hi = {(float)v[4], (float)v[5], (float)v[6], (float)v[7]};
+    if constexpr (STREAMED) {
+        __builtin_nontemporal_store(lo, to);
+        __builtin_nontemporal_store(hi, to + 1);
+    } else {
+        to[0] = lo;
+        to[1] = hi;
+    }
 }
 
 // Largest of the four lanes of a quad.
@@ -128,12 +139,19 @@ __device__ __forceinline__ int ended_before(const CacheArgs& a, int i, int lane)
 
 // Writing and reading back, bound by HBM.  A thread owns eight channels of a token's key and value: 16 bytes of
 // them in bf16, one dword of elements.  A workgroup takes 16 (d = 128) or 32 tokens of one kv head, whose elements
-// lie beside each other in a page.  grid: (tokens, kv heads)
-template <int D, typename T, bool WRITE>
+// lie beside each other in a page; the heads of the same tokens follow on the same XCD, so that whole rows of the packed
+// tensors are read or written at about the same time.
+//
+// STREAMED: rows that are read back past the last-level cache, for results that it does not hold anyway.  65536 tokens
+// of 8 heads of 128 in bf16 (256 MiB of results) 89 us with plain stores and 54 us streamed; 4096 tokens (16 MiB) 6.3
+// and 5.7 us, but attention of 16 queries that reads them next then takes 37.5 us instead of 32.6.
+template <int D, typename T, bool WRITE, bool STREAMED>
 __global__ __launch_bounds__(256) void kda_cache_rows_kernel(const CacheArgs a) {
     constexpr int LPR = D / 8, TB = 256 / LPR;
-    const int lane = threadIdx.x & 63, c = threadIdx.x % LPR, hk = blockIdx.y;
-    const int i0 = blockIdx.x * TB, i = i0 + threadIdx.x / LPR;
+    const uint32_t unit = (blockIdx.x & 7) * (uint32_t)a.per_xcd + (blockIdx.x >> 3);
+    if (unit >= (uint32_t)a.n_units) return;
+    const int lane = threadIdx.x & 63, c = threadIdx.x % LPR, hk = (int)(unit % (uint32_t)a.Hkv);
+    const int i0 = (int)(unit / (uint32_t)a.Hkv) * TB, i = i0 + threadIdx.x / LPR;
     const int b0 = ended_before(a, i0, lane);
     const bool there = i < a.N;
     long long page = 0;
@@ -167,8 +185,8 @@ __global__ __launch_bounds__(256) void kda_cache_rows_kernel(const CacheArgs a) 
             widen8(y, cy, block_scale(ey));
         }
         const long long to = ((long long)i * a.Hkv + hk) * D + 8 * c;
-        store8(reinterpret_cast<T*>(a.k_out) + to, x);
-        store8(reinterpret_cast<T*>(a.v_out) + to, y);
+        store8<STREAMED>(reinterpret_cast<T*>(a.k_out) + to, x);
+        store8<STREAMED>(reinterpret_cast<T*>(a.v_out) + to, y);
     }
 }
 
@@ -177,6 +195,7 @@ namespace {
 // Sequences' shares of a call: in tiles of 128 keys, `per` of them a slot, so that the slots of all sequences
 // are alike whatever their lengths; each sequence has one slot at least.
 constexpr int kSlotKeys = 128;
+constexpr float kSumMax = 16384.0f;
 
 __device__ __forceinline__ int seq_len(const AttnStepArgs& a, int b) {
     const int n = a.lens[b];
@@ -197,7 +216,9 @@ __device__ __forceinline__ int wave_sum(int x) {
 }
 __device__ __forceinline__ int tiles_per_slot(const AttnStepArgs& a, int lane) {
     int all = 0;
-    for (int b = 0; b < a.N; b += 64) all += wave_sum(seq_tiles(a, b + lane));
+    if (a.N == 1) all = seq_tiles(a, 0);
+    else
+        for (int b = 0; b < a.N; b += 64) all += wave_sum(seq_tiles(a, b + lane));
     const int per = (int)(((long long)all + a.want - 1) / a.want);
     return per > 1 ? per : 1;
 }
@@ -212,7 +233,7 @@ __device__ __forceinline__ int tiles_per_slot(const AttnStepArgs& a, int lane) {
 // wave's own in LDS to be transposed.  Queries of fp32 are fed as three bf16 parts, probabilities as two, or three
 // for fp32 outputs: the products take a fifth of the time that the loads do.
 template <int D, typename T>
-__global__ __launch_bounds__(256) void kda_attn_step_kernel(const AttnStepArgs a) {
+__global__ __launch_bounds__(256, D == 128 && sizeof(T) == 4 ? 3 : 4) void kda_attn_step_kernel(const AttnStepArgs a) {
     constexpr int TK = 32;                        // rows per tile
     constexpr int CH = D / 4, KB = D / 32;        // channels of a lane, dwords of them
     constexpr int OP = D + 4;                     // pitch of the partial outputs
@@ -232,7 +253,10 @@ __global__ __launch_bounds__(256) void kda_attn_step_kernel(const AttnStepArgs a
     // the slot's sequence and its part of it
     const int per = tiles_per_slot(a, lane);
     int b = -1, split = slot, n_split = 0;
-    for (int b0 = 0; b0 < a.N; b0 += 64) {
+    if (a.N == 1) {
+        n_split = seq_slots(seq_tiles(a, 0), per);
+        if (slot < n_split) b = 0;
+    } else for (int b0 = 0; b0 < a.N; b0 += 64) {
         const int mine = b0 + lane < a.N ? seq_slots(seq_tiles(a, b0 + lane), per) : 0;
         int sum = mine;
 #pragma unroll
@@ -281,20 +305,19 @@ __global__ __launch_bounds__(256) void kda_attn_step_kernel(const AttnStepArgs a
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = 0.0f;
             }
+            Frag<__bf16> f[QP];
+            parts_of<QP>(f, f32x4_t{x[0], x[1], x[2], x[3]}, f32x4_t{x[4], x[5], x[6], x[7]});
 #pragma unroll
-            for (int i = 0; i < QP; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    fq[i][kb].set(j, x[j]);
-                    x[j] -= fq[i][kb].get(j);
-                }
+            for (int i = 0; i < QP; ++i) fq[i][kb] = f[i];
         }
     }
     f32x4_t O[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) O[i] = zero4();
     float m = -INFINITY, l = 0.0f;
+    bool ready = false;                           // every row has a maximum
     const float sc = a.scale * kLog2e;
+    const int all_see = len - a.m + 1 + (int)((uint32_t)(16 * rt) / (uint32_t)R) < k1 ? len - a.m + 1 + (int)((uint32_t)(16 * rt) / (uint32_t)R) : k1;
 
     const int* table = a.pages + (long long)b * a.max_pages;
     const long long head = (long long)hk * a.page_bytes, pages_step = (long long)a.Hkv * a.page_bytes;
@@ -335,8 +358,18 @@ __global__ __launch_bounds__(256) void kda_attn_step_kernel(const AttnStepArgs a
         request(start);
     }
     for (int t0 = start; t0 < k1; t0 += 4 * TK) {
+        // values to LDS, then the scores: their codes are in registers for as short as can be
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            const float sv = block_scale(ok[kt] && t0 + 16 * kt + r < k1 ? ew[kt] : kLeastExp);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                bf16x8_t w;
+                widen8(w, cw[kt][kb], sv);
+                *reinterpret_cast<KDA_LDS bf16x8_t*>(put[kb] + 16 * 32 * kt) = w;
+            }
+        }
         f32x4_t sT[2];
-        bf16x8_t wide[2][KB];
         bool live[2];
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
@@ -350,60 +383,63 @@ __global__ __launch_bounds__(256) void kda_attn_step_kernel(const AttnStepArgs a
 #pragma unroll
                 for (int i = QP - 1; i >= 0; --i) sT[kt] = mma(fk, fq[i][kb], sT[kt]);
             }
-            const uint32_t e = ok[kt] && t0 + 16 * kt + r < k1 ? ew[kt] : kLeastExp;
-            const float sv = block_scale(e);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) widen8(wide[kt][kb], cw[kt][kb], sv);
         }
+        __builtin_amdgcn_sched_barrier(0);
         if (t0 + 4 * TK < k1) request(t0 + 4 * TK);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) *reinterpret_cast<KDA_LDS bf16x8_t*>(put[kb] + 16 * 32 * kt) = wide[kt][kb];
 
-        const int to = (sees < k1 ? sees : k1) - t0 - 4 * g;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sT[kt][j] = live[kt] && 16 * kt + j < to ? sT[kt][j] * sc : -INFINITY;
-                mx = fmaxf(mx, sT[kt][j]);
-            }
-        // The maximum only has to keep exponentials in range: it is raised where a score passes it by 2^8.
-        float al = 1.0f;
-        const bool raise = __any(mx > m + 8.0f);
-        if (raise) {
-            mx = fmaxf(m, max_over_groups<true>(mx));
-            al = fast_exp2(m - (mx == -INFINITY ? 0.0f : mx));
-            m = mx;
-        }
-        const float base = m == -INFINITY ? 0.0f : m;   // nothing seen so far, or scores below fp32's range: no weight
-        float sum = 0.0f;
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sT[kt][j] = fast_exp2(sT[kt][j] - base);
-                sum += sT[kt][j];
-            }
-        l = l * al + sum;
-        Frag<__bf16> fp[PP];
-#pragma unroll
-        for (int i = 0; i < PP; ++i) {
-            acc_pair_frag<__bf16>(fp[i], sT[0], sT[1], true);
+        // The maximum only has to keep exponentials in range.  A tile that every row sees whole is taken with the maximum
+        // at hand; where a sum of its exponentials passes kSumMax, and for the others, it is brought up to date.
+        const bool whole = t0 + TK <= all_see && live[0] && live[1];
+        bool done = false;
+        if (whole && ready) {
+            f32x4_t p[2];
+            float sum = 0.0f;
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sT[kt][j] -= fp[i].get(4 * kt + j);
+                for (int j = 0; j < 4; ++j) {
+                    p[kt][j] = fast_exp2(fmaf(sT[kt][j], sc, -m));
+                    sum += p[kt][j];
+                }
+            done = !__any(!(sum < kSumMax));
+            if (done) {
+                l += sum;
+                sT[0] = p[0];
+                sT[1] = p[1];
+            }
         }
-        if (raise) {
+        if (!done) {
+            const int to = (sees < k1 ? sees : k1) - t0 - 4 * g;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!whole) sT[kt][j] = live[kt] && 16 * kt + j < to ? sT[kt][j] : -INFINITY;
+                    mx = fmaxf(mx, sT[kt][j]);
+                }
+            mx = fmaxf(m, max_over_groups<true>(mx) * sc);
+            const float base = mx == -INFINITY ? 0.0f : mx;   // nothing seen so far, or scores below fp32's range: no weight
+            const float al = fast_exp2(m - base);
+            m = mx;
+            float sum = 0.0f;
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sT[kt][j] = fast_exp2(fmaf(sT[kt][j], sc, -base));
+                    sum += sT[kt][j];
+                }
+            l = l * al + sum;
+            ready = __all(mx != -INFINITY);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) O[i][j] *= al;
         }
+        Frag<__bf16> fp[PP];
+        parts_of<PP>(fp, sT[0], sT[1]);
         wave_order();
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -459,18 +495,19 @@ __global__ __launch_bounds__(256) void kda_attn_step_kernel(const AttnStepArgs a
     }
 }
 
-// Joins the slots of a sequence that has more than one.  grid: (sequence, query, head) rows; one wave: D / 4 lanes
-// own four channels of a slot, and 64 / (D / 4) slots are taken side by side.
+// Joins the slots of a sequence that has more than one.  grid: (sequence, query, head) rows; D / 4 lanes own four channels
+// of a slot, and the 4 * 64 / (D / 4) groups of a workgroup take slots side by side.
 template <int D, typename T>
-__global__ __launch_bounds__(64) void kda_attn_step_join_kernel(const AttnStepArgs a) {
-    constexpr int NL = D / 4, NS = 64 / NL;
-    const int lane = threadIdx.x, d = (lane % NL) * 4, i0 = lane / NL;
+__global__ __launch_bounds__(256) void kda_attn_step_join_kernel(const AttnStepArgs a) {
+    constexpr int NL = D / 4, NS = 256 / NL;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, d = (tid % NL) * 4, i0 = tid / NL;
     const uint32_t mh = (uint32_t)a.m * (uint32_t)a.H;
     const int b = (int)(blockIdx.x / mh);
     const uint32_t place = blockIdx.x - (uint32_t)b * mh;
     const int per = tiles_per_slot(a, lane);
     int before = 0, n = 1;
-    for (int b0 = 0; b0 <= b; b0 += 64) {
+    if (a.N == 1) before = n = seq_slots(seq_tiles(a, 0), per);
+    else for (int b0 = 0; b0 <= b; b0 += 64) {
         const int mine = b0 + lane <= b ? seq_slots(seq_tiles(a, b0 + lane), per) : 0;
         before += wave_sum(mine);
         if (b - b0 < 64) n = __builtin_amdgcn_readlane(mine, b - b0);
@@ -479,40 +516,59 @@ __global__ __launch_bounds__(64) void kda_attn_step_join_kernel(const AttnStepAr
     if (n == 1) return;
     const float* ml = a.ws_ml + 2 * ((long long)before * mh + place);
     const float* o = a.ws_o + ((long long)before * mh + place) * D + d;
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 64) M = fmaxf(M, ml[2 * (long long)i * mh]);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
-    const float base = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
+    // every group keeps a maximum of its own slots
+    float M = -INFINITY, L = 0.0f;
     f32x4_t v = zero4();
-#pragma unroll 4
+#pragma unroll 8
     for (int i = i0; i < n; i += NS) {
-        const float f = fast_exp2(ml[2 * (long long)i * mh] - base);
-        L = fmaf(f, ml[2 * (long long)i * mh + 1], L);
+        const float m = ml[2 * (long long)i * mh], l = ml[2 * (long long)i * mh + 1];
         const f32x4_t x = *reinterpret_cast<const f32x4_t*>(o + (long long)i * mh * D);
+        const float top = fmaxf(M, m), base = top == -INFINITY ? 0.0f : top;
+        const float f = fast_exp2(M - base), e = fast_exp2(m - base);
+        M = top;
+        L = fmaf(L, f, e * l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], f, e * x[j]);
+    }
+    __shared__ float sM[NS], sL[NS];
+    __shared__ __attribute__((aligned(16))) float sv[NS][D];
+    *reinterpret_cast<f32x4_t*>(&sv[i0][d]) = v;
+    if (d == 0) {
+        sM[i0] = M;
+        sL[i0] = L;
+    }
+    __syncthreads();
+    if (tid >= NL) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) M = fmaxf(M, sM[i]);
+    const float base = M == -INFINITY ? 0.0f : M;
+    L = 0.0f;
+    v = zero4();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const float f = fast_exp2(sM[i] - base);
+        L = fmaf(f, sL[i], L);
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sv[i][d]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = fmaf(f, x[j], v[j]);
-    }
-#pragma unroll
-    for (int x = NL; x < 64; x <<= 1) {
-        L += __shfl_xor(L, x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += __shfl_xor(v[j], x);
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= inv;
-    if (i0 == 0) store4<T>(reinterpret_cast<T*>(a.o) + (long long)blockIdx.x * D + d, v);
+    store4<T>(reinterpret_cast<T*>(a.o) + (long long)blockIdx.x * D + d, v);
 }
 
 namespace {
 
-template <int D, typename T> hipError_t cache_rows_t(bool write, const CacheArgs& a, hipStream_t s) {
+template <int D, typename T> hipError_t cache_rows_t(bool write, CacheArgs a, hipStream_t s) {
     constexpr int TB = 256 / (D / 8);
-    const dim3 grid((unsigned)(((long long)a.N + TB - 1) / TB), (unsigned)a.Hkv);
-    if (write) kda_cache_rows_kernel<D, T, true><<<grid, 256, 0, s>>>(a);
-    else kda_cache_rows_kernel<D, T, false><<<grid, 256, 0, s>>>(a);
+    a.n_units = ((long long)a.N + TB - 1) / TB * a.Hkv;
+    a.per_xcd = (a.n_units + 7) / 8;
+    const dim3 grid((unsigned)(8 * a.per_xcd));
+    if (write) kda_cache_rows_kernel<D, T, true, false><<<grid, 256, 0, s>>>(a);
+    else if (a.streamed) kda_cache_rows_kernel<D, T, false, true><<<grid, 256, 0, s>>>(a);
+    else kda_cache_rows_kernel<D, T, false, false><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -521,7 +577,7 @@ template <int D, typename T> hipError_t attn_step_t(const AttnStepArgs& a, hipSt
     kda_attn_step_kernel<D, T><<<dim3((unsigned)((long long)a.slots * rt * a.Hkv)), 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.slots == a.N) return e;
-    kda_attn_step_join_kernel<D, T><<<dim3((unsigned)((long long)a.N * a.m * a.H)), 64, 0, s>>>(a);
+    kda_attn_step_join_kernel<D, T><<<dim3((unsigned)((long long)a.N * a.m * a.H)), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

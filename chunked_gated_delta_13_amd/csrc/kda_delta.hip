@@ -45,31 +45,6 @@ __device__ __forceinline__ void frag_get(Frag<__bf16>& f, const KDA_LDS __bf16* 
     f.v = *reinterpret_cast<const KDA_LDS bf16x8_t*>(p);
 }
 
-// Two stacked accumulator tiles as an operand in NP parts, the first one largest.  (bf16: a pair of elements is rounded by
-// one instruction and widened again by one each.)
-template <int NP> __device__ __forceinline__ void parts_of(Frag<__bf16> (&f)[NP], f32x4_t lo, f32x4_t hi) {
-    float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bf16x2_t u = {(__bf16)x[2 * j], (__bf16)x[2 * j + 1]};
-            f[p].v[2 * j] = u[0];
-            f[p].v[2 * j + 1] = u[1];
-            if (p + 1 < NP) {
-                uint32_t w = __builtin_bit_cast(uint32_t, u);
-                asm("" : "+v"(w));   // (else either element is rounded once more on its own)
-                x[2 * j] -= __uint_as_float(w << 16);
-                x[2 * j + 1] -= __uint_as_float(w & 0xffff0000u);
-            }
-        }
-    }
-}
-template <int NP> __device__ __forceinline__ void parts_of(Frag<float> (&f)[NP], f32x4_t lo, f32x4_t hi) {
-    static_assert(NP == 1, "fp32 operands are whole");
-    acc_pair_frag<float>(f[0], lo, hi, true);
-}
-
 // c += a b of two rows of tiles for factors in parts: the products above 2^-24, the smallest first.
 template <typename T, int NP>
 __device__ __forceinline__ void mma_parts(const Frag<T> (&a)[2][NP], const Frag<T> (&b)[NP], f32x4_t& c0, f32x4_t& c1) {

@@ -109,7 +109,9 @@ struct CacheArgs {
     const int* cu;            // [B + 1], or nullptr: token i is sequence i's
     const int* start;         // [B] position of each sequence's first token, or nullptr (0)
     long long k_stride, v_stride, page_bytes;
+    long long n_units, per_xcd;
     int B, N, Hkv, n_pages, max_pages, page, page_shift;
+    int streamed;             // read rows go past the caches
 };
 
 hipError_t launch_cache_rows(bool write, int d, bool f32, const CacheArgs& a, hipStream_t s);

@@ -576,7 +576,7 @@ kda_status_t kda_cache_read(const void *k_cache, const void *v_cache, const int 
  *   workspace  kda_attn_step_workspace_bytes(...) bytes of device memory (may be NULL when that is 0), written before
  *              it is read; calls that overlap in time need one each
  * Rows whose table entry lies outside the pool are not seen; n_pages is at least 1.  N == 0, m == 0 or H == 0 is a no-op.
- * N m H is at most 2^25, the tokens that all tables hold, N max_pages page / 128 + N, at most 2^30, and N ceil(m H / Hkv / 16) Hkv at most
+ * N m H is at most 2^23, the tokens that all tables hold, N max_pages page / 128 + N, at most 2^30, and N ceil(m H / Hkv / 16) Hkv at most
  * about 2^23.  Scores have to lie inside fp32's range, as above.  A NaN in a row that a later one of the m queries sees
  * reaches the earlier ones too.  Statistics and sums are fp32, every cached value is exact, and a probability enters the
  * product with v as two bf16 parts (16 bits; three, 24 bits, for fp32 outputs).
