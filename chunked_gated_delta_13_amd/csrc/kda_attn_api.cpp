@@ -36,11 +36,11 @@ kda_status_t check_attn_shape(int B, int Nq, int Nk, int H, int Hkv, int d, kda_
     return KDA_OK;
 }
 
-// A prompt's workgroups take 128 rows (query and head of a group) each where that gives every compute unit one,
-// else 64.  Where these are few too, their keys are split into ranges of at least two tiles (one in fp32), for at
-// most two workgroups per compute unit (one in fp32), if that shortens the chain: in microseconds, a tile takes
-// 0.65 (d = 64) or 0.9 (d = 128) in bf16 and 2.6 or 4.8 in fp32, the join 3, and a range's outputs are written
-// and read at 3.7 TB/s, so that the best count is the root of tiles / outputs.  Lengths are on the device: the
+// A prompt's workgroups take 128 rows (query and head of a group) each where that gives every compute unit one, else 64.
+// Where 64 rows do not give every compute unit one either, groups of waves share the rows' keys (bf16), and the keys are
+// split into ranges, with at most one workgroup per compute unit, if that shortens the chain: in microseconds, a step of
+// the groups takes 0.65 (d = 64) or 0.9 (d = 128) in bf16 and 2 or 3.6 in fp32, the join 3, and a range's outputs are written
+// and read at 3.7 TB/s, so that the best count is the root of steps / outputs.  Lengths are on the device: the
 // sequences are taken to be alike.
 void attn_plan(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dt, int* few, int* n_split) {
     const int cus = cu_count();
@@ -49,15 +49,17 @@ void attn_plan(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dt, int
     *few = Hkv * (rows / 128 + (B + 1) / 2) < cus ? 1 : 0;
     *n_split = 1;
     const long long units = Hkv * (rows / 64 + (B + 1) / 2);
-    if (!*few || Nq == 0 || B == 0) return;
-    const long long tiles = ((long long)Nk / B + 63) / 64;
-    const double tile_us = f32 ? 0.4 + 0.034 * d : 0.42 + 0.0036 * d, part_us = (double)Nq * H * d * 8 / 3.7e6;
-    long long n = (f32 ? 1LL : 2LL) * cus / units;
-    if (n > tiles / (f32 ? 1 : 2)) n = tiles / (f32 ? 1 : 2);
-    const double best = sqrt((double)tiles * tile_us / part_us);
+    if (units > cus || Nq == 0 || B == 0) return;
+    *few = 2;
+    const int kg = f32 ? 1 : kda::attn_groups(d);
+    const long long tiles = ((long long)Nk / B + 63) / 64, steps = (tiles + kg - 1) / kg;
+    const double step_us = f32 ? 0.4 + 0.025 * d : 0.42 + 0.0036 * d, part_us = (double)Nq * H * d * 8 / 3.7e6;
+    long long n = cus / units;
+    if (n > steps) n = steps;
+    const double best = sqrt((double)steps * step_us / part_us);
     if (best < (double)n) n = (long long)best;
     if (n < 2) return;
-    const double whole = (double)tiles * tile_us, split = (double)((tiles + n - 1) / n) * tile_us + (double)n * part_us + 3.0;
+    const double whole = (double)steps * step_us, split = (double)((steps + n - 1) / n) * step_us + (double)n * part_us + 3.0;
     if (split < whole) *n_split = (int)n;
 }
 

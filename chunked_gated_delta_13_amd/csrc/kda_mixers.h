@@ -79,6 +79,9 @@ struct WindowArgs {
 hipError_t launch_window_prefill(int d, bool f32, const WindowArgs& a, hipStream_t s);
 hipError_t launch_window_step(int d, bool f32, const WindowArgs& a, hipStream_t s);
 
+// Groups of waves that share the keys of 64 rows where compute units are left: what LDS holds.
+constexpr int attn_groups(int d) { return d == 64 ? 4 : 2; }
+
 struct AttnArgs {
     const void* q;            // [Nq] rows of H * d, stride q_stride elements
     const void* k;            // [Nk] rows of Hkv * d
@@ -89,9 +92,9 @@ struct AttnArgs {
     long long q_stride, k_stride, v_stride;
     int B, Nq, Nk, H, Hkv;
     float scale;
-    int few;                  // 1: too few rows for 128 of them per workgroup
+    int few;                  // 1: too few rows for 128 of them per workgroup; 2: for 64 of them on every compute unit
     int n_split;              // ranges of keys
-    long long per_xcd;        // eighths of the row tiles
+    int n_sets;               // sets of kv heads that XCDs share out
     float* ws_o;              // [Nq * H, n_split, d] partial outputs of a split call
     float* ws_ml;             // [Nq * H, n_split, 2] their maxima (base 2) and sums
 };

@@ -521,7 +521,8 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
  * time need one each); with NULL they run as one range.  Scores have to lie inside fp32's range: one below it has no
  * weight, a query with none inside it gets zeros, one with a score above it NaN.  A NaN or an infinity in k or v may reach the
  * queries up to 127 before it as well.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded
- * to bf16 as the operand of the product with v.
+ * to bf16 as the operand of the product with v.  fp32 inputs and probabilities are multiplied in three bf16 parts (24
+ * bits); values from 3.39e38 on count as infinities there.
  */
 size_t kda_attn_prefill_workspace_bytes(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dtype);
 kda_status_t kda_attn_prefill(const void *q, const void *k, const void *v, const int *cu_q, const int *cu_k,

@@ -106,7 +106,7 @@ SPLITS = [
     ([1], [3000], 2, 1, 128, "bf16"),
     ([5, 3], [2000, 70], 4, 2, 64, "f32"),
     ([40, 33, 0, 17], [900, 40, 2000, 1], 4, 2, 128, "bf16"),
-    ([64, 20], [100, 1500], 2, 1, 64, "bf16"),
+    ([64, 20], [100, 9000], 2, 1, 64, "bf16"),
     ([6, 9], [4, 1500], 3, 3, 128, "f32"),                        # queries that see none
 ]
 
