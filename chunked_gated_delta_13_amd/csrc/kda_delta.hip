@@ -14,9 +14,10 @@
 // Numerics.  bf16 keys and queries are exact operands.  On the state's path S, T, R and U enter the products as three
 // bf16 parts (24 bits; the six products of two such factors above 2^-24 are formed), so that states are as exact as with
 // fp32 operands, at three to six bf16 products instead of the sixteen that one in fp32 takes.  The outputs, rounded to
-// bf16 anyway, take S in one part, U in two and B in one.  fp32 inputs use fp32 products throughout.
+// bf16 anyway, take S and U in two and B in one (S in one part costs 5% less and takes them from 2.2e-3 to 2.5e-3 off,
+// 1.7e-3 of it their own rounding).  fp32 inputs use fp32 products throughout.
 #include "kda_mixers.h"
-#include "kda_tile.h"
+#include "kda_softmax.h"
 
 namespace kda {
 
@@ -75,25 +76,12 @@ __device__ __forceinline__ double lane_f64(double x, int lane) {
     return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
 }
 
-// LDS accesses of one wave run in program order; this keeps the compiler from reordering them.
-__device__ __forceinline__ void wave_order() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // Values of lane I of each quad.
 template <int I> __device__ __forceinline__ f32x4_t quad_lane(const f32x4_t& v) {
     f32x4_t o;
 #pragma unroll
     for (int x = 0; x < 4; ++x) o[x] = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v[x]), I * 0x55, 0xF, 0xF, true));
     return o;
-}
-
-template <typename T> __device__ __forceinline__ void store4_t(T* p, const f32x4_t& v) {
-    typename Vec4<T>::type o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(v[i]);
-    *reinterpret_cast<typename Vec4<T>::type*>(p) = o;
 }
 
 }  // namespace
@@ -295,7 +283,9 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
                         for (int i = 0; i < NA; ++i) X[i] = mma(kf[kb & 1][i], s[kb & 1][p], X[i]);
                     if constexpr (OUT) {
 #pragma unroll
-                        for (int i = 0; i < NA; ++i) O[i] = mma(s[kb & 1][0], qf[i], O[i]);
+                        for (int p = NP > 1 ? 1 : 0; p >= 0; --p)
+#pragma unroll
+                            for (int i = 0; i < NA; ++i) O[i] = mma(s[kb & 1][p], qf[i], O[i]);
                     }
                 }
             }
@@ -359,7 +349,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
                 }
 #pragma unroll
                 for (int i = 0; i < NA; ++i)
-                    if (n * C + 16 * i + r < todo) store4_t<T>(at_byte(op + (long long)(n * C + 16 * i) * o_step, pinned_u(o_off)), O[i]);
+                    if (n * C + 16 * i + r < todo) store4<T>(at_byte(op + (long long)(n * C + 16 * i) * o_step, pinned_u(o_off)), O[i]);
             }
             const float dec = arr[5 * C];
 #pragma unroll
@@ -809,7 +799,7 @@ __global__ __launch_bounds__(4 * DV) void kda_delta_step_kernel(const DeltaArgs 
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) q[j] = fmaf(al, q[j], kq * u[j]);
-        store4_t<T>(reinterpret_cast<T*>(a.o) + nh * DV + col, q);
+        store4<T>(reinterpret_cast<T*>(a.o) + nh * DV + col, q);
     }
 #pragma unroll
     for (int m = 0; m < RPT; ++m) {

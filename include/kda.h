@@ -468,14 +468,15 @@ kda_status_t kda_window_step(const void *q, const void *k, const void *v, void *
  *   S_T        [B, H, dk, dv] fp32 or NULL  (out)  state after each sequence's last token; may be S0
  *   dk, dv     64 or 128 each
  *   seg_len    0: the library splits the sequence where that fills the GPU; else tokens per segment (a multiple of 64;
- *              >= T = no split).  The result does not depend on it beyond rounding
+ *              >= T = no split).  The result does not depend on it beyond rounding as long as no update expands (beta |k|^2 at
+ *              most 2): a split takes what lies before a token as forgotten if the decays from it to the end of its segment
+ *              multiply to less than 2^-126.  Other keys need seg_len >= T
  *   workspace  kda_delta_prefill_workspace_bytes(...) bytes of device memory (may be NULL when that is 0), written
  *              before it is read; calls that overlap in time need one each
  * Rows of q, k and v start on 16-byte boundaries; H * dv and the three strides are at most 2^22 elements.  B * H, times
- * the segments of a split, is at most 2^20, T at most
- * 2^30.  T == 0 is valid: S_T receives S0 (or zeros).  B == 0 or H == 0 is a no-op.  A NaN or an infinity may reach the other tokens of its block of 64 and
- * every token after it.  States and exponents are fp32, and with bf16 inputs every factor on the state's path keeps 24
- * bits; the products that form o take the state and the weights 2^(c_i - c_j) (q_i . k_j) rounded to bf16.
+ * the segments of a split, is at most 2^20, T at most 2^30.  T == 0 is valid: S_T receives S0 (or zeros).  B == 0 or
+ * H == 0 is a no-op.  A NaN or an infinity may reach the other tokens of its block of 64 and every token after it.  States and exponents are fp32, and with bf16 inputs every factor on the state's path keeps 24
+ * bits; the products that form o take the state in 16 bits and the weights 2^(c_i - c_j) (q_i . k_j) rounded to bf16.
  */
 size_t kda_delta_prefill_workspace_bytes(int B, int T, int H, int Hk, int dk, int dv, kda_dtype_t dtype,
                                          int seg_len);
