@@ -54,6 +54,8 @@ CASES = [
     ([70, 66], [2, 500], 2, 2, 128, "f32", 0, 0),
     ([1] * 70, [i % 9 for i in range(70)], 2, 1, 64, "bf16", 0, 0),   # more sequences than lanes of a wave
     ([2] * 130 + [90], None, 16, 2, 64, "bf16", 0, 0),
+    ([200, 250], None, 56, 8, 128, "bf16", 0, 0),                # 64 rows a workgroup, one group of waves
+    ([200, 20, 230], [210, 20, 900], 28, 4, 64, "bf16", 0, 2),
 ]
 
 
