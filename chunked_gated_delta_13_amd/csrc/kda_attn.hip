@@ -37,17 +37,22 @@ struct AttnUnit {
 
 // An XCD serves every `n_sets`-th kv head (n_sets: the greatest common divisor of their count and 8), so that what it reads
 // is read again from its own L2; XCDs with the same heads take turns at their row tiles.  Long tiles are started
-// first, whatever their head: with one head after the other six prompts of up to 2000 tokens took half as long again.
+// first, whatever their head: with one head after the other six prompts of up to 2000 tokens took half as long again.  The
+// ranges of a split, whose keys few workgroups share, go to the XCDs in turn.
 template <int BM, bool SPLIT> __device__ __forceinline__ bool attn_unit(const AttnArgs& a, int lane, AttnUnit& u) {
-    uint32_t unit = blockIdx.x >> 3;
-    u.split = 0;
+    int x;
     if constexpr (SPLIT) {
+        uint32_t unit = blockIdx.x;
         u.split = (int)(unit % (uint32_t)a.n_split);
         unit /= (uint32_t)a.n_split;
+        u.hk = (int)(unit % (uint32_t)a.Hkv);
+        x = (int)(unit / (uint32_t)a.Hkv);
+    } else {
+        const uint32_t unit = blockIdx.x >> 3, xcd = blockIdx.x & 7, sets = (uint32_t)a.n_sets, heads = (uint32_t)a.Hkv / sets;
+        u.split = 0;
+        u.hk = (int)(unit % heads * sets + xcd % sets);
+        x = (int)(unit / heads * (8 / sets) + xcd / sets);
     }
-    const uint32_t xcd = blockIdx.x & 7, sets = (uint32_t)a.n_sets, heads = (uint32_t)a.Hkv / sets;
-    u.hk = (int)(unit % heads * sets + xcd % sets);
-    int x = (int)(unit / heads * (8 / sets) + xcd / sets);
     const int R = (int)((uint32_t)a.H / (uint32_t)a.Hkv);
     u.R = R;
 
@@ -617,48 +622,20 @@ __global__ __launch_bounds__(512) void kda_attn_prefill_f32_kernel(const AttnArg
     }
 }
 
-// Joins the ranges of a split call.  grid: (query, head) rows; one wave: D / 4 lanes own four channels of a
-// range, and 64 / (D / 4) ranges are taken side by side.  Rows outside the sequences have no parts.
+// Joins the ranges of a split call.  grid: (query, head) rows.  Rows outside the sequences have no parts.
 template <int D, typename T>
-__global__ __launch_bounds__(64) void kda_attn_join_kernel(const AttnArgs a) {
-    constexpr int NL = D / 4, NS = 64 / NL;
+__global__ __launch_bounds__(256) void kda_attn_join_kernel(const AttnArgs a) {
     const long long row = blockIdx.x;
-    const int lane = threadIdx.x, d = (lane % NL) * 4, i0 = lane / NL;
     const int query = (int)(blockIdx.x / (uint32_t)a.H);
     bool in = false;
-    for (int b = lane; b < a.B; b += 64) {
+    for (int b = threadIdx.x & 63; b < a.B; b += 64) {
         int first = 0, len = 0;
         packed(a.cu_q, b, a.Nq, &first, &len);
         in = in || (query >= first && query - first < len);
     }
-    if (!__any(in)) return;
-    const float* ml = a.ws_ml + 2 * row * a.n_split;
-    const float* o = a.ws_o + row * a.n_split * D + d;
-    float M = -INFINITY;
-    for (int i = lane; i < a.n_split; i += 64) M = fmaxf(M, ml[2 * i]);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
-    const float base = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
-    f32x4_t v = zero4();
-#pragma unroll 4
-    for (int i = i0; i < a.n_split; i += NS) {
-        const float f = fast_exp2(ml[2 * i] - base);
-        L = fmaf(f, ml[2 * i + 1], L);
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(o + (long long)i * D);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf(f, x[j], v[j]);
-    }
-#pragma unroll
-    for (int x = NL; x < 64; x <<= 1) {
-        L += __shfl_xor(L, x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += __shfl_xor(v[j], x);
-    }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] *= inv;
-    if (i0 == 0) store4<T>(reinterpret_cast<T*>(a.o) + row * D + d, v);
+    if (!__any(in)) return;   // (every wave finds the same)
+    const long long first = row * a.n_split;
+    join_parts<D, T>(a.ws_ml + 2 * first, a.ws_o + first * D, a.n_split, 1, reinterpret_cast<T*>(a.o) + row * D);
 }
 
 namespace {
@@ -672,13 +649,13 @@ hipError_t attend(AttnArgs a, hipStream_t s) {
     a.n_sets = 1;
     while (a.n_sets < 8 && a.Hkv % (2 * a.n_sets) == 0) a.n_sets *= 2;
     const long long turns = 8 / a.n_sets, per_xcd = (tiles + turns - 1) / turns;
-    const long long blocks = 8 * per_xcd * (a.Hkv / a.n_sets) * (SPLIT ? a.n_split : 1);
+    const long long blocks = SPLIT ? tiles * a.Hkv * a.n_split : 8 * per_xcd * (a.Hkv / a.n_sets);
     if (blocks > 0xffffffffLL / THREADS) return hipErrorInvalidValue;
     if constexpr (sizeof(T) == 4) kda_attn_prefill_f32_kernel<D, SPLIT><<<dim3((unsigned)blocks), THREADS, 0, s>>>(a);
     else kda_attn_prefill_kernel<D, NQ, KG, SPLIT><<<dim3((unsigned)blocks), THREADS, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (!SPLIT || e != hipSuccess) return e;
-    kda_attn_join_kernel<D, T><<<dim3((unsigned)((long long)a.Nq * a.H)), 64, 0, s>>>(a);
+    kda_attn_join_kernel<D, T><<<dim3((unsigned)((long long)a.Nq * a.H)), 256, 0, s>>>(a);   // (few rows: see the plan)
     return hipGetLastError();
 }
 

@@ -13,7 +13,7 @@ using namespace kda::host;
 
 namespace {
 
-constexpr size_t kStreamedBytes = (size_t)192 << 20;   // results that do not stay in the 256 MB last-level cache
+constexpr size_t kStreamedBytes = (size_t)128 << 20;   // half of the last-level cache: what else is in use passes the rest
 constexpr long long kMaxRows = 1LL << 30;   // rows and keys that 32 bits count, with room for a tile more
 
 kda_status_t check_heads(int H, int Hkv, int d, kda_dtype_t dt) {
@@ -39,7 +39,7 @@ kda_status_t check_attn_shape(int B, int Nq, int Nk, int H, int Hkv, int d, kda_
 // A prompt's workgroups take 128 rows (query and head of a group) each where that gives every compute unit one, else 64.
 // Where 64 rows do not give every compute unit one either, groups of waves share the rows' keys (bf16), and the keys are
 // split into ranges, with at most one workgroup per compute unit, if that shortens the chain: in microseconds, a step of
-// the groups takes 0.65 (d = 64) or 0.9 (d = 128) in bf16 and 2 or 3.6 in fp32, the join 3, and a range's outputs are written
+// the groups takes 1.3 in bf16, and 1.5 (d = 64) or 2.75 (d = 128) in fp32, the join 3, and a range's outputs are written
 // and read at 3.7 TB/s, so that the best count is the root of steps / outputs.  Lengths are on the device: the
 // sequences are taken to be alike.
 void attn_plan(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dt, int* few, int* n_split) {
@@ -53,7 +53,7 @@ void attn_plan(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dt, int
     *few = 2;
     const int kg = f32 ? 1 : kda::attn_groups(d);
     const long long tiles = ((long long)Nk / B + 63) / 64, steps = (tiles + kg - 1) / kg;
-    const double step_us = f32 ? 0.4 + 0.025 * d : 0.42 + 0.0036 * d, part_us = (double)Nq * H * d * 8 / 3.7e6;
+    const double step_us = f32 ? 0.25 + 0.0195 * d : 1.3, part_us = (double)Nq * H * d * 8 / 3.7e6;
     long long n = cus / units;
     if (n > steps) n = steps;
     const double best = sqrt((double)steps * step_us / part_us);
@@ -249,7 +249,7 @@ kda_status_t kda_cache_read(const void* k_cache, const void* v_cache, const int*
     a.v_cache = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(v_cache));
     a.k_out = k;
     a.v_out = v;
-    a.streamed = 2 * out > kStreamedBytes ? 1 : 0;
+    a.streamed = 2 * out >= kStreamedBytes ? 1 : 0;
     (void)hipGetLastError();
     if (kda::launch_cache_rows(false, d, dt == KDA_F32, a, reinterpret_cast<hipStream_t>(stream)) != hipSuccess) return KDA_ERR_DEVICE;
     return KDA_OK;

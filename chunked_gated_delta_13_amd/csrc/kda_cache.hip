@@ -142,9 +142,10 @@ __device__ __forceinline__ int ended_before(const CacheArgs& a, int i, int lane)
 // lie beside each other in a page; the heads of the same tokens follow on the same XCD, so that whole rows of the packed
 // tensors are read or written at about the same time.
 //
-// STREAMED: rows that are read back past the last-level cache, for results that it does not hold anyway.  65536 tokens
-// of 8 heads of 128 in bf16 (256 MiB of results) 89 us with plain stores and 54 us streamed; 4096 tokens (16 MiB) 6.3
-// and 5.7 us, but attention of 16 queries that reads them next then takes 37.5 us instead of 32.6.
+// STREAMED: rows are read back past the last-level cache, from half its size of them on, where what else is in use passes the
+// rest.  8 heads of 128 in bf16, alone and with attention of 16 queries that reads them next: 65536 tokens (256 MiB) 89 and
+// 341 us with plain stores, 50 and 349 us streamed; 32768 tokens 28 and 188, 25 and 179 us; 16384 tokens 15 and 92, 12 and
+// 104 us.  A prompt's write and read of 48000 tokens 105 and 57 us.
 template <int D, typename T, bool WRITE, bool STREAMED>
 __global__ __launch_bounds__(256) void kda_cache_rows_kernel(const CacheArgs a) {
     constexpr int LPR = D / 8, TB = 256 / LPR;
@@ -495,12 +496,10 @@ __global__ __launch_bounds__(256, D == 128 && sizeof(T) == 4 ? 3 : 4) void kda_a
     }
 }
 
-// Joins the slots of a sequence that has more than one.  grid: (sequence, query, head) rows; D / 4 lanes own four channels
-// of a slot, and the 4 * 64 / (D / 4) groups of a workgroup take slots side by side.
+// Joins the slots of a sequence that has more than one.  grid: (sequence, query, head) rows.
 template <int D, typename T>
 __global__ __launch_bounds__(256) void kda_attn_step_join_kernel(const AttnStepArgs a) {
-    constexpr int NL = D / 4, NS = 256 / NL;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, d = (tid % NL) * 4, i0 = tid / NL;
+    const int lane = threadIdx.x & 63;
     const uint32_t mh = (uint32_t)a.m * (uint32_t)a.H;
     const int b = (int)(blockIdx.x / mh);
     const uint32_t place = blockIdx.x - (uint32_t)b * mh;
@@ -514,49 +513,8 @@ __global__ __launch_bounds__(256) void kda_attn_step_join_kernel(const AttnStepA
     }
     before -= n;
     if (n == 1) return;
-    const float* ml = a.ws_ml + 2 * ((long long)before * mh + place);
-    const float* o = a.ws_o + ((long long)before * mh + place) * D + d;
-    // every group keeps a maximum of its own slots
-    float M = -INFINITY, L = 0.0f;
-    f32x4_t v = zero4();
-#pragma unroll 8
-    for (int i = i0; i < n; i += NS) {
-        const float m = ml[2 * (long long)i * mh], l = ml[2 * (long long)i * mh + 1];
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(o + (long long)i * mh * D);
-        const float top = fmaxf(M, m), base = top == -INFINITY ? 0.0f : top;
-        const float f = fast_exp2(M - base), e = fast_exp2(m - base);
-        M = top;
-        L = fmaf(L, f, e * l);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], f, e * x[j]);
-    }
-    __shared__ float sM[NS], sL[NS];
-    __shared__ __attribute__((aligned(16))) float sv[NS][D];
-    *reinterpret_cast<f32x4_t*>(&sv[i0][d]) = v;
-    if (d == 0) {
-        sM[i0] = M;
-        sL[i0] = L;
-    }
-    __syncthreads();
-    if (tid >= NL) return;
-    M = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) M = fmaxf(M, sM[i]);
-    const float base = M == -INFINITY ? 0.0f : M;
-    L = 0.0f;
-    v = zero4();
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const float f = fast_exp2(sM[i] - base);
-        L = fmaf(f, sL[i], L);
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sv[i][d]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf(f, x[j], v[j]);
-    }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] *= inv;
-    store4<T>(reinterpret_cast<T*>(a.o) + (long long)blockIdx.x * D + d, v);
+    const long long first = (long long)before * mh + place;
+    join_parts<D, T>(a.ws_ml + 2 * first, a.ws_o + first * D, n, mh, reinterpret_cast<T*>(a.o) + (long long)blockIdx.x * D);
 }
 
 namespace {

@@ -14,8 +14,8 @@
 // Numerics.  bf16 keys and queries are exact operands.  On the state's path S, T, R and U enter the products as three
 // bf16 parts (24 bits; the six products of two such factors above 2^-24 are formed), so that states are as exact as with
 // fp32 operands, at three to six bf16 products instead of the sixteen that one in fp32 takes.  The outputs, rounded to
-// bf16 anyway, take S and U in two and B in one (S in one part costs 5% less and takes them from 2.2e-3 to 2.5e-3 off,
-// 1.7e-3 of it their own rounding).  fp32 inputs use fp32 products throughout.
+// bf16 anyway, take S, U and B in two (in one part S and B leave them 2.5e-3 off where their own rounding is 1.7e-3, and
+// the few outputs of a token or two up to 4e-3; it costs 8%).  fp32 inputs use fp32 products throughout.
 #include "kda_mixers.h"
 #include "kda_softmax.h"
 
@@ -107,9 +107,10 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
     constexpr int FR = 64 * 8;                                   // elements of an operand
     constexpr int ARR = 5 * C + 16;                              // exponents (high, low parts), 2^c, 2^(c_C - c), beta, 2^c_C
     constexpr int NLOW = NA * (NA - 1) / 2;
+    constexpr int OP = NP > 1 ? 2 : 1;                           // parts of a factor of the outputs
     struct Shared {
         T k[3][KT], q[OUT ? 2 : 1][KT], v[VT];
-        T t[NP][NF * FR], b[2][OUT ? NF * FR : 8];
+        T t[NP][NF * FR], b[2][OP][OUT ? NF * FR : 8];
         float low[NLOW * 256], diag[NA * 256], rows[NA * 256], pair[512];   // A's blocks below the diagonal, transposed; T's on it, as they
                                                                             // are and transposed; two of T's below it
         float arr[3][ARR];
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
                         for (int i = 0; i < NA; ++i) X[i] = mma(kf[kb & 1][i], s[kb & 1][p], X[i]);
                     if constexpr (OUT) {
 #pragma unroll
-                        for (int p = NP > 1 ? 1 : 0; p >= 0; --p)
+                        for (int p = OP - 1; p >= 0; --p)
 #pragma unroll
                             for (int i = 0; i < NA; ++i) O[i] = mma(s[kb & 1][p], qf[i], O[i]);
                     }
@@ -327,11 +328,10 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
 
             // 3: outputs, then the state
             if constexpr (OUT) {
-                const KDA_LDS T* bf = lds_pin(&sh->b[n & 1][0] + lane * 8);
-                constexpr int UP = NP > 1 ? 2 : 1;
-                Frag<T> f[NF];
+                const KDA_LDS T* bf = lds_pin(&sh->b[n & 1][0][0] + lane * 8);
+                Frag<T> f[2][NF], uu[NQ][OP];
 #pragma unroll
-                for (int i = 0; i < NF; ++i) frag_get(f[i], bf + i * FR);
+                for (int i = 0; i < NF; ++i) frag_get(f[(OP - 1) & 1][i], bf + ((OP - 1) * NF + i) * FR);
 #pragma unroll
                 for (int i = 0; i < NA; ++i) {
                     const float grow = arr[2 * C + 16 * i + r];
@@ -339,13 +339,20 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
                     for (int j = 0; j < 4; ++j) O[i][j] *= grow;
                 }
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    Frag<T> uu[UP];
-                    parts_of<UP>(uu, U[2 * q], U[2 * q + 1]);
+                for (int q = 0; q < NQ; ++q) parts_of<OP>(uu[q], U[2 * q], U[2 * q + 1]);
+                // (the product of the two second parts is left out)
 #pragma unroll
-                    for (int p = UP - 1; p >= 0; --p)
+                for (int y = OP - 1; y >= 0; --y) {
+                    if (y > 0) {
 #pragma unroll
-                        for (int i = 2 * q; i < NA; ++i) O[i] = mma(uu[p], f[frag_at(i, q)], O[i]);
+                        for (int i = 0; i < NF; ++i) frag_get(f[0][i], bf + i * FR);
+                    }
+#pragma unroll
+                    for (int p = OP - 1 - y; p >= 0; --p)
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                            for (int i = 2 * q; i < NA; ++i) O[i] = mma(uu[q][p], f[y][frag_at(i, q)], O[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < NA; ++i)
@@ -465,7 +472,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
         // the halves of operands that lie above the diagonal stay zero
         for (int i = tid - 64 * NSW; i < NP * NF * FR; i += 256) (&sh->t[0][0])[i] = (T)0.0f;
         if constexpr (OUT)
-            for (int i = tid - 64 * NSW; i < 2 * NF * FR; i += 256) (&sh->b[0][0])[i] = (T)0.0f;
+            for (int i = tid - 64 * NSW; i < 2 * OP * NF * FR; i += 256) (&sh->b[0][0][0])[i] = (T)0.0f;
     }
     barrier_all();
     for (int n = first; n < nc; ++n) {
@@ -601,10 +608,19 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
         };
         auto weights = [&](int i, int j) {   // B_ij
             const f32x4_t P = product(q_rows, i, j), w = decays(i, j);
-            typename Vec4<T>::type o;
+            f32x4_t e;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) o[x] = from_f32<T>(i == j && 4 * g + x > r ? 0.0f : w[x] * P[x]);
-            *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->b[n & 1][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o;
+            for (int x = 0; x < 4; ++x) e[x] = i == j && 4 * g + x > r ? 0.0f : w[x] * P[x];
+#pragma unroll
+            for (int p = 0; p < OP; ++p) {
+                typename Vec4<T>::type o;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    o[x] = from_f32<T>(e[x]);
+                    e[x] -= to_f32<T>(o[x]);
+                }
+                *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->b[n & 1][p][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o;
+            }
         };
         if (cw < NA) put(cw, cw, Dt);
         if (cw == 1 || (NA == 4 && cw == 3)) {

@@ -64,4 +64,54 @@ template <typename T> __device__ __forceinline__ void store4(T* p, const f32x4_t
     *reinterpret_cast<vec4*>(p) = o;
 }
 
+// Joins n partial outputs of one row: part i's output lies at o + i step D, its maximum (base 2) and sum at ml + 2 i step.  256
+// threads: D / 4 lanes own four channels of a part, and the 256 / (D / 4) groups take parts side by side.
+template <int D, typename T>
+__device__ __forceinline__ void join_parts(const float* ml, const float* o, int n, long long step, T* out) {
+    constexpr int NL = D / 4, NS = 256 / NL;
+    const int tid = threadIdx.x, d = (tid % NL) * 4, i0 = tid / NL;
+    o += d;
+    // every group keeps a maximum of its own parts
+    float M = -INFINITY, L = 0.0f;
+    f32x4_t v = zero4();
+#pragma unroll 8
+    for (int i = i0; i < n; i += NS) {
+        const float m = ml[2 * (long long)i * step], l = ml[2 * (long long)i * step + 1];
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(o + (long long)i * step * D);
+        const float top = fmaxf(M, m), base = top == -INFINITY ? 0.0f : top;
+        const float f = fast_exp2(M - base), e = fast_exp2(m - base);
+        M = top;
+        L = fmaf(L, f, e * l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], f, e * x[j]);
+    }
+    __shared__ float sM[NS], sL[NS];
+    __shared__ __attribute__((aligned(16))) float sv[NS][D];
+    *reinterpret_cast<f32x4_t*>(&sv[i0][d]) = v;
+    if (d == 0) {
+        sM[i0] = M;
+        sL[i0] = L;
+    }
+    __syncthreads();
+    if (tid >= NL) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) M = fmaxf(M, sM[i]);
+    const float base = M == -INFINITY ? 0.0f : M;
+    L = 0.0f;
+    v = zero4();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const float f = fast_exp2(sM[i] - base);
+        L = fmaf(f, sL[i], L);
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sv[i][d]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(f, x[j], v[j]);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= inv;
+    store4<T>(out + d, v);
+}
+
 }  // namespace kda

@@ -476,7 +476,7 @@ kda_status_t kda_window_step(const void *q, const void *k, const void *v, void *
  * Rows of q, k and v start on 16-byte boundaries; H * dv and the three strides are at most 2^22 elements.  B * H, times
  * the segments of a split, is at most 2^20, T at most 2^30.  T == 0 is valid: S_T receives S0 (or zeros).  B == 0 or
  * H == 0 is a no-op.  A NaN or an infinity may reach the other tokens of its block of 64 and every token after it.  States and exponents are fp32, and with bf16 inputs every factor on the state's path keeps 24
- * bits; the products that form o take the state in 16 bits and the weights 2^(c_i - c_j) (q_i . k_j) rounded to bf16.
+ * bits, every factor of o 16.
  */
 size_t kda_delta_prefill_workspace_bytes(int B, int T, int H, int Hk, int dk, int dv, kda_dtype_t dtype,
                                          int seg_len);
@@ -521,8 +521,8 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
  * keys, joined afterwards, when a workspace of kda_attn_prefill_workspace_bytes(...) bytes is given (calls that overlap in
  * time need one each); with NULL they run as one range.  Scores have to lie inside fp32's range: one below it has no
  * weight, a query with none inside it gets zeros, one with a score above it NaN.  A NaN or an infinity in k or v may reach the
- * queries up to 127 before it as well.  Statistics and sums are fp32; with bf16 inputs the probabilities are rounded
- * to bf16 as the operand of the product with v.  fp32 inputs and probabilities are multiplied in three bf16 parts (24
+ * queries up to 127 before it as well.  Statistics and sums are fp32; with bf16 inputs the probabilities enter the
+ * product with v rounded to bf16.  fp32 inputs and probabilities are multiplied in three bf16 parts (24
  * bits); values from 3.39e38 on count as infinities there.
  */
 size_t kda_attn_prefill_workspace_bytes(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dtype);
