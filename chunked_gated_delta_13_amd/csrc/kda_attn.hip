@@ -200,8 +200,8 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : KG) void kda_attn_prefill_k
             KDA_LDS T* dst = sK + buf * (2 * TILE) + (Steps::group0(wave) + j) * TileStep<T>::ROWS * 32;
 #pragma unroll
             for (int i = 0; i < Steps::NB; ++i) {
-                lds_dma16(reinterpret_cast<const float*>(kp + pcol + 32 * i), dst + i * kKeys * 32);
-                lds_dma16(reinterpret_cast<const float*>(vp + pcol + 32 * i), dst + TILE + i * kKeys * 32);
+                dma16(kp + pcol + 32 * i, lds_address(dst + i * kKeys * 32));
+                dma16(vp + pcol + 32 * i, lds_address(dst + TILE + i * kKeys * 32));
             }
         }
     };

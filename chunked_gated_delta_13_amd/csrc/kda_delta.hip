@@ -31,13 +31,6 @@ template <> struct DeltaTraits<float> { static constexpr int C = 32, NP = 1; };
 constexpr float kDeadExponent = -126.0f;    // a segment's decay that leaves nothing of its entry state
 constexpr float kLeastExponent = -160.0f;   // 2^-160 of any state is below fp32's range: the same as nothing
 
-// Straight from memory (a uniform base and a lane's offset in bytes) to LDS, 16 bytes a lane, without the compiler's
-// waits (see barrier_all): it would wait for every such request before the next read of LDS.  `lds` is uniform.
-__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_address(const void KDA_LDS* p) { return (uint32_t)(size_t)p; }
-
 // An operand kept as the wave holds it: 8 elements a lane, lane after lane.
 __device__ __forceinline__ void frag_get(Frag<float>& f, const KDA_LDS float* p) {
     frag_join(f, *reinterpret_cast<const KDA_LDS f32x4_t*>(p), *reinterpret_cast<const KDA_LDS f32x4_t*>(p + 4));

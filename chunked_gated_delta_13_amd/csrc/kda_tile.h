@@ -171,6 +171,17 @@ template <typename T, int ROWS> struct TilePut {
     }
 };
 
+// Straight from memory to LDS, 16 bytes a lane, without the compiler's waits: it would have every such request arrive before
+// the next transposed read of LDS.  What is requested is waited for with barrier_all.  `lds` is uniform.  From a uniform
+// base and a lane's offset in bytes, or from a lane's address.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void dma16(const void* at, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void KDA_LDS* p) { return (uint32_t)(size_t)p; }
+
 // The 16-byte piece of its row that a lane fetches when a step goes straight from memory to LDS, lane by
 // lane: the one whose place in the block is the lane's.
 template <typename T> __device__ __forceinline__ int tile_dma_piece(int row, int lane) {
