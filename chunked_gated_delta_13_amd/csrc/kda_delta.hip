@@ -5,7 +5,7 @@
 //
 // Chunks of C tokens.  With c_i the sum of the exponents (base 2) up to token i of the chunk and S0 its entry state:
 //     A_ij = beta_i 2^(c_i - c_j) (k_i . k_j)  for j < i,     T = (I + A)^-1
-//     R = diag(beta) (V - diag(2^c) K S0),     U = T R
+//     R = V - diag(2^c) K S0,     U = T diag(beta) R
 //     O = diag(2^c) Q S0 + B U,                B_ij = 2^(c_i - c_j) (q_i . k_j)  for j <= i
 //     S <- 2^(c_C) S0 + K^T diag(2^(c_C - c_j)) U
 // With one decay per token the differences of exponents are formed directly, never above 0 for decays: nothing has to be
@@ -37,6 +37,28 @@ __device__ __forceinline__ void frag_get(Frag<float>& f, const KDA_LDS float* p)
 }
 __device__ __forceinline__ void frag_get(Frag<__bf16>& f, const KDA_LDS __bf16* p) {
     f.v = *reinterpret_cast<const KDA_LDS bf16x8_t*>(p);
+}
+
+// Four elements in NP parts, the first one largest.
+template <int NP> __device__ __forceinline__ void parts4(bf16x4_t (&o)[NP], f32x4_t v) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const bf16x2_t u = {(__bf16)v[2 * j], (__bf16)v[2 * j + 1]};
+            o[p][2 * j] = u[0];
+            o[p][2 * j + 1] = u[1];
+            if (p + 1 < NP) {
+                uint32_t w = __builtin_bit_cast(uint32_t, u);
+                asm("" : "+v"(w));   // (else either element is rounded once more on its own)
+                v[2 * j] -= __uint_as_float(w << 16);
+                v[2 * j + 1] -= __uint_as_float(w & 0xffff0000u);
+            }
+        }
+}
+template <int NP> __device__ __forceinline__ void parts4(f32x4_t (&o)[NP], f32x4_t v) {
+    static_assert(NP == 1, "fp32 operands are whole");
+    o[0] = v;
 }
 
 // c += a b of two rows of tiles for factors in parts: the products above 2^-24, the smallest first.
@@ -285,7 +307,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             }
             barrier_all();   // (V has arrived, for every wave)
 
-            // 2: R = beta (V - 2^c X) in X's place, then U = T R
+            // 2: R = V - 2^c X in X's place, then U = (T diag(beta)) R
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 Frag<T> v;
@@ -295,9 +317,8 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
                 for (int x = 0; x < 2; ++x) {
                     const int i = q + x * NQ;
                     const f32x4_t grow = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 2 * C + 16 * i + 4 * g);
-                    const f32x4_t beta = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 4 * C + 16 * i + 4 * g);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) X[i][j] = beta[j] * fmaf(-grow[j], X[i][j], v.get(4 * x + j));
+                    for (int j = 0; j < 4; ++j) X[i][j] = fmaf(-grow[j], X[i][j], v.get(4 * x + j));
                 }
             }
             f32x4_t U[NA];
@@ -508,12 +529,14 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
 #pragma unroll
             for (int x = 0; x < 4; ++x) G[x] *= beta * w[x];
             dump(low(i, j), G);
+            return w;
         };
 
         // 1: A by tiles of K K^T.  Wave i forms the inverse of the diagonal one of row i.
-        f32x4_t Dt = zero4();   // T_ii transposed
+        f32x4_t Dt = zero4(), up = zero4(), w1 = zero4(), w2 = zero4();   // T_ii transposed; decays, for A and for B
         if (cw < NA) {
-            const f32x4_t G = product(k_rows, cw, cw), up = decays(cw, cw);
+            const f32x4_t G = product(k_rows, cw, cw);
+            up = decays(cw, cw);
             const float br = arr[4 * C + 16 * cw + r], hj = arr[16 * cw + r], lj = arr[C + 16 * cw + r];
             const f32x4_t hi = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 16 * cw + 4 * g), lo = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + C + 16 * cw + 4 * g);
             const f32x4_t beta = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 4 * C + 16 * cw + 4 * g);
@@ -559,11 +582,11 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             dump(&sh->diag[cw * 256], D);
         }
         if constexpr (NA == 4) {
-            below(cw < 2 ? 3 : (cw == 2 ? 2 : 1), cw == 2 ? 1 : (cw == 1 ? 2 : 0));   // (3,0) (3,2) (2,1) (1,0)
+            w1 = below(cw < 2 ? 3 : (cw == 2 ? 2 : 1), cw == 2 ? 1 : (cw == 1 ? 2 : 0));   // (3,0) (3,2) (2,1) (1,0)
             if (cw == 0) below(2, 0);
-            if (cw == 3) below(3, 1);
+            if (cw == 3) w2 = below(3, 1);
         } else {
-            if (cw == 2) below(1, 0);
+            if (cw == 2) w1 = below(1, 0);
         }
         barrier_lds();
 
@@ -587,33 +610,26 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
         barrier_lds();
 
         // 3: the rest of T, and all of it to the state waves, which have read the last one; B
-        auto put = [&](int i, int j, f32x4_t v) {
+        auto put = [&](int i, int j, f32x4_t v) {   // with beta: U = (T diag(beta)) (V - 2^c X)
+            const f32x4_t beta = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 4 * C + 16 * j + 4 * g);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                typename Vec4<T>::type o;
+            for (int x = 0; x < 4; ++x) v[x] *= beta[x];
+            typename Vec4<T>::type o[NP];
+            parts4<NP>(o, v);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    o[x] = from_f32<T>(v[x]);
-                    v[x] -= to_f32<T>(o[x]);
-                }
-                *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->t[p][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o;
-            }
+            for (int p = 0; p < NP; ++p)
+                *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->t[p][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o[p];
         };
-        auto weights = [&](int i, int j) {   // B_ij
-            const f32x4_t P = product(q_rows, i, j), w = decays(i, j);
+        auto weights = [&](int i, int j, const f32x4_t& w) {   // B_ij, from its decays
+            const f32x4_t P = product(q_rows, i, j);
             f32x4_t e;
 #pragma unroll
             for (int x = 0; x < 4; ++x) e[x] = i == j && 4 * g + x > r ? 0.0f : w[x] * P[x];
+            typename Vec4<T>::type o[OP];
+            parts4<OP>(o, e);
 #pragma unroll
-            for (int p = 0; p < OP; ++p) {
-                typename Vec4<T>::type o;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    o[x] = from_f32<T>(e[x]);
-                    e[x] -= to_f32<T>(o[x]);
-                }
-                *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->b[n & 1][p][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o;
-            }
+            for (int p = 0; p < OP; ++p)
+                *reinterpret_cast<KDA_LDS typename Vec4<T>::type*>(&sh->b[n & 1][p][frag_at(i, j >> 1) * FR + lane * 8 + (j & 1) * 4]) = o[p];
         };
         if (cw < NA) put(cw, cw, Dt);
         if (cw == 1 || (NA == 4 && cw == 3)) {
@@ -621,17 +637,17 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             if constexpr (OUT) {
                 if constexpr (NA == 4) {
                     if (cw == 1) {
-                        weights(0, 0);
-                        weights(1, 0);
-                        weights(1, 1);
-                        weights(2, 0);
+                        weights(0, 0, decays(0, 0));
+                        weights(1, 1, up);
+                        weights(2, 0, decays(2, 0));
+                        weights(3, 2, w1);
                     } else {
-                        weights(2, 1);
-                        weights(2, 2);
-                        weights(3, 3);
+                        weights(1, 0, w1);
+                        weights(3, 1, w2);
+                        weights(3, 3, up);
                     }
                 } else {
-                    weights(1, 0);
+                    weights(1, 1, up);
                 }
             }
             if (cw == 3 && more) put_arr(n + 1);
@@ -646,16 +662,16 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             put(3, cw >> 1, negated(mma16(x1, D3, mma16(x0, T32, zero4()))));
             if constexpr (OUT) {
                 if (cw == 0) {
-                    weights(3, 0);
+                    weights(3, 0, w1);
                 } else {
-                    weights(3, 1);
-                    weights(3, 2);
+                    weights(2, 1, w1);
+                    weights(2, 2, up);
                 }
             }
         } else {
             if constexpr (OUT) {
-                if (cw == 0) weights(0, 0);
-                if (cw == 2) weights(1, 1);
+                if (cw == 0) weights(0, 0, up);
+                if (cw == 2) weights(1, 0, w1);
             }
             if (cw == 3 && more) put_arr(n + 1);
         }
