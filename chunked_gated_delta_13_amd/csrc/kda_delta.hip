@@ -248,6 +248,10 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
 #pragma unroll
                 for (int j = 0; j < 4; ++j) S[t][j] = ident && 16 * t + 4 * g + j == col ? 1.0f : 0.0f;
         }
+        // Waves of one SIMD are served the oldest first: the second state wave of one ended an interval 2000 cycles after the
+        // first.  It goes first, and a chunk wave before either but in interval 3, where it has time (1700 -> 1652 us).
+        if (wave >= 4) __builtin_amdgcn_s_setprio(2);
+        else __builtin_amdgcn_s_setprio(1);
         TileRows<T, C, DK> rk, rq;
         TileCols<T, C> ck, cvt;
         rk.set(sh->k[0], lane);
@@ -426,7 +430,6 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
 
     // ---------------------------------------------------------------------------------------------- chunk waves
     const int cw = wave - NSW;
-    __builtin_amdgcn_s_setprio(3);   // (the state waves wait for these at every barrier otherwise: 5% slower)
     const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * a.k_stride + (long long)hk * DK;
     const T* qp = reinterpret_cast<const T*>(a.q) + tok0 * a.q_stride + (long long)hk * DK;
     static_assert(GROUPS == 4, "a chunk wave has a group of rows");
@@ -532,6 +535,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             return w;
         };
 
+        __builtin_amdgcn_s_setprio(3);
         // 1: A by tiles of K K^T.  Wave i forms the inverse of the diagonal one of row i.
         f32x4_t Dt = zero4(), up = zero4(), w1 = zero4(), w2 = zero4();   // T_ii transposed; decays, for A and for B
         if (cw < NA) {
@@ -609,6 +613,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
         }
         barrier_lds();
 
+        __builtin_amdgcn_s_setprio(0);
         // 3: the rest of T, and all of it to the state waves, which have read the last one; B
         auto put = [&](int i, int j, f32x4_t v) {   // with beta: U = (T diag(beta)) (V - 2^c X)
             const f32x4_t beta = *reinterpret_cast<const KDA_LDS f32x4_t*>(arr + 4 * C + 16 * j + 4 * g);
