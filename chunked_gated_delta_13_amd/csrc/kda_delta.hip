@@ -112,6 +112,10 @@ template <int I> __device__ __forceinline__ f32x4_t quad_lane(const f32x4_t& v) 
 // K has three buffers (chunks c, n and the one in flight), Q, B and the exponents' tables two or three, T and V one: each is
 // overwritten only in an interval after its last reader's.
 //
+// Bound by issue: 4 prompts of 16384 tokens, 56 heads on 28 of 128 in 1655 us, 13900 cycles a chunk; products take 16.7 cycles,
+// two vector instructions beside each are free and further ones take 4, which makes 10400 cycles for a chunk's.  LDS
+// is busy in 35% of the cycles, HBM moves 1.7 TB/s.
+//
 // OUT: outputs are formed (else only states).
 template <typename T, int DK, int NSW, bool OUT>
 __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const DeltaArgs a) {
@@ -755,7 +759,8 @@ __global__ __launch_bounds__(4 * DK) void kda_delta_join_kernel(const float* M, 
 // products.  With p = S^T k and r = S^T q of the old state:
 //     u = beta (v - a p),     S <- a S + k u^T,     o = a r + (k . q) u
 // A workgroup owns one (sequence, head): dv / 4 column groups of four (a state's row is one contiguous run) x 16 row
-// groups, and takes states so that an XCD streams one contiguous range of them.
+// groups, and takes states so that an XCD streams one contiguous range of them.  256 sequences of 56 heads of 128: 304 us, 6.2
+// TB/s, the rate of the best plain read-modify-write.
 template <int DK, int DV, typename T>
 __global__ __launch_bounds__(4 * DV) void kda_delta_step_kernel(const DeltaArgs a) {
     constexpr int NCG = DV / 4, NRG = 16, NW = NCG * NRG / 64, RPT = DK / NRG;
