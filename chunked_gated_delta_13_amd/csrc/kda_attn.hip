@@ -643,7 +643,7 @@ __global__ __launch_bounds__(256) void kda_attn_join_kernel(const AttnArgs a) {
     }
     if (!__any(in)) return;   // (every wave finds the same)
     const long long first = row * a.n_split;
-    join_parts<D, T>(a.ws_ml + 2 * first, a.ws_o + first * D, a.n_split, 1, reinterpret_cast<T*>(a.o) + row * D);
+    join_parts<D, T, 256>(a.ws_ml + 2 * first, a.ws_o + first * D, a.n_split, 1, reinterpret_cast<T*>(a.o) + row * D);
 }
 
 namespace {

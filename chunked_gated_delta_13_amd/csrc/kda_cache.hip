@@ -233,7 +233,7 @@ __device__ __forceinline__ int tiles_per_slot(const AttnStepArgs& a, int lane) {
 // keys are widened straight into the operand (bf16 holds every value), those of values go through a tile of the
 // wave's own in LDS to be transposed.  Queries of fp32 are fed as three bf16 parts, probabilities as two, or three
 // for fp32 outputs: the products take a fifth of the time that the loads do.  64 sequences of 1000 to 16384 tokens, 56 heads
-// on 8 of 128: 87 us and 8 for the join, 4.1 TB/s in all (loads of the same pages alone 88, in order of addresses 69); one
+// on 8 of 128: 87 us and 5 for the join, 4.1 TB/s in all (loads of the same pages alone 88, in order of addresses 69); one
 // of 32777 tokens 12.4 and 4.7 us.
 template <int D, typename T>
 __global__ __launch_bounds__(256, D == 128 && sizeof(T) == 4 ? 3 : 4) void kda_attn_step_kernel(const AttnStepArgs a) {
@@ -499,8 +499,8 @@ __global__ __launch_bounds__(256, D == 128 && sizeof(T) == 4 ? 3 : 4) void kda_a
 }
 
 // Joins the slots of a sequence that has more than one.  grid: (sequence, query, head) rows.
-template <int D, typename T>
-__global__ __launch_bounds__(256) void kda_attn_step_join_kernel(const AttnStepArgs a) {
+template <int D, typename T, int THREADS>
+__global__ __launch_bounds__(THREADS) void kda_attn_step_join_kernel(const AttnStepArgs a) {
     const int lane = threadIdx.x & 63;
     const uint32_t mh = (uint32_t)a.m * (uint32_t)a.H;
     const int b = (int)(blockIdx.x / mh);
@@ -516,7 +516,7 @@ __global__ __launch_bounds__(256) void kda_attn_step_join_kernel(const AttnStepA
     before -= n;
     if (n == 1) return;
     const long long first = (long long)before * mh + place;
-    join_parts<D, T>(a.ws_ml + 2 * first, a.ws_o + first * D, n, mh, reinterpret_cast<T*>(a.o) + (long long)blockIdx.x * D);
+    join_parts<D, T, THREADS>(a.ws_ml + 2 * first, a.ws_o + first * D, n, mh, reinterpret_cast<T*>(a.o) + (long long)blockIdx.x * D);
 }
 
 namespace {
@@ -537,7 +537,11 @@ template <int D, typename T> hipError_t attn_step_t(const AttnStepArgs& a, hipSt
     kda_attn_step_kernel<D, T><<<dim3((unsigned)((long long)a.slots * rt * a.Hkv)), 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.slots == a.N) return e;
-    kda_attn_step_join_kernel<D, T><<<dim3((unsigned)((long long)a.N * a.m * a.H)), 256, 0, s>>>(a);
+    // Four waves a row where its sequence can have many slots (one of 128 of them 4.9 us, 8.9 with one wave), one where rows are
+    // many and slots few (64 sequences 8.3 us with four, 5.0 with one).
+    const dim3 rows((unsigned)((long long)a.N * a.m * a.H));
+    if (a.want >= 8LL * a.N) kda_attn_step_join_kernel<D, T, 256><<<rows, 256, 0, s>>>(a);
+    else kda_attn_step_join_kernel<D, T, 64><<<rows, 64, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -64,11 +64,11 @@ template <typename T> __device__ __forceinline__ void store4(T* p, const f32x4_t
     *reinterpret_cast<vec4*>(p) = o;
 }
 
-// Joins n partial outputs of one row: part i's output lies at o + i step D, its maximum (base 2) and sum at ml + 2 i step.  256
-// threads: D / 4 lanes own four channels of a part, and the 256 / (D / 4) groups take parts side by side.
-template <int D, typename T>
+// Joins n partial outputs of one row: part i's output lies at o + i step D, its maximum (base 2) and sum at ml + 2 i step.  Of
+// the workgroup's threads D / 4 own four channels of a part, and groups of as many take parts side by side.
+template <int D, typename T, int THREADS>
 __device__ __forceinline__ void join_parts(const float* ml, const float* o, int n, long long step, T* out) {
-    constexpr int NL = D / 4, NS = 256 / NL;
+    constexpr int NL = D / 4, NS = THREADS / NL;
     const int tid = threadIdx.x, d = (tid % NL) * 4, i0 = tid / NL;
     o += d;
     // every group keeps a maximum of its own parts
