@@ -372,11 +372,11 @@ kda_status_t kda_conv_step(const void *x, const void *w, const void *bias, void 
  *              (a multiple of 64; >= T = no split).  The result does not depend on it beyond rounding.
  *   workspace  kda_ssm_prefill_workspace_bytes(...) bytes of device memory (may be NULL when that is 0),
  *              written before it is read; calls that overlap in time need one each
- * Rows of x, Bm, Cm and z start on 16-byte boundaries; H * p and the five strides are at most 2^22
- * elements, B * H at most 2^22, and B * H segments of a split sequence at most 2^20.  T == 0 is valid: S_T receives S0 (or zeros).
- * B == 0 or H == 0 is a no-op.  States and exponents are fp32.  With bf16 inputs two operands of the products
- * that form y are rounded to bf16: the state in S^T C, and the weights e^(c_i - c_j) dt_j (C_i . B_j) by
- * which a token takes the inputs of its own block of 64; the state's update rounds neither.
+ * Rows of x, Bm, Cm and z start on 16-byte boundaries; H * p and the five strides are at most 2^22 elements, B * H at
+ * most 2^22, and B * H segments of a split sequence at most 2^20.  T == 0 is valid: S_T receives S0 (or zeros). B ==
+ * 0 or H == 0 is a no-op.  States and exponents are fp32.  With bf16 inputs two operands of the products that form y
+ * are rounded to bf16: the state in S^T C, and the weights e^(c_i - c_j) dt_j (C_i . B_j) by which a token takes the
+ * inputs of its own block of 64; the state's update rounds neither.
  */
 size_t kda_ssm_prefill_workspace_bytes(int B, int T, int H, int G, int n, int p, kda_dtype_t dtype,
                                        int seg_len);
@@ -437,11 +437,11 @@ kda_status_t kda_window_prefill(const void *q, const void *k, const void *v, voi
                                 void *stream);
 
 /*
- * One new token of N sequences over their ring caches: q [N, H, d], k, v [N, Hkv, d], o [N, H, d].
- * pos [N] int32 (DEVICE): tokens of each sequence before this one (negative values count as 0).  N is at
- * most 65535, N H at most 2^23.  The token's k and v are written to their row of the caches and are visible
- * to its own query.  The workspace holds kda_window_step_workspace_bytes(...) bytes (may be NULL when that is
- * 0); calls that overlap in time need one each.  With bf16 inputs a probability enters the product with v as two bf16 parts (16 bits).
+ * One new token of N sequences over their ring caches: q [N, H, d], k, v [N, Hkv, d], o [N, H, d]. pos [N] int32
+ * (DEVICE): tokens of each sequence before this one (negative values count as 0).  N is at most 65535, N H at most
+ * 2^23.  The token's k and v are written to their row of the caches and are visible to its own query.  The workspace
+ * holds kda_window_step_workspace_bytes(...) bytes (may be NULL when that is 0); calls that overlap in time need one
+ * each.  With bf16 inputs a probability enters the product with v as two bf16 parts (16 bits).
  */
 size_t kda_window_step_workspace_bytes(int N, int H, int Hkv, int d, int window, int sinks,
                                        kda_dtype_t dtype);
@@ -473,10 +473,11 @@ kda_status_t kda_window_step(const void *q, const void *k, const void *v, void *
  *              multiply to less than 2^-126.  Other keys need seg_len >= T
  *   workspace  kda_delta_prefill_workspace_bytes(...) bytes of device memory (may be NULL when that is 0), written
  *              before it is read; calls that overlap in time need one each
- * Rows of q, k and v start on 16-byte boundaries; H * dv and the three strides are at most 2^22 elements.  B * H, times
- * the segments of a split, is at most 2^20, T at most 2^30.  T == 0 is valid: S_T receives S0 (or zeros).  B == 0 or
- * H == 0 is a no-op.  A NaN or an infinity may reach the other tokens of its block of 64 and every token after it.  States and exponents are fp32, and with bf16 inputs every factor on the state's path keeps 24
- * bits, every factor of o 16.
+ * Rows of q, k and v start on 16-byte boundaries; H * dv and the three strides are at most 2^22 elements.  B * H,
+ * times the segments of a split, is at most 2^20, T at most 2^30.  T == 0 is valid: S_T receives S0 (or zeros).  B ==
+ * 0 or H == 0 is a no-op.  A NaN or an infinity may reach the other tokens of its block of 64 and every token after
+ * it.  States and exponents are fp32, and with bf16 inputs every factor on the state's path keeps 24 bits, every
+ * factor of o 16.
  */
 size_t kda_delta_prefill_workspace_bytes(int B, int T, int H, int Hk, int dk, int dv, kda_dtype_t dtype,
                                          int seg_len);
@@ -487,8 +488,8 @@ kda_status_t kda_delta_prefill(const void *q, const void *k, const void *v, cons
                                size_t workspace_bytes, void *stream);
 
 /*
- * One token of the gated delta rule for N sequences, S [N, H, dk, dv] updated in place: the same arguments without the
- * time axis (q, k [N, Hk, dk], v, o [N, H, dv], g, beta [N, H]).
+ * One token of the gated delta rule for N sequences, S [N, H, dk, dv] updated in place: the same arguments without
+ * the time axis (q, k [N, Hk, dk], v, o [N, H, dv], g, beta [N, H]).
  */
 kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
                             float *S, void *o, int N, int H, int Hk, int dk, int dv, long long q_stride,
@@ -518,12 +519,12 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
  *   d          64 or 128;  0 < scale <= 2.3e38 (scale log2(e) is finite)
  * Rows of q, k and v start on 16-byte boundaries.  Nq == 0, B == 0 or H == 0 is a no-op.  H is at most 65536, Nk and
  * Nq H / Hkv at most 2^30, (Nq H / Hkv / 64 + B) Hkv at most 2^23.  Few queries over many keys are run as ranges of
- * keys, joined afterwards, when a workspace of kda_attn_prefill_workspace_bytes(...) bytes is given (calls that overlap in
- * time need one each); with NULL they run as one range.  Scores have to lie inside fp32's range: one below it has no
- * weight, a query with none inside it gets zeros, one with a score above it NaN.  A NaN or an infinity in k or v may reach the
- * queries up to 127 before it as well.  Statistics and sums are fp32; with bf16 inputs the probabilities enter the
- * product with v rounded to bf16.  fp32 inputs and probabilities are multiplied in three bf16 parts (24
- * bits); values from 3.39e38 on count as infinities there.
+ * keys, joined afterwards, when a workspace of kda_attn_prefill_workspace_bytes(...) bytes is given (calls that
+ * overlap in time need one each); with NULL they run as one range.  Scores have to lie inside fp32's range: one below
+ * it has no weight, a query with none inside it gets zeros, one with a score above it NaN.  A NaN or an infinity in k
+ * or v may reach the queries up to 127 before it as well.  Statistics and sums are fp32; with bf16 inputs the
+ * probabilities enter the product with v rounded to bf16.  fp32 inputs and probabilities are multiplied in three bf16
+ * parts (24 bits); values from 3.39e38 on count as infinities there.
  */
 size_t kda_attn_prefill_workspace_bytes(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dtype);
 kda_status_t kda_attn_prefill(const void *q, const void *k, const void *v, const int *cu_q, const int *cu_k,
@@ -534,9 +535,10 @@ kda_status_t kda_attn_prefill(const void *q, const void *k, const void *v, const
 /*
  * A paged cache of keys and values in 4 bits an element (open microscaling form): 32 channels of a row share a power
  * of two 2^e, kept as the byte e + 127, and an element is a sign, two bits of exponent and one of fraction: 0, .5, 1,
- * 1.5, 2, 3, 4, 6.  e is the smallest integer from -125 to 95 with max |x| <= 7 2^e (larger elements, from 7 2^95 on, are
- * kept as 6 2^95); elements are rounded to the nearest value, ties to the even fraction.  A block that holds a NaN or an infinity has the byte 255 and reads as NaN.  The
- * bytes 0, 1 and 223 to 254, which are never written, have no meaning.
+ * 1.5, 2, 3, 4, 6.  e is the smallest integer from -125 to 95 with max |x| <= 7 2^e (larger elements, from 7 2^95 on,
+ * are kept as 6 2^95); elements are rounded to the nearest value, ties to the even fraction.  A block that holds a
+ * NaN or an infinity has the byte 255 and reads as NaN.  The bytes 0, 1 and 223 to 254, which are never written, have
+ * no meaning.
  *
  *   k_cache, v_cache  [n_pages, Hkv, page (d / 2 + d / 32)] bytes   a page of one kv head: `page` rows of d / 2 bytes of
  *                     elements (even channels in the low halves), then `page` rows of d / 32 exponents
@@ -552,7 +554,8 @@ kda_status_t kda_attn_prefill(const void *q, const void *k, const void *v, const
  *   cu         [B + 1] int32 DEVICE      rows of sequence b, as cu_q above; NULL: one token each (N == B)
  *   start      [B] int32 DEVICE or NULL (0)  position of each sequence's first token (negative values count as 0)
  * Tokens past the table, on an entry outside the pool, or outside the sequences are not written.  No two tokens of a
- * call may share a place: which of them it then holds is open, byte by byte.  N Hkv is at most 2^27, Hkv at most 65535.
+ * call may share a place: which of them it then holds is open, byte by byte.  N Hkv is at most 2^27, Hkv at most
+ * 65535.
  */
 kda_status_t kda_cache_write(const void *k, const void *v, void *k_cache, void *v_cache, const int *pages,
                              const int *cu, const int *start, int B, int N, int Hkv, int d, int n_pages,
@@ -560,8 +563,8 @@ kda_status_t kda_cache_write(const void *k, const void *v, void *k_cache, void *
                              kda_dtype_t dtype, void *stream);
 
 /*
- * Reads N packed rows back: k, v [N, Hkv, d] dtype (out), exact in either type.  The other arguments are as for writing;
- * a position without a page is zeros, a row outside the sequences is left as it was.
+ * Reads N packed rows back: k, v [N, Hkv, d] dtype (out), exact in either type.  The other arguments are as for
+ * writing; a position without a page is zeros, a row outside the sequences is left as it was.
  */
 kda_status_t kda_cache_read(const void *k_cache, const void *v_cache, const int *pages, const int *cu,
                             const int *start, void *k, void *v, int B, int N, int Hkv, int d, int n_pages,
@@ -577,11 +580,12 @@ kda_status_t kda_cache_read(const void *k_cache, const void *v_cache, const int 
  *   o          [N, m, H, d] dtype  (out)
  *   workspace  kda_attn_step_workspace_bytes(...) bytes of device memory (may be NULL when that is 0), written before
  *              it is read; calls that overlap in time need one each
- * Rows whose table entry lies outside the pool are not seen; n_pages is at least 1.  N == 0, m == 0 or H == 0 is a no-op.
- * N m H is at most 2^23, the tokens that all tables hold, N max_pages page / 128 + N, at most 2^30, and N ceil(m H / Hkv / 16) Hkv at most
- * about 2^23.  Scores have to lie inside fp32's range, as above.  A NaN in a row that a later one of the m queries sees
- * reaches the earlier ones too.  Statistics and sums are fp32, every cached value is exact, and a probability enters the
- * product with v as two bf16 parts (16 bits; three, 24 bits, for fp32 outputs).
+ * Rows whose table entry lies outside the pool are not seen; n_pages is at least 1.  N == 0, m == 0 or H == 0 is a
+ * no-op. N m H is at most 2^23, the tokens that all tables hold, N max_pages page / 128 + N, at most 2^30, and N
+ * ceil(m H / Hkv / 16) Hkv at most about 2^23.  Scores have to lie inside fp32's range, as above.  A NaN in a row
+ * that a later one of the m queries sees reaches the earlier ones too.  Statistics and sums are fp32, every cached
+ * value is exact, and a probability enters the product with v as two bf16 parts (16 bits; three, 24 bits, for fp32
+ * outputs).
  */
 size_t kda_attn_step_workspace_bytes(int N, int m, int H, int Hkv, int d, int max_pages, int page,
                                      kda_dtype_t dtype);
