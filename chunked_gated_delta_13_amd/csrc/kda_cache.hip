@@ -33,6 +33,10 @@ __device__ __forceinline__ void widen8(bf16x8_t& v, uint32_t c, float s) {
     v = bf16x8_t{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
+// Eight elements of a row as they lie in memory (16 bytes are aligned).
+template <typename T> struct Eight { typedef bf16x8_t type; };
+template <> struct Eight<float> { typedef __attribute__((ext_vector_type(8), aligned(16))) float type; };
+
 __device__ __forceinline__ void load8(float (&x)[8], const __bf16* p) {
     const bf16x8_t v = *reinterpret_cast<const bf16x8_t*>(p);
 #pragma unroll
@@ -153,8 +157,18 @@ __global__ __launch_bounds__(256) void kda_cache_rows_kernel(const CacheArgs a) 
     if (unit >= (uint32_t)a.n_units) return;
     const int lane = threadIdx.x & 63, c = threadIdx.x % LPR, hk = (int)(unit % (uint32_t)a.Hkv);
     const int i0 = (int)(unit / (uint32_t)a.Hkv) * TB, i = i0 + threadIdx.x / LPR;
-    const int b0 = ended_before(a, i0, lane);
     const bool there = i < a.N;
+    // Rows are requested before their places are looked up, four loads one after the other (48000 tokens, 8 heads: 59 -> 56 us,
+    // where a plain sum over the same rows takes 63; two or four tokens a thread are no faster).
+    typedef typename Eight<T>::type eight_t;
+    eight_t xs = {}, ys = {};
+    if constexpr (WRITE) {
+        if (there) {
+            xs = *reinterpret_cast<const eight_t*>(reinterpret_cast<const T*>(a.k) + (long long)i * a.k_stride + (long long)hk * D + 8 * c);
+            ys = *reinterpret_cast<const eight_t*>(reinterpret_cast<const T*>(a.v) + (long long)i * a.v_stride + (long long)hk * D + 8 * c);
+        }
+    }
+    const int b0 = ended_before(a, i0, lane);
     long long page = 0;
     int row = 0;
     bool inside = false, has = false;
@@ -163,10 +177,13 @@ __global__ __launch_bounds__(256) void kda_cache_rows_kernel(const CacheArgs a) 
     const long long at = base + (long long)row * (D / 2) + 4 * c;
     const long long at_e = base + (long long)a.page * (D / 2) + (long long)row * (D / 32) + c / 4;
     if constexpr (WRITE) {
-        float x[8], y[8];
         if (has) {   // (the four lanes of a quad hold one block, and have a place or none together)
-            load8(x, reinterpret_cast<const T*>(a.k) + (long long)i * a.k_stride + (long long)hk * D + 8 * c);
-            load8(y, reinterpret_cast<const T*>(a.v) + (long long)i * a.v_stride + (long long)hk * D + 8 * c);
+            float x[8], y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = (float)xs[j];
+                y[j] = (float)ys[j];
+            }
             uint32_t ex, ey;
             const uint32_t cx = narrow8(x, &ex), cy = narrow8(y, &ey);
             *reinterpret_cast<uint32_t*>(a.k_cache + at) = cx;
