@@ -46,11 +46,12 @@ template <int NP> __device__ __forceinline__ void parts4(bf16x4_t (&o)[NP], f32x
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const bf16x2_t u = {(__bf16)v[2 * j], (__bf16)v[2 * j + 1]};
-            o[p][2 * j] = u[0];
-            o[p][2 * j + 1] = u[1];
+            uint32_t w = __builtin_bit_cast(uint32_t, u);
+            if (p + 1 < NP) asm("" : "+v"(w));   // (as in parts_of)
+            const bf16x2_t y = __builtin_bit_cast(bf16x2_t, w);
+            o[p][2 * j] = y[0];
+            o[p][2 * j + 1] = y[1];
             if (p + 1 < NP) {
-                uint32_t w = __builtin_bit_cast(uint32_t, u);
-                asm("" : "+v"(w));   // (else either element is rounded once more on its own)
                 v[2 * j] -= __uint_as_float(w << 16);
                 v[2 * j + 1] -= __uint_as_float(w & 0xffff0000u);
             }

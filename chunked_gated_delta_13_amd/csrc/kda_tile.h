@@ -210,11 +210,12 @@ template <int NP> __device__ __forceinline__ void parts_of(Frag<__bf16> (&f)[NP]
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bf16x2_t u = {(__bf16)x[2 * j], (__bf16)x[2 * j + 1]};
-            f[p].v[2 * j] = u[0];
-            f[p].v[2 * j + 1] = u[1];
+            uint32_t w = __builtin_bit_cast(uint32_t, u);
+            if (p + 1 < NP) asm("" : "+v"(w));   // (else either element is rounded once more on its own; what is kept is w, or it is copied)
+            const bf16x2_t v = __builtin_bit_cast(bf16x2_t, w);
+            f[p].v[2 * j] = v[0];
+            f[p].v[2 * j + 1] = v[1];
             if (p + 1 < NP) {
-                uint32_t w = __builtin_bit_cast(uint32_t, u);
-                asm("" : "+v"(w));   // (else either element is rounded once more on its own)
                 x[2 * j] -= __uint_as_float(w << 16);
                 x[2 * j + 1] -= __uint_as_float(w & 0xffff0000u);
             }
