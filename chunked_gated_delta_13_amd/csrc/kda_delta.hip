@@ -113,8 +113,8 @@ template <int I> __device__ __forceinline__ f32x4_t quad_lane(const f32x4_t& v) 
 // K has three buffers (chunks c, n and the one in flight), Q, B and the exponents' tables two or three, T and V one: each is
 // overwritten only in an interval after its last reader's.
 //
-// Bound by issue: 4 prompts of 16384 tokens, 56 heads on 28 of 128 in 1655 us, 13900 cycles a chunk; products take 16.7 cycles,
-// two vector instructions beside each are free and further ones take 4, which makes 10400 cycles for a chunk's.  LDS
+// Bound by issue: 4 prompts of 16384 tokens, 56 heads on 28 of 128 in 1620 us, 13500 cycles a chunk; products take 16.7 cycles,
+// two vector instructions beside each are free and further ones take 4, which makes 10000 cycles for a chunk's.  LDS
 // is busy in 35% of the cycles, HBM moves 1.7 TB/s.
 //
 // OUT: outputs are formed (else only states).
@@ -183,13 +183,15 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
 
     if constexpr (!OUT) {
         // Where the decays from some chunk to the segment's end together leave less than 2^-126 of a state, nothing before
-        // that chunk matters (as long as no token's transition expands: beta |k|^2 at most 2): the state from zero is run from there, and the transition is dead (marked, not formed).  Sums of
-        // 64 chunks at a time from the end backwards, 8 or 16 of them a wave.
+        // that chunk matters (as long as no token's transition expands: beta |k|^2 at most 2): the state from zero is run from
+        // there, and the transition is dead (marked, not formed).  Sums of 64 chunks at a time from the end backwards, 8 or 16 of
+        // them a wave.  A few short segments are not looked at: forming all transitions, each on a compute unit of its own, takes
+        // less than that (3 prompts of 301 tokens in segments of two chunks 32.8 -> 30.3 us).
         constexpr int NW = NSW + 4;
         KDA_LDS float* sums = &sh->low[0];
         bool dead = false;
         float total = 0.0f;
-        for (int last = nc; last > 0 && !dead; last -= 64) {
+        for (int last = nc <= 4 && a.n_seg_launch < 8 ? 0 : nc; last > 0 && !dead; last -= 64) {
             for (int i = wave; i < 64; i += NW) {
                 const int c = last - 1 - i, at = c * C + lane;
                 float e = 0.0f;
