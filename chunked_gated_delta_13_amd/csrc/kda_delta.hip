@@ -102,8 +102,13 @@ template <int I> __device__ __forceinline__ f32x4_t quad_lane(const f32x4_t& v) 
 
 }  // namespace
 
+// Chunk waves: eight beside four state waves in bf16, of which four form the inverses and T, the others A's other blocks and B: a
+// lone wave of a SIMD issues an instruction every eight cycles at best (16 heads of 128, one chunk 12.9 -> 11.7 us, ten 49.8 ->
+// 47.4; in fp32, whose products take longer, 31.1 and 31.8 for 3 prompts of 301 tokens).
+template <typename T> constexpr int chunk_waves(int nsw) { return nsw == 4 && sizeof(T) == 2 ? 8 : 4; }
+
 // Prompt.  A workgroup runs one (sequence, head, segment, slice of 16 NSW state columns) with two roles: NSW state
-// waves hold the slice (16 columns each, fp32, in the accumulators' layout) and run chunk c; four chunk waves
+// waves hold the slice (16 columns each, fp32, in the accumulators' layout) and run chunk c; the chunk waves
 // prepare what chunk c + 1 needs and does not depend on the state.  With eight state waves a SIMD hosts two of them and a
 // chunk wave.  Three workgroup barriers a chunk:
 //     interval   state waves, chunk c             chunk waves, chunk n = c + 1
@@ -119,7 +124,7 @@ template <int I> __device__ __forceinline__ f32x4_t quad_lane(const f32x4_t& v) 
 //
 // OUT: outputs are formed (else only states).
 template <typename T, int DK, int NSW, bool OUT>
-__global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const DeltaArgs a) {
+__global__ __launch_bounds__(64 * (NSW + chunk_waves<T>(NSW))) void kda_delta_prefill_kernel(const DeltaArgs a) {
     constexpr int C = DeltaTraits<T>::C, NP = DeltaTraits<T>::NP, NA = C / 16, NQ = C / 32;   // token tiles, pairs of them
     constexpr int NT = DK / 16, NKB = DK / 32, DVS = 16 * NSW;
     constexpr int KT = C * DK, VT = C * DVS;                     // elements of a tile
@@ -128,6 +133,8 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
     constexpr int ARR = 5 * C + 16;                              // exponents (high, low parts), 2^c, 2^(c_C - c), beta, 2^c_C
     constexpr int NLOW = NA * (NA - 1) / 2;
     constexpr int OP = NP > 1 ? 2 : 1;                           // parts of a factor of the outputs
+    constexpr int NCW = chunk_waves<T>(NSW), CS = NCW / 4;       // chunk waves; those that share a group of rows
+    static_assert(NCW == 4 || NA == 4, "eight chunk waves share four rows of blocks");
     struct Shared {
         T k[3][KT], q[OUT ? 2 : 1][KT], v[VT];
         T t[NP][NF * FR], b[2][OP][OUT ? NF * FR : 8];
@@ -187,7 +194,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
         // there, and the transition is dead (marked, not formed).  Sums of 64 chunks at a time from the end backwards, 8 or 16 of
         // them a wave.  A few short segments are not looked at: forming all transitions, each on a compute unit of its own, takes
         // less than that (3 prompts of 301 tokens in segments of two chunks 32.8 -> 30.3 us).
-        constexpr int NW = NSW + 4;
+        constexpr int NW = NSW + NCW;
         KDA_LDS float* sums = &sh->low[0];
         bool dead = false;
         float total = 0.0f;
@@ -439,19 +446,20 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
     const int cw = wave - NSW;
     const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * a.k_stride + (long long)hk * DK;
     const T* qp = reinterpret_cast<const T*>(a.q) + tok0 * a.q_stride + (long long)hk * DK;
-    static_assert(GROUPS == 4, "a chunk wave has a group of rows");
-    const uint32_t k_off = lane_off(a.k_stride, cw, C), q_off = lane_off(a.q_stride, cw, C);
+    static_assert(GROUPS == 4 && NKB % CS == 0, "chunk waves share groups of rows");
+    const int rows_of = cw & 3, block0 = (cw >> 2) * (NKB / CS);
+    const uint32_t k_off = lane_off(a.k_stride, rows_of, C), q_off = lane_off(a.q_stride, rows_of, C);
     auto fetch_kq = [&](int chunk) {
         const int left = todo - chunk * C;
-        const uint32_t ko = left >= C ? k_off : lane_off(a.k_stride, cw, left - 1);
+        const uint32_t ko = left >= C ? k_off : lane_off(a.k_stride, rows_of, left - 1);
         const T* base = kp + (long long)chunk * C * a.k_stride;
 #pragma unroll
-        for (int i = 0; i < NKB; ++i) fetch(base, ko, sh->k[chunk % 3], cw, i);
+        for (int i = 0; i < NKB / CS; ++i) fetch(base, ko, sh->k[chunk % 3], rows_of, block0 + i);
         if constexpr (OUT) {
-            const uint32_t qo = left >= C ? q_off : lane_off(a.q_stride, cw, left - 1);
+            const uint32_t qo = left >= C ? q_off : lane_off(a.q_stride, rows_of, left - 1);
             base = qp + (long long)chunk * C * a.q_stride;
 #pragma unroll
-            for (int i = 0; i < NKB; ++i) fetch(base, qo, sh->q[chunk & 1], cw, i);
+            for (int i = 0; i < NKB / CS; ++i) fetch(base, qo, sh->q[chunk & 1], rows_of, block0 + i);
         }
     };
     // exponents and beta of a chunk's tokens, one a lane (the last wave)
@@ -489,19 +497,19 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
 
     if (nc > 0) {
         fetch_kq(first);
-        if (cw == 3) {
+        if (cw == NCW - 1) {
             request_arr(first);
             put_arr(first);
         }
         // the halves of operands that lie above the diagonal stay zero
-        for (int i = tid - 64 * NSW; i < NP * NF * FR; i += 256) (&sh->t[0][0])[i] = (T)0.0f;
+        for (int i = tid - 64 * NSW; i < NP * NF * FR; i += 64 * NCW) (&sh->t[0][0])[i] = (T)0.0f;
         if constexpr (OUT)
-            for (int i = tid - 64 * NSW; i < 2 * OP * NF * FR; i += 256) (&sh->b[0][0][0])[i] = (T)0.0f;
+            for (int i = tid - 64 * NSW; i < 2 * OP * NF * FR; i += 64 * NCW) (&sh->b[0][0][0])[i] = (T)0.0f;
     }
     barrier_all();
     for (int n = first; n < nc; ++n) {
         const bool more = n + 1 < nc;
-        if (cw == 3 && more) request_arr(n + 1);
+        if (cw == NCW - 1 && more) request_arr(n + 1);
         const KDA_LDS float* arr = &sh->arr[n % 3][0];
         const TileRows<T, C, DK> k_rows = rk.at_delta((n % 3) * KT);
         const TileRows<T, C, DK> q_rows = rq.at_delta((OUT ? n & 1 : 0) * KT);
@@ -592,7 +600,12 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             }
             dump(&sh->diag[cw * 256], D);
         }
-        if constexpr (NA == 4) {
+        if constexpr (NCW == 8) {
+            const int x = cw - 4;
+            if (x >= 0) w1 = below(x < 2 ? 3 : (x == 2 ? 2 : 1), x == 2 ? 1 : (x == 1 ? 2 : 0));   // (3,0) (3,2) (2,1) (1,0)
+            if (x == 0) w2 = below(2, 0);
+            if (x == 3) w2 = below(3, 1);
+        } else if constexpr (NA == 4) {
             w1 = below(cw < 2 ? 3 : (cw == 2 ? 2 : 1), cw == 2 ? 1 : (cw == 1 ? 2 : 0));   // (3,0) (3,2) (2,1) (1,0)
             if (cw == 0) below(2, 0);
             if (cw == 3) w2 = below(3, 1);
@@ -613,7 +626,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
                 if (cw == 1) dump(&sh->pair[0], negated(mma16(Dt, Q, zero4())));   // T_10
                 else dump(&sh->pair[256], x0);
             }
-        } else if (NA == 4) {   // A_2x T_xx, A_3x T_xx for x = cw / 2
+        } else if (NA == 4 && cw < 4) {   // A_2x T_xx, A_3x T_xx for x = cw / 2
             const f32x4_t D = dumped(&sh->diag[(cw >> 1) * 256]);
             x0 = mma16(dumped(low(2, cw >> 1)), D, zero4());
             x1 = mma16(dumped(low(3, cw >> 1)), D, zero4());
@@ -646,24 +659,7 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
         if (cw < NA) put(cw, cw, Dt);
         if (cw == 1 || (NA == 4 && cw == 3)) {
             put(cw, cw - 1, x0);
-            if constexpr (OUT) {
-                if constexpr (NA == 4) {
-                    if (cw == 1) {
-                        weights(0, 0, decays(0, 0));
-                        weights(1, 1, up);
-                        weights(2, 0, decays(2, 0));
-                        weights(3, 2, w1);
-                    } else {
-                        weights(1, 0, w1);
-                        weights(3, 1, w2);
-                        weights(3, 3, up);
-                    }
-                } else {
-                    weights(1, 1, up);
-                }
-            }
-            if (cw == 3 && more) put_arr(n + 1);
-        } else if constexpr (NA == 4) {
+        } else if (NA == 4 && cw < 4) {
             if (cw == 0) {
                 const f32x4_t T10 = dumped(&sh->pair[0]);
                 x0 = mma16(dumped(low(2, 1)), T10, x0);
@@ -672,21 +668,46 @@ __global__ __launch_bounds__(64 * NSW + 256) void kda_delta_prefill_kernel(const
             const f32x4_t D2 = dumped(&sh->rows[2 * 256]), D3 = dumped(&sh->rows[3 * 256]), T32 = dumped(&sh->pair[256]);
             put(2, cw >> 1, negated(mma16(x0, D2, zero4())));
             put(3, cw >> 1, negated(mma16(x1, D3, mma16(x0, T32, zero4()))));
-            if constexpr (OUT) {
+        }
+        if constexpr (OUT) {   // B, from the decays at hand where a wave has formed them
+            if constexpr (NCW == 8) {
+                if (cw == 4) {
+                    weights(3, 0, w1);
+                    weights(2, 0, w2);
+                    weights(0, 0, decays(0, 0));
+                } else if (cw == 5) {
+                    weights(3, 2, w1);
+                    weights(1, 1, decays(1, 1));
+                    weights(3, 3, decays(3, 3));
+                } else if (cw == 6) {
+                    weights(2, 1, w1);
+                    weights(2, 2, decays(2, 2));
+                } else if (cw == 7) {
+                    weights(1, 0, w1);
+                    weights(3, 1, w2);
+                }
+            } else if constexpr (NA == 4) {
                 if (cw == 0) {
                     weights(3, 0, w1);
-                } else {
+                } else if (cw == 1) {
+                    weights(0, 0, decays(0, 0));
+                    weights(1, 1, up);
+                    weights(2, 0, decays(2, 0));
+                    weights(3, 2, w1);
+                } else if (cw == 2) {
                     weights(2, 1, w1);
                     weights(2, 2, up);
+                } else {
+                    weights(1, 0, w1);
+                    weights(3, 1, w2);
+                    weights(3, 3, up);
                 }
-            }
-        } else {
-            if constexpr (OUT) {
-                if (cw == 0) weights(0, 0, up);
+            } else {
+                if (cw < 2) weights(cw, cw, up);
                 if (cw == 2) weights(1, 0, w1);
             }
-            if (cw == 3 && more) put_arr(n + 1);
         }
+        if (cw == NCW - 1 && more) put_arr(n + 1);
         barrier_all();   // (K and Q of n + 1 have arrived)
     }
     if (nc > 0) {
@@ -855,7 +876,7 @@ template <typename T, int DK, int NSW, bool OUT> hipError_t run_chunks(DeltaArgs
     a.n_units = (long long)a.BH * a.n_seg_launch * (a.slices + a.id_slices);
     a.per_xcd = (a.n_units + 7) / 8;
     if (a.n_units > (1LL << 22)) return hipErrorInvalidValue;
-    kda_delta_prefill_kernel<T, DK, NSW, OUT><<<dim3((unsigned)(8 * a.per_xcd)), 64 * NSW + 256, 0, s>>>(a);
+    kda_delta_prefill_kernel<T, DK, NSW, OUT><<<dim3((unsigned)(8 * a.per_xcd)), 64 * (NSW + chunk_waves<T>(NSW)), 0, s>>>(a);
     return hipGetLastError();
 }
 template <typename T, int DK> hipError_t prefill_t(bool out, int width, const DeltaArgs& a, hipStream_t s) {
