@@ -56,6 +56,8 @@ CASES = [
     ([2] * 130 + [90], None, 16, 2, 64, "bf16", 0, 0),
     ([200, 250], None, 56, 8, 128, "bf16", 0, 0),                # 64 rows a workgroup, one group of waves
     ([200, 20, 230], [210, 20, 900], 28, 4, 64, "bf16", 0, 2),
+    ([130, 70], None, 24, 12, 64, "bf16", 0, 0),                 # kv heads in sets of four, and of eight
+    ([90, 40, 3], None, 16, 16, 128, "f32", 0, 1),
 ]
 
 

@@ -199,6 +199,8 @@ STEPS = [
     ([5000, 64], 2, 8, 2, 128, 128, "bf16"),
     ([30 + 3 * i for i in range(70)], 1, 2, 1, 64, 16, "bf16"),  # more sequences than lanes of a wave
     ([40, 90], 9, 8, 2, 64, 32, "f32"),                          # 36 rows: three matrix tiles
+    ([900 + 7 * i for i in range(40)], 1, 16, 8, 64, 32, "bf16"),   # a few slots each, joined by one wave a row
+    ([500 + 11 * i for i in range(30)], 2, 12, 6, 128, 16, "f32"),
 ]
 
 
