@@ -99,18 +99,21 @@ __device__ __forceinline__ uint32_t narrow8(const float (&x)[8], uint32_t* byte)
 }
 
 // The place of packed token i in the cache, in rows of one head's page: false where it has none.  b0 is a
-// sequence at or before the token's.
+// sequence at or before the token's.  Ends outside the tensor are clamped: 0 <= i < N, so only a first row below 0
+// has to be seen to.
 __device__ __forceinline__ bool place_of(const CacheArgs& a, int i, int b0, long long* page, int* row, bool* inside) {
     int b = b0;
     long long pos = 0;
     *inside = true;
     if (a.cu) {
         while (b < a.B && a.cu[b + 1] <= i) ++b;
-        if (b >= a.B || i < a.cu[b]) {
+        int first = b < a.B ? a.cu[b] : i + 1;
+        if (first < 0) first = 0;
+        if (i < first) {
             *inside = false;
             return false;
         }
-        pos = i - a.cu[b];
+        pos = i - first;
     } else {
         b = i;
     }
