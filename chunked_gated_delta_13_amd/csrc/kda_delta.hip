@@ -28,7 +28,8 @@ template <typename T> struct DeltaTraits;
 template <> struct DeltaTraits<__bf16> { static constexpr int C = 64, NP = 3; };
 template <> struct DeltaTraits<float> { static constexpr int C = 32, NP = 1; };
 
-constexpr float kDeadExponent = -126.0f;    // a segment's decay that leaves nothing of its entry state
+constexpr float kDeadExponent = -126.0f;    // a segment's transition that leaves nothing of its entry state
+constexpr float kDeadSlack = 2.0f;          // what decays leave for updates that expand a little
 constexpr float kLeastExponent = -160.0f;   // 2^-160 of any state is below fp32's range: the same as nothing
 
 // An operand kept as the wave holds it: 8 elements a lane, lane after lane.
@@ -189,11 +190,14 @@ __global__ __launch_bounds__(64 * (NSW + chunk_waves<T>(NSW))) void kda_delta_pr
     const long long tok0 = (long long)b * a.T + begin;
 
     if constexpr (!OUT) {
-        // Where the decays from some chunk to the segment's end together leave less than 2^-126 of a state, nothing before
-        // that chunk matters (as long as no token's transition expands: beta |k|^2 at most 2): the state from zero is run from
-        // there, and the transition is dead (marked, not formed).  Sums of 64 chunks at a time from the end backwards, 8 or 16 of
-        // them a wave.  A few short segments are not looked at: forming all transitions, each on a compute unit of its own, takes
-        // less than that (3 prompts of 301 tokens in segments of two chunks 32.8 -> 30.3 us).
+        // Where the transitions from some chunk to the segment's end together leave less than 2^-126 of a state, nothing before
+        // that chunk matters: the state from zero is run from there, and the transition is dead (marked, not formed).  A token's
+        // transition a (I - beta k k^T) has the norm a max(1, |1 - beta |k|^2|).  The chunk is found by the decays (sums of 64
+        // chunks at a time from the end backwards, 8 or 16 of them a wave); then what all of the segment's updates expand, where
+        // beta |k|^2 passes 2 or is negative, is added, and if that is too much the whole segment and its transition are
+        // formed (20001 tokens, 16 heads 353 -> 363 us; by the decays alone expanding updates lost what they had kept).  A few short
+        // segments are not looked at: forming all transitions, each on a compute unit of its own, takes less than that (3 prompts of
+        // 301 tokens in segments of two chunks 32.8 -> 30.3 us).
         constexpr int NW = NSW + NCW;
         KDA_LDS float* sums = &sh->low[0];
         bool dead = false;
@@ -216,13 +220,50 @@ __global__ __launch_bounds__(64 * (NSW + chunk_waves<T>(NSW))) void kda_delta_pr
                 if (lane >= x) e += y;
             }
             e += total;
-            const unsigned long long past = __ballot(e <= kDeadExponent);
+            const unsigned long long past = __ballot(e <= kDeadExponent - kDeadSlack);
             if (past) {
                 dead = true;
                 first = last - 1 - __builtin_ctzll(past);
             }
-            total = __shfl(e, 63);
+            total = __shfl(e, past ? __builtin_ctzll(past) : 63);
             barrier_lds();
+        }
+        if (dead) {
+            constexpr int LE = 16 / (int)sizeof(T), LR = DK / LE, RL = 64 / LR, NL = C / RL;   // elements of a lane, lanes of a row, rows
+            typedef __attribute__((ext_vector_type(LE))) T piece_t;                            // of a load, loads of a chunk
+            const T* kr = reinterpret_cast<const T*>(a.k) + tok0 * a.k_stride + (long long)hk * DK + (lane % LR) * LE;
+            float more = 0.0f;
+            for (int c = wave; c < nc; c += NW) {
+                piece_t x[NL];
+                float beta[NL];
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {   // (rows past the unit's: the last one again, without a weight)
+                    const int row = c * C + i * RL + lane / LR, at = row < todo ? row : todo - 1;
+                    x[i] = *reinterpret_cast<const piece_t*>(kr + at * a.k_stride);
+                    beta[i] = a.beta[(tok0 + at) * a.H + h];
+                }
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    float n = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < LE; ++j) n = fmaf((float)x[i][j], (float)x[i][j], n);
+#pragma unroll
+                    for (int s = 1; s < LR; s <<= 1) n += __shfl_xor(n, s);
+                    const float f = fabsf(fmaf(-beta[i], n, 1.0f));
+                    // (base 2; a NaN kills nothing either)
+                    if (c * C + i * RL + lane / LR < todo && !(f <= 1.0f)) more += __builtin_amdgcn_logf(f);
+                }
+            }
+#pragma unroll
+            for (int x = LR; x < 64; x <<= 1) more += __shfl_xor(more, x);
+            if (lane == 0) sums[wave] = more;
+            barrier_lds();
+#pragma unroll
+            for (int i = 0; i < NW; ++i) total += sums[i];
+            if (!__all(total <= kDeadExponent)) {   // (the same in every lane)
+                dead = false;
+                first = 0;
+            }
         }
         if (ident) {
             if (slice == 0 && tid == 0) a.dead[bh * a.m_bh + seg] = dead ? 1 : 0;

@@ -223,8 +223,8 @@ def delta_prefill(q, k, v, g, beta, S0=None, *, lens=None, seg_len=0, o=None, S_
     (S_T may be S0; None when return_state is False).  As in chunk_prefill, q and k are taken as they are (callers
     normalise and scale them), and beta too.  ``lens`` (int32 [B]) gives the tokens of each sequence of a padded batch; rows of o behind
     them are left as they were.  ``seg_len`` forces the tokens per segment of the sequence split (a multiple of 64; 0 = the
-    library's choice).  A split forgets what lies behind decays of less than 2^-126 together, which is right as long as
-    no update expands (beta |k|^2 at most 2); for other keys give seg_len >= T.
+    library's choice).  The result does not depend on it beyond rounding: a split takes as forgotten only what the transitions
+    behind it, e^g max(1, |1 - beta |k|^2|) each, have shrunk to less than 2^-126.
     """
     return (_native or _load()).delta_prefill(q, k, v, g, beta, S0, lens, seg_len, o, S_T, return_state, workspace)
 

@@ -468,9 +468,9 @@ kda_status_t kda_window_step(const void *q, const void *k, const void *v, void *
  *   S_T        [B, H, dk, dv] fp32 or NULL  (out)  state after each sequence's last token; may be S0
  *   dk, dv     64 or 128 each
  *   seg_len    0: the library splits the sequence where that fills the GPU; else tokens per segment (a multiple of 64;
- *              >= T = no split).  The result does not depend on it beyond rounding as long as no update expands (beta |k|^2 at
- *              most 2): a split takes what lies before a token as forgotten if the decays from it to the end of its segment
- *              multiply to less than 2^-126.  Other keys need seg_len >= T
+ *              >= T = no split).  The result does not depend on it beyond rounding: a split takes what lies before a
+ *              token as forgotten only where the norms of the transitions from it to the end of its segment, e^g max(1, |1 -
+ *              beta |k|^2|) each, multiply to less than 2^-126
  *   workspace  kda_delta_prefill_workspace_bytes(...) bytes of device memory (may be NULL when that is 0), written
  *              before it is read; calls that overlap in time need one each
  * Rows of q, k and v start on 16-byte boundaries; H * dv and the three strides are at most 2^22 elements.  B * H,
