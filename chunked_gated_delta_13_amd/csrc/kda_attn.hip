@@ -403,9 +403,9 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : KG) void kda_attn_prefill_k
 }
 
 // fp32.  The matrix cores multiply bf16 at sixteen times the rate of fp32, so every operand is taken in three bf16 parts
-// (x = h + m + l to 2^-24 of x) and of a product of two operands the six largest products of parts, from h h down to l h, m m
-// and h l: what is left out is below 2^-23 of it.  A wave's queries are split once; keys and values once per workgroup
-// and tile, on their way from registers to LDS.
+// (x = h + m + l to 2^-24 of x, or to 2^-126, where bf16's normal numbers end) and of a product of two operands the six
+// largest products of parts, from h h down to l h, m m and h l: what is left out is below 2^-23 of it.  A wave's queries
+// are split once; keys and values once per workgroup and tile, on their way from registers to LDS.
 //
 // Eight waves run 64 rows: 16 rows each, waves 4 to 7 the same rows as 0 to 3 over the other half of each tile's keys, so
 // that a long prompt's chain of tiles is half as long; the halves are joined at the end.  A tile takes two phases: the values

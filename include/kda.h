@@ -524,7 +524,8 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
  * it has no weight, a query with none inside it gets zeros, one with a score above it NaN.  A NaN or an infinity in k
  * or v may reach the queries up to 127 before it as well.  Statistics and sums are fp32; with bf16 inputs the
  * probabilities enter the product with v rounded to bf16.  fp32 inputs and probabilities are multiplied in three bf16
- * parts (24 bits); values from 3.39e38 on count as infinities there.
+ * parts: 24 bits of a value or 2^-126, whichever is more (so values below 2^-102 keep fewer bits); values from 3.39e38 on
+ * count as infinities there.
  */
 size_t kda_attn_prefill_workspace_bytes(int B, int Nq, int Nk, int H, int Hkv, int d, kda_dtype_t dtype);
 kda_status_t kda_attn_prefill(const void *q, const void *k, const void *v, const int *cu_q, const int *cu_k,
@@ -584,8 +585,8 @@ kda_status_t kda_cache_read(const void *k_cache, const void *v_cache, const int 
  * no-op. N m H is at most 2^23, the tokens that all tables hold, N max_pages page / 128 + N, at most 2^30, and N
  * ceil(m H / Hkv / 16) Hkv at most about 2^23.  Scores have to lie inside fp32's range, as above.  A NaN in a row
  * that a later one of the m queries sees reaches the earlier ones too.  Statistics and sums are fp32, every cached
- * value is exact, and a probability enters the product with v as two bf16 parts (16 bits; three, 24 bits, for fp32
- * outputs).
+ * value is exact, fp32 queries are three bf16 parts (24 bits or 2^-126, as above), and a probability enters the product
+ * with v as two (16 bits; three, 24 bits, for fp32 outputs).
  */
 size_t kda_attn_step_workspace_bytes(int N, int m, int H, int Hkv, int d, int max_pages, int page,
                                      kda_dtype_t dtype);
