@@ -152,9 +152,9 @@ __device__ __forceinline__ bool join_groups(KDA_LDS f32x4_t* room, f32x4_t (&O)[
 // the matrix cores.
 //
 // Bound by the issue of products and of the exponentials between them: prompts of 333 to 16384 tokens, 56 heads on 8 of 128,
-// 3.6 ms, 1.15 PFLOP/s (a large library product 1.40).  Products are busy in 56% of the cycles, vector instructions in 32%;
-// scores of the next tile formed beside the exponentials of this one in the same wave were slower (4.9 ms), since
-// their registers leave no room.
+// 3.54 to 3.72 ms by card, 1.12 to 1.17 PFLOP/s (a large library product 1.40).  Products are busy in 56% of the cycles, and
+// vector instructions, these among them, are issued in 47%; scores of the next tile formed beside the exponentials of this one
+// in the same wave were slower (4.9 ms), since their registers leave no room.
 //
 // The running maximum only has to keep exponentials in range.  A tile that every row of the wave sees whole is
 // taken with the maximum at hand, without forming its own; only if a sum of its exponentials passes kSumMax (a
@@ -411,8 +411,8 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : KG) void kda_attn_prefill_k
 // that a long prompt's chain of tiles is half as long; the halves are joined at the end.  A tile takes two phases: the values
 // are split while the scores are formed, the next keys while the values are summed, so that one copy of each (96 KB at
 // d = 128) is enough and splitting runs beside the products.  Of the two waves of a SIMD one splits first, one last.  Prompts of
-// up to 2000 tokens, 16 heads on 4 of 128: 131 us (fp32 products 259), 3.6 us a tile; bound by issue, products 39% and vector
-// instructions 37% of the cycles, and by the longest prompt's tiles one after the other.
+// up to 2000 tokens, 16 heads on 4 of 128: 131 to 134 us (fp32 products 259), 3.6 us a tile; bound by issue (products busy in 39%
+// of the cycles, vector instructions, these among them, issued in 42%) and by the longest prompt's tiles one after the other.
 template <int D, bool SPLIT>
 __global__ __launch_bounds__(512) void kda_attn_prefill_f32_kernel(const AttnArgs a) {
     constexpr int BM = 64, TILE = kKeys * D, NT = D / 16;

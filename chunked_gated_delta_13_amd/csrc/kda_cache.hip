@@ -16,8 +16,6 @@
 
 namespace kda {
 
-typedef __attribute__((ext_vector_type(2))) float f32x2_t;
-
 namespace {
 
 // Bytes of the smallest and largest powers of two, 2^-125 and 2^95: no value is subnormal, and the conversions of
@@ -161,8 +159,9 @@ __global__ __launch_bounds__(256) void kda_cache_rows_kernel(const CacheArgs a) 
     const int lane = threadIdx.x & 63, c = threadIdx.x % LPR, hk = (int)(unit % (uint32_t)a.Hkv);
     const int i0 = (int)(unit / (uint32_t)a.Hkv) * TB, i = i0 + threadIdx.x / LPR;
     const bool there = i < a.N;
-    // Rows are requested before their places are looked up, four loads one after the other (48000 tokens, 8 heads: 59 -> 56 us,
-    // where a plain sum over the same rows takes 63; two or four tokens a thread are no faster).
+    // Rows are requested before their places are looked up, four loads one after the other (write and read of 48000 tokens of 8
+    // heads whose rows lie in the last-level cache: 59 -> 56 us; on other data each time 97 to 99 either way; two or four tokens a
+    // thread are no faster).
     typedef typename Eight<T>::type eight_t;
     eight_t xs = {}, ys = {};
     if constexpr (WRITE) {

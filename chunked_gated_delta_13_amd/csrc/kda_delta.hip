@@ -119,9 +119,10 @@ template <typename T> constexpr int chunk_waves(int nsw) { return nsw == 4 && si
 // K has three buffers (chunks c, n and the one in flight), Q, B and the exponents' tables two or three, T and V one: each is
 // overwritten only in an interval after its last reader's.
 //
-// Bound by issue: 4 prompts of 16384 tokens, 56 heads on 28 of 128 in 1620 us, 13500 cycles a chunk; products take 16.7 cycles,
-// two vector instructions beside each are free and further ones take 4, which makes 10000 cycles for a chunk's.  LDS
-// is busy in 35% of the cycles, HBM moves 1.7 TB/s.
+// Bound by issue: 4 prompts of 16384 tokens, 56 heads on 28 of 128 in 1600 to 1660 us, 13500 cycles a chunk; products take 16.7
+// cycles, two vector instructions beside each are free and further ones take 4, which makes 10000 cycles for a chunk's.
+// Products are busy in 54% of the cycles, vector instructions, these among them, issued in 57%, LDS busy in 35%; HBM moves
+// 1.7 TB/s.
 //
 // OUT: outputs are formed (else only states).
 template <typename T, int DK, int NSW, bool OUT>
@@ -196,8 +197,8 @@ __global__ __launch_bounds__(64 * (NSW + chunk_waves<T>(NSW))) void kda_delta_pr
         // chunks at a time from the end backwards, 8 or 16 of them a wave); then what all of the segment's updates expand, where
         // beta |k|^2 passes 2 or is negative, is added, and if that is too much the whole segment and its transition are
         // formed (20001 tokens, 16 heads 353 -> 363 us; by the decays alone expanding updates lost what they had kept).  A few short
-        // segments are not looked at: forming all transitions, each on a compute unit of its own, takes less than that (3 prompts of
-        // 301 tokens in segments of two chunks 32.8 -> 30.3 us).
+        // segments are not looked at: forming all transitions, each on a compute unit of its own, takes less than that (in fp32 3
+        // prompts of 301 tokens 33.4 -> 30.6 us, 4 of 333 46.3 -> 42.7; in bf16 3 of 602 tokens 35.1 -> 32.8, with d = 128 59.4 -> 53.4).
         constexpr int NW = NSW + NCW;
         KDA_LDS float* sums = &sh->low[0];
         bool dead = false;

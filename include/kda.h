@@ -521,7 +521,8 @@ kda_status_t kda_delta_step(const void *q, const void *k, const void *v, const f
  * Nq H / Hkv at most 2^30, (Nq H / Hkv / 64 + B) Hkv at most 2^23.  Few queries over many keys are run as ranges of
  * keys, joined afterwards, when a workspace of kda_attn_prefill_workspace_bytes(...) bytes is given (calls that
  * overlap in time need one each); with NULL they run as one range.  Scores have to lie inside fp32's range: one below
- * it has no weight, a query with none inside it gets zeros, one with a score above it NaN.  A NaN or an infinity in k
+ * it has no weight, a query with none inside it gets zeros, one with a score above it NaN.  Products with v are summed
+ * before they are divided by the sum of the weights: values above 2^80 may overflow on the way.  A NaN or an infinity in k
  * or v may reach the queries up to 127 before it as well.  Statistics and sums are fp32; with bf16 inputs the
  * probabilities enter the product with v rounded to bf16.  fp32 inputs and probabilities are multiplied in three bf16
  * parts: 24 bits of a value or 2^-126, whichever is more (so values below 2^-102 keep fewer bits); values from 3.39e38 on
@@ -583,7 +584,7 @@ kda_status_t kda_cache_read(const void *k_cache, const void *v_cache, const int 
  *              it is read; calls that overlap in time need one each
  * Rows whose table entry lies outside the pool are not seen; n_pages is at least 1.  N == 0, m == 0 or H == 0 is a
  * no-op. N m H is at most 2^23, the tokens that all tables hold, N max_pages page / 128 + N, at most 2^30, and N
- * ceil(m H / Hkv / 16) Hkv at most about 2^23.  Scores have to lie inside fp32's range, as above.  A NaN in a row
+ * ceil(m H / Hkv / 16) Hkv at most about 2^23.  Scores and sums of products with v have to lie inside fp32's range, as above.  A NaN in a row
  * that a later one of the m queries sees reaches the earlier ones too.  Statistics and sums are fp32, every cached
  * value is exact, fp32 queries are three bf16 parts (24 bits or 2^-126, as above), and a probability enters the product
  * with v as two (16 bits; three, 24 bits, for fp32 outputs).
